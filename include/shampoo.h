@@ -11,6 +11,15 @@
  *   shampoo_precondition     U = X_L G X_R
  *   shampoo_graft_update     theta <- theta - lr (||P||/||U||) U with P Adam's direction
  *
+ * Beside it, for the tensors that are not blocked and for the layers whose
+ * gradients the step consumes:
+ *
+ *   shampoo_grad_norm        norm of many tensors and the coefficient that clips it
+ *   shampoo_adamw            an AdamW step over many tensors, moments in 32 or 8 bits
+ *   shampoo_mx4_quantize     4-bit microscaled (MX4) copies of a matrix, along its rows and columns
+ *   shampoo_mx4_product      C <- alpha A B^T + beta C on MX4 operands
+ *   shampoo_mx4_linear       Y = mx4(X) W^T with an MX4 weight
+ *
  * Sources (cited by page title and section): "DASH: Faster Shampoo via Batched
  * Block Preconditioning and Efficient Inverse-Root Solvers", the howistudyai.com
  * explainer of the paper ([DASH] below; its sections "Building blocks",
@@ -49,7 +58,7 @@
 extern "C" {
 #endif
 
-#define SHAMPOO_ABI_VERSION 2
+#define SHAMPOO_ABI_VERSION 3
 
 /* Return codes. */
 enum {
@@ -312,6 +321,166 @@ int shampoo_graft_update_noalloc(const shampoo_block* g_blocks, const shampoo_bl
                                  const shampoo_block* param_blocks, const shampoo_block* m_blocks,
                                  const shampoo_block* v_blocks, int64_t nblocks, int B, float lr, float beta1,
                                  float beta2, float eps, int step, float* scale_out, hipStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * AdamW over many tensors
+ * ---------------------------------------------------------------------- */
+
+/* Element types of the tensors below. */
+enum {
+  SHAMPOO_T_F32 = 0,
+  SHAMPOO_T_BF16 = 1
+};
+
+/* Storage of AdamW's moments. */
+enum {
+  SHAMPOO_STATE_F32 = 0,
+  SHAMPOO_STATE_MX8 = 1       /* one byte each, a scale byte per 32 elements (shampoo_adamw) */
+};
+
+/* A tensor of n elements, dense in memory, taken in its flat order.  `ptr` is
+ * its device address, aligned to its element size (nothing more is needed);
+ * `offset` the place of its first element in the state buffers, a multiple
+ * of SHAMPOO_GROUP.  The table lives in device memory. */
+typedef struct shampoo_tensor {
+  void* ptr;
+  int64_t n;
+  int64_t offset;
+} shampoo_tensor;
+
+/* A piece of a tensor: its elements [index * SHAMPOO_SEGMENT,
+ * min(n, (index + 1) * SHAMPOO_SEGMENT)).  A segment list names every piece
+ * of every tensor of a table once, in device memory. */
+typedef struct shampoo_segment {
+  int32_t tensor;
+  int32_t index;
+} shampoo_segment;
+
+#define SHAMPOO_GROUP 32       /* elements that share a scale byte */
+#define SHAMPOO_SEGMENT 4096
+
+/*
+ * shampoo_grad_norm -- Euclidean norm of many tensors taken as one vector.
+ *
+ *   tensors, segments  device tables (nsegments pieces; n and ptr are used)
+ *   dtype      SHAMPOO_T_F32 or SHAMPOO_T_BF16, of all tensors
+ *   max_norm   > 0 (may be infinite)
+ *   out        device float[2]: norm, and min(1, max_norm / norm) -- 1 for a norm
+ *              of 0, NaN for a norm that is not finite
+ *   ws         shampoo_grad_norm_workspace_bytes(nsegments) bytes
+ * Squares are summed in double in a fixed order: no fp32 gradient overflows
+ * them, and a call repeated gives the same bits.  nsegments = 0 gives 0 and 1.
+ */
+int shampoo_grad_norm(const shampoo_tensor* tensors, const shampoo_segment* segments, int64_t nsegments,
+                      int dtype, float max_norm, float* out, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments);
+
+/*
+ * shampoo_adamw -- one AdamW step (decoupled weight decay) of many tensors.
+ *
+ *   Per element, in fp32:
+ *     g <- c g                                   (c = *grad_scale, 1 if grad_scale is NULL)
+ *     m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2
+ *     p <- p (1 - eta w) - eta / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   with eta = lr hyper[t][0] and w = hyper[t][1] of the element's tensor t.
+ *
+ *   params, grads, copies   device tables of the same tensors in the same order
+ *              (copies may be NULL: else p is also written there in bf16,
+ *              rounded to nearest even; only with fp32 parameters).  The
+ *              state offsets are those of `params`
+ *   hyper      device float[ntensors][2]: factor on lr, weight decay
+ *   param_dtype, grad_dtype   SHAMPOO_T_F32 or SHAMPOO_T_BF16
+ *   m, v       device state at the tensors' offsets, 16-byte aligned: float, or
+ *              for SHAMPOO_STATE_MX8 codes of one byte with m_scale and v_scale,
+ *              one byte per SHAMPOO_GROUP elements (both NULL for SHAMPOO_STATE_F32)
+ *   step       1-based step count;  0 <= beta1, beta2 < 1;  eps >= 0
+ *   seed       of the stochastic rounding below (unused for fp32 parameters
+ *              with SHAMPOO_STATE_F32)
+ *   grad_scale NULL or a device float: a clipping or unscaling factor.  If it
+ *              is not finite the call changes nothing
+ *
+ * SHAMPOO_STATE_MX8: an m code is a sign and an OCP E4M3 value (bias 7), a v
+ * code an unsigned E5M3 value (bias 15, every code finite); the value is the
+ * code's times 2^(s - 127), s the group's scale byte, and NaN for s = 255.
+ * With E the exponent field of the group's largest magnitude, s = max(E - 7, 1)
+ * for m and max(E - 15, 1) for v (255 if E = 255: one entry that is not finite
+ * makes its group NaN).  Codes round stochastically: where x lies the fraction
+ * f of the way between two neighbours, the upper is taken if
+ * f + (h + 1/2) / 65536 >= 1, so that small changes of a moment are kept on
+ * average; h is the low (m) or high (v) half of the element's 32-bit hash, a
+ * function of seed, step and its place in the state buffer.  A v code is at
+ * least 1: a moment that rounds to 0 cannot leave eps alone under m.
+ * bf16 parameters round stochastically by the same rule (16 other bits of the
+ * hash), fp32 parameters to nearest even.
+ */
+int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, const shampoo_tensor* copies,
+                  const float* hyper, int64_t ntensors, const shampoo_segment* segments, int64_t nsegments,
+                  int param_dtype, int grad_dtype, int state, void* m, void* v, uint8_t* m_scale,
+                  uint8_t* v_scale, double lr, double beta1, double beta2, double eps, int step, uint64_t seed,
+                  const float* grad_scale, hipStream_t stream);
+
+/* Values of n 8-bit moments (n a multiple of SHAMPOO_GROUP) as fp32 or bf16;
+ * bf16 holds every value exactly.  Either of m and v may be NULL with its
+ * scale and output. */
+int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
+                          int64_t n, void* m_out, void* v_out, int dtype, hipStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * MX4: 4-bit microscaled matrices
+ * ---------------------------------------------------------------------- */
+
+/* An MX4 matrix of R rows and C columns is a pair of byte arrays,
+ *   codes  [R][Cp / 2]   two E2M1 values a byte, the lower column in the low half
+ *   scales [R][Cp / 32]  one E8M0 byte s for 32 consecutive columns: 2^(s - 127)
+ * with Cp = C rounded up to a multiple of 128; the columns from C to Cp hold
+ * code 0.  Both arrays are 16-byte aligned.  (OCP microscaling MXFP4.) */
+#define SHAMPOO_MX4_PAD 128
+
+/*
+ * shampoo_mx4_quantize -- MX4 copies of x and / or of its transpose.
+ *
+ *   x          device matrix [rows][cols] of dtype, row stride ld >= cols
+ *   codes, scales      MX4 matrix [rows][cols], or both NULL
+ *   codes_t, scales_t  MX4 matrix [cols][rows] of x^T (32 consecutive rows of x
+ *              share a scale), or both NULL
+ * s = max(E - 2, 0) with E the exponent field of the group's largest
+ * magnitude as fp32; values round to nearest even and saturate at 6 * 2^(s-127).
+ * A group with an entry that is not finite gets codes 0 and s = 255 (NaN).
+ */
+int shampoo_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                         uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, hipStream_t stream);
+
+/* Values of an MX4 matrix, as fp32 or bf16 (which holds every value that
+ * shampoo_mx4_quantize writes exactly), row stride ld >= cols. */
+int shampoo_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                           int dtype, int64_t ld, hipStream_t stream);
+
+/*
+ * shampoo_mx4_product -- C <- alpha A B^T + beta C, fp32 accumulation.
+ *
+ *   A [M][K] and B [N][K]   MX4 matrices
+ *   C          device matrix [M][N] of dtype, row stride ldc >= N, apart from A
+ *              and B.  beta = 0: C is only written
+ *   ws         shampoo_mx4_workspace_bytes(M, N, K) bytes (NULL if that is 0)
+ */
+int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                        const uint8_t* b_scales, int64_t M, int64_t N, int64_t K, float alpha, float beta, void* c,
+                        int dtype, int64_t ldc, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * shampoo_mx4_linear -- Y = mx4(X) W^T: X [M][K] is quantised along its rows
+ * and multiplied by the MX4 weight W [N][K].
+ *
+ *   X          of dtype, row stride ldx;  Y [M][N] of dtype, row stride ldy
+ *   ws         shampoo_mx4_linear_workspace_bytes(M, N, K) bytes
+ */
+int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const uint8_t* w_scales, int64_t M,
+                       int64_t N, int64_t K, void* y, int64_t ldy, int dtype, void* ws, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* Workspace sizes of the two calls above (0 for invalid sizes too). */
+size_t shampoo_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Workspace size in bytes for an operation (op = SHAMPOO_OP_*).  `count` is
  * nfactors for SCALE/NEWTON/CHEBY and nblocks for ACCUMULATE/PRECONDITION;

@@ -1,0 +1,227 @@
+"""AdamW over many tensors at once, with its moments in 32 or in 8 bits, and
+the norm that clips their gradients: the step for the tensors that the block
+preconditioner leaves (norm vectors, biases, embeddings), or for all of them.
+All the arithmetic runs in the HIP library (see capi and include/shampoo.h).
+
+    grads = TensorTable([p.grad for p in params])
+    opt = AdamW(params, lr=1e-3, weight_decay=0.1, state="mx8")
+    norm = grad_norm(grads, 1.0)               # [norm, clipping factor], on the device
+    opt.step(grads, grad_scale=norm[1:])
+"""
+from __future__ import annotations
+
+import contextlib
+
+import numpy as np
+import torch
+
+from . import capi
+
+_TYPES = {torch.float32: capi.T_F32, torch.bfloat16: capi.T_BF16}
+_STATES = {"f32": capi.STATE_F32, "mx8": capi.STATE_MX8}
+
+
+def _on(stream):
+    """Context in which allocations belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _dense(t):
+    """Whether t fills one stretch of memory without gaps or overlap."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _layout(t):
+    """What two tensors must share for their flat orders to name the same elements."""
+    return t.numel() if t.is_contiguous() else (tuple(t.shape), t.stride())
+
+
+class TensorTable:
+    """Device table of tensors in their flat memory order (the tensors are kept
+    alive with it).  All of one type, float32 or bfloat16, and dense.  A table
+    is built again when its tensors move (gradients that are freed between
+    steps); tensors whose memory stays need it once."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        dtypes = {t.dtype for t in tensors}
+        if len(dtypes) > 1:
+            raise ValueError("the tensors of a table have one type")
+        dtype = dtypes.pop() if dtypes else torch.float32
+        if dtype not in _TYPES:
+            raise ValueError(f"tensors must be float32 or bfloat16, not {dtype}")
+        for i, t in enumerate(tensors):
+            if not t.is_cuda:
+                raise ValueError(f"tensor {i} is not a CUDA tensor")
+            if t.device != tensors[0].device:
+                raise ValueError("the tensors of a table are on one device")
+            if not _dense(t):
+                raise ValueError(f"tensor {i} is not dense")
+        self.dtype = dtype
+        self.type = _TYPES[dtype]
+        self.device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+        self.layouts = [_layout(t) for t in tensors]
+        self._keep = tensors
+        sizes = np.array([t.numel() for t in tensors], dtype=np.int64)
+        padded = (sizes + capi.GROUP - 1) // capi.GROUP * capi.GROUP
+        self.offsets = np.concatenate([np.zeros(1, np.int64), np.cumsum(padded)]).astype(np.int64)
+        self.total = int(self.offsets[-1])   # elements of a state buffer
+        self.sizes = sizes
+        self.n = len(tensors)
+        rows = np.zeros((max(self.n, 1), 3), dtype=np.int64)
+        for i, t in enumerate(tensors):
+            rows[i] = t.data_ptr(), sizes[i], self.offsets[i]
+        pieces = (sizes + capi.SEGMENT - 1) // capi.SEGMENT
+        if self.n and int(pieces.max()) > 0x7FFFFFFF:
+            raise ValueError("a tensor is too large for the segment list")
+        self.nsegments = int(pieces.sum())
+        seg = np.zeros((max(self.nsegments, 1), 2), dtype=np.int32)
+        seg[:self.nsegments, 0] = np.repeat(np.arange(self.n), pieces)
+        seg[:self.nsegments, 1] = np.arange(self.nsegments) - np.repeat(np.cumsum(pieces) - pieces, pieces)
+        self.tensor = torch.from_numpy(rows).to(self.device)
+        self.segments = torch.from_numpy(seg).to(self.device)
+        self.ptr = self.tensor.data_ptr()
+        self.segments_ptr = self.segments.data_ptr()
+        self._norm_ws = capi.shampoo_grad_norm_workspace_bytes(self.nsegments)
+
+
+def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
+    """float32 [2] on the device: the Euclidean norm of all the table's tensors
+    as one vector, and min(1, max_norm / norm) (NaN if the norm is not finite,
+    which makes AdamW.step change nothing)."""
+    with _on(stream):
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=table.device)
+        elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2):
+            raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements")
+        ws = torch.empty(table._norm_ws, dtype=torch.uint8, device=table.device)
+        handle = torch.cuda.current_stream(table.device).cuda_stream
+        capi.check(capi.shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
+                                          out.data_ptr(), ws.data_ptr(), table._norm_ws, handle),
+                   "shampoo_grad_norm")
+    return out
+
+
+def _per_tensor(value, n, name):
+    values = [float(v) for v in value] if isinstance(value, (list, tuple)) else [float(value)] * n
+    if len(values) != n:
+        raise ValueError(f"{name} has {len(values)} values for {n} tensors")
+    return values
+
+
+class AdamW:
+    """AdamW (decoupled weight decay) over a list of tensors, updated in place.
+
+    params        float32 or bfloat16 tensors of one type, or a TensorTable.
+                  bfloat16 parameters are rounded stochastically, so that steps
+                  below their spacing are kept on average
+    weight_decay  a number, or one for each tensor
+    lr_scale      factor on the learning rate, a number or one for each tensor
+    state         "f32", or "mx8": two bytes of moments an element
+    copies        bfloat16 tensors that receive the float32 parameters, rounded
+    seed          of the stochastic rounding: equal seeds give equal bits
+
+    The moments live in flat buffers, every tensor starting at a multiple of
+    32 elements (`offsets`).  `t` counts the steps taken."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, lr_scale=1.0, state="f32",
+                 copies=None, seed=0):
+        self.params = params if isinstance(params, TensorTable) else TensorTable(params)
+        if state not in _STATES:
+            raise ValueError(f"state must be one of {sorted(_STATES)}")
+        b1, b2 = betas
+        if not (0.0 <= b1 < 1.0 and 0.0 <= b2 < 1.0 and eps >= 0.0):
+            raise ValueError("need 0 <= betas < 1 and eps >= 0")
+        self.lr, self.betas, self.eps, self.seed, self.t = lr, (float(b1), float(b2)), eps, int(seed), 0
+        if not 0 <= self.seed < 1 << 64:
+            raise ValueError("seed must fit 64 bits")
+        self.state = state
+        p, dev = self.params, self.params.device
+        self.offsets = p.offsets
+        self.copies = None
+        if copies is not None:
+            self.copies = copies if isinstance(copies, TensorTable) else TensorTable(copies)
+            if p.dtype != torch.float32 or self.copies.dtype != torch.bfloat16:
+                raise ValueError("copies are bfloat16 copies of float32 parameters")
+            self._same(self.copies, "copies")
+        hyper = np.array([_per_tensor(lr_scale, p.n, "lr_scale"), _per_tensor(weight_decay, p.n, "weight_decay")],
+                         dtype=np.float32).T
+        self.hyper = torch.from_numpy(np.ascontiguousarray(hyper)).to(dev)
+        low = state == "mx8"
+        dtype = torch.uint8 if low else torch.float32
+        self.m = torch.zeros(p.total, dtype=dtype, device=dev)
+        self.v = torch.zeros(p.total, dtype=dtype, device=dev)
+        self.m_scale = torch.zeros(p.total // capi.GROUP, dtype=torch.uint8, device=dev) if low else None
+        self.v_scale = torch.zeros(p.total // capi.GROUP, dtype=torch.uint8, device=dev) if low else None
+
+    def _same(self, table, name):
+        if table.layouts != self.params.layouts:
+            raise ValueError(f"{name} differ from the parameters in number, size or layout")
+        if table.device != self.params.device:
+            raise ValueError(f"{name} are on another device than the parameters")
+
+    def step(self, grads, lr=None, grad_scale=None, stream=None):
+        """One step with the gradients of a TensorTable (or a list of tensors).
+        grad_scale: float32 tensor of one element on the device that multiplies
+        the gradients; if it is not finite, nothing changes but `t`."""
+        if not isinstance(grads, TensorTable):
+            grads = TensorTable(grads)
+        p = self.params
+        self._same(grads, "gradients")
+        scale_ptr = 0
+        if grad_scale is not None:
+            if not (grad_scale.is_cuda and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1):
+                raise ValueError("grad_scale must be a float32 CUDA tensor of one element")
+            scale_ptr = grad_scale.data_ptr()
+        low = self.m_scale is not None
+        handle = (stream or torch.cuda.current_stream(p.device)).cuda_stream
+        capi.check(capi.shampoo_adamw(
+            p.ptr, grads.ptr, self.copies.ptr if self.copies is not None else 0, self.hyper.data_ptr(), p.n,
+            p.segments_ptr, p.nsegments, p.type, grads.type, _STATES[self.state], self.m.data_ptr(), self.v.data_ptr(),
+            self.m_scale.data_ptr() if low else 0, self.v_scale.data_ptr() if low else 0,
+            self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.t + 1, self.seed, scale_ptr,
+            handle), "shampoo_adamw")
+        self.t += 1
+
+    def moments(self, dtype=torch.float32, stream=None):
+        """The values of (m, v) as flat tensors in the state's layout."""
+        if dtype not in _TYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        if self.m_scale is None:
+            with _on(stream):
+                return self.m.to(dtype), self.v.to(dtype)
+        with _on(stream):
+            m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
+            capi.check(capi.shampoo_adamw_moments(
+                self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), m.numel(),
+                m.data_ptr(), v.data_ptr(), _TYPES[dtype], torch.cuda.current_stream(m.device).cuda_stream),
+                "shampoo_adamw_moments")
+        return m, v
+
+    def state_dict(self):
+        """What a resume needs bit for bit: the moments as stored, the step count
+        and the seed.  Tensors are returned as they are."""
+        sd = {"m": self.m, "v": self.v, "t": int(self.t), "seed": int(self.seed)}
+        if self.m_scale is not None:
+            sd.update(m_scale=self.m_scale, v_scale=self.v_scale)
+        return sd
+
+    def load_state_dict(self, sd):
+        """Restore a state_dict() of an AdamW over tensors of the same sizes and the same kind of state."""
+        names = [k for k in ("m", "v", "m_scale", "v_scale") if getattr(self, k) is not None]
+        if {k for k in sd if k not in ("t", "seed")} != set(names):
+            raise ValueError("the saved moments are of another kind")
+        for name in names:
+            dst, src = getattr(self, name), sd[name]
+            if tuple(src.shape) != tuple(dst.shape) or src.dtype != dst.dtype:
+                raise ValueError(f"{name}: saved {tuple(src.shape)} {src.dtype}, expected "
+                                 f"{tuple(dst.shape)} {dst.dtype}")
+            dst.copy_(src)
+        self.t, self.seed = int(sd["t"]), int(sd["seed"])

@@ -11,6 +11,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,8 +20,8 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libshampoo_mi355x.so")
 ARCH = os.environ.get("SHAMPOO_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["shampoo.hip"]
-HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h"]
+SOURCES = ["shampoo.hip", "adamw.hip", "mx4.hip"]
+HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h", "kernels_adamw.h", "kernels_mx4.h"]
 
 
 def hipcc():
@@ -28,18 +29,18 @@ def hipcc():
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def command(out=LIB):
-    return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+def compile_command(source, out):
+    return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-c",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-I", os.path.join(ROOT, "include"),
-            "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
+            "-o", out, os.path.join(CSRC, source)]
 
 
-def build(verbose=False):
-    """Compile the library (always recompiles).  Raises on failure."""
-    os.makedirs(LIBDIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
+def link_command(objects, out):
+    return [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", "-o", out] + objects
+
+
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -49,6 +50,18 @@ def build(verbose=False):
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
+
+
+def build(verbose=False):
+    """Compile the library (always recompiles, its sources side by side).  Raises on failure."""
+    os.makedirs(LIBDIR, exist_ok=True)
+    objects = [os.path.join(LIBDIR, s + ".o") for s in SOURCES]
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
+        list(ex.map(lambda job: _run(compile_command(*job), verbose), zip(SOURCES, objects)))
+    tmp = LIB + ".tmp"
+    _run(link_command(objects, tmp), verbose)
+    for o in objects:
+        os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libshampoo_mi355x.so")
 
@@ -49,8 +49,16 @@ OP_NEWTON = 3
 OP_CHEBY = 4
 OP_PRECONDITION = 5
 OP_GRAFT = 6
+# Element types and moment storage of the AdamW step and the MX4 calls
+T_F32 = 0
+T_BF16 = 1
+STATE_F32 = 0
+STATE_MX8 = 1
+GROUP = 32                # elements that share a scale byte
+SEGMENT = 4096
+MX4_PAD = 128             # columns of an MX4 matrix are padded to a multiple of this
 
-ABI_VERSION = 2
+ABI_VERSION = 3
 
 
 class shampoo_block(ctypes.Structure):
@@ -59,6 +67,14 @@ class shampoo_block(ctypes.Structure):
 
 class shampoo_scale(ctypes.Structure):
     _fields_ = [("c", c_float), ("eps", c_float), ("lambda_", c_float), ("trace", c_float)]
+
+
+class shampoo_tensor(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("n", c_int64), ("offset", c_int64)]
+
+
+class shampoo_segment(ctypes.Structure):
+    _fields_ = [("tensor", c_int32), ("index", c_int32)]
 
 
 class ShampooError(RuntimeError):
@@ -96,6 +112,23 @@ _SIGNATURES = {
                                      c_void_p, c_size_t, c_void_p]),
     "shampoo_graft_update_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int,
                                              c_float, c_float, c_float, c_float, c_int, c_void_p, c_void_p]),
+    "shampoo_grad_norm": (c_int, [c_void_p, c_void_p, c_int64, c_int, c_float, c_void_p, c_void_p, c_size_t,
+                                  c_void_p]),
+    "shampoo_grad_norm_workspace_bytes": (c_size_t, [c_int64]),
+    "shampoo_adamw": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int,
+                              c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_double, c_double, c_double, c_double,
+                              c_int, c_uint64, c_void_p, c_void_p]),
+    "shampoo_adamw_moments": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int,
+                                      c_void_p]),
+    "shampoo_mx4_quantize": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p]),
+    "shampoo_mx4_dequantize": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int, c_int64, c_void_p]),
+    "shampoo_mx4_product": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_float,
+                                    c_float, c_void_p, c_int, c_int64, c_void_p, c_size_t, c_void_p]),
+    "shampoo_mx4_linear": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_void_p,
+                                   c_int64, c_int, c_void_p, c_size_t, c_void_p]),
+    "shampoo_mx4_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "shampoo_mx4_linear_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -195,3 +228,47 @@ def shampoo_graft_update_noalloc(g_blocks, u_blocks, param_blocks, m_blocks, v_b
                                  beta2, eps, step, scale_out, stream):
     return load().shampoo_graft_update_noalloc(g_blocks, u_blocks, param_blocks, m_blocks, v_blocks, nblocks, B,
                                                lr, beta1, beta2, eps, step, scale_out, stream)
+
+
+def shampoo_grad_norm(tensors, segments, nsegments, dtype, max_norm, out, ws, ws_bytes, stream):
+    return load().shampoo_grad_norm(tensors, segments, nsegments, dtype, max_norm, out, ws, ws_bytes, stream)
+
+
+def shampoo_grad_norm_workspace_bytes(nsegments):
+    return load().shampoo_grad_norm_workspace_bytes(nsegments)
+
+
+def shampoo_adamw(params, grads, copies, hyper, ntensors, segments, nsegments, param_dtype, grad_dtype, state, m, v,
+                  m_scale, v_scale, lr, beta1, beta2, eps, step, seed, grad_scale, stream):
+    return load().shampoo_adamw(params, grads, copies, hyper, ntensors, segments, nsegments, param_dtype, grad_dtype,
+                                state, m, v, m_scale, v_scale, lr, beta1, beta2, eps, step, seed, grad_scale, stream)
+
+
+def shampoo_adamw_moments(m, m_scale, v, v_scale, n, m_out, v_out, dtype, stream):
+    return load().shampoo_adamw_moments(m, m_scale, v, v_scale, n, m_out, v_out, dtype, stream)
+
+
+def shampoo_mx4_quantize(x, dtype, rows, cols, ld, codes, scales, codes_t, scales_t, stream):
+    return load().shampoo_mx4_quantize(x, dtype, rows, cols, ld, codes, scales, codes_t, scales_t, stream)
+
+
+def shampoo_mx4_dequantize(codes, scales, rows, cols, out, dtype, ld, stream):
+    return load().shampoo_mx4_dequantize(codes, scales, rows, cols, out, dtype, ld, stream)
+
+
+def shampoo_mx4_product(a_codes, a_scales, b_codes, b_scales, M, N, K, alpha, beta, c, dtype, ldc, ws, ws_bytes,
+                        stream):
+    return load().shampoo_mx4_product(a_codes, a_scales, b_codes, b_scales, M, N, K, alpha, beta, c, dtype, ldc, ws,
+                                      ws_bytes, stream)
+
+
+def shampoo_mx4_linear(x, ldx, w_codes, w_scales, M, N, K, y, ldy, dtype, ws, ws_bytes, stream):
+    return load().shampoo_mx4_linear(x, ldx, w_codes, w_scales, M, N, K, y, ldy, dtype, ws, ws_bytes, stream)
+
+
+def shampoo_mx4_workspace_bytes(M, N, K):
+    return load().shampoo_mx4_workspace_bytes(M, N, K)
+
+
+def shampoo_mx4_linear_workspace_bytes(M, N, K):
+    return load().shampoo_mx4_linear_workspace_bytes(M, N, K)

@@ -1,0 +1,124 @@
+// C entry points of the AdamW step and the gradient norm (gfx950): arguments
+// are checked on the host, kernels enqueued on the caller's stream; nothing
+// is allocated and nothing synchronises.
+#include <cmath>
+
+#include "kernels_adamw.h"
+
+using namespace shp;
+
+namespace {
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int kNormBlocks = 2048;
+
+int check_launch() { return hipGetLastError() == hipSuccess ? SHAMPOO_OK : SHAMPOO_EHIP; }
+
+bool valid_type(int t) { return t == SHAMPOO_T_F32 || t == SHAMPOO_T_BF16; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int norm_blocks(int64_t nseg) { return (int)(nseg < kNormBlocks ? nseg : kNormBlocks); }
+
+// The part of the hash's counter that a whole step shares.
+uint32_t step_key(uint64_t seed, int step) {
+  const uint32_t s = hash_finish((uint32_t)seed * kHashC1 + (uint32_t)(seed >> 32) * kHashC4);
+  return hash_finish(s + (uint32_t)step * kHashC1);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments) {
+  if (nsegments <= 0) return 0;
+  return (size_t)norm_blocks(nsegments) * sizeof(double);
+}
+
+int shampoo_grad_norm(const shampoo_tensor* tensors, const shampoo_segment* segments, int64_t nsegments, int dtype,
+                      float max_norm, float* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (nsegments < 0 || !(max_norm > 0.f) || out == nullptr) return SHAMPOO_EINVAL;
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  if (nsegments > 0) {
+    if (tensors == nullptr || segments == nullptr) return SHAMPOO_EINVAL;
+    if (ws == nullptr || ws_bytes < shampoo_grad_norm_workspace_bytes(nsegments)) return SHAMPOO_EWORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 7) != 0) return SHAMPOO_EINVAL;
+  }
+  const int blocks = norm_blocks(nsegments);
+  double* partial = static_cast<double*>(ws);
+  if (blocks > 0) {
+    hipLaunchKernelGGL(grad_norm_partial_kernel, dim3(blocks), dim3(256), 0, stream, tensors, segments, nsegments,
+                       dtype == SHAMPOO_T_BF16, partial);
+    if (check_launch() != SHAMPOO_OK) return SHAMPOO_EHIP;
+  }
+  hipLaunchKernelGGL(grad_norm_final_kernel, dim3(1), dim3(256), 0, stream, partial, blocks, max_norm, out);
+  return check_launch();
+}
+
+int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, const shampoo_tensor* copies,
+                  const float* hyper, int64_t ntensors, const shampoo_segment* segments, int64_t nsegments,
+                  int param_dtype, int grad_dtype, int state, void* m, void* v, uint8_t* m_scale, uint8_t* v_scale,
+                  double lr, double beta1, double beta2, double eps, int step, uint64_t seed,
+                  const float* grad_scale, hipStream_t stream) {
+  if (ntensors < 0 || nsegments < 0 || step < 1 || !std::isfinite(lr)) return SHAMPOO_EINVAL;
+  if (!(beta1 >= 0. && beta1 < 1.) || !(beta2 >= 0. && beta2 < 1.) || !(eps >= 0.) || std::isinf(eps))
+    return SHAMPOO_EINVAL;
+  if (!valid_type(param_dtype) || !valid_type(grad_dtype)) return SHAMPOO_EUNSUPPORTED;
+  if (state != SHAMPOO_STATE_F32 && state != SHAMPOO_STATE_MX8) return SHAMPOO_EUNSUPPORTED;
+  if (copies != nullptr && param_dtype != SHAMPOO_T_F32) return SHAMPOO_EUNSUPPORTED;
+  if (ntensors == 0 || nsegments == 0) return SHAMPOO_OK;
+  if (params == nullptr || grads == nullptr || hyper == nullptr || segments == nullptr || m == nullptr ||
+      v == nullptr)
+    return SHAMPOO_EINVAL;
+  const bool mx8 = state == SHAMPOO_STATE_MX8;
+  if (mx8 != (m_scale != nullptr) || mx8 != (v_scale != nullptr)) return SHAMPOO_EINVAL;
+  if (!aligned16(m) || !aligned16(v)) return SHAMPOO_EINVAL;
+  if (nsegments > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  AdamwArgs a;
+  a.params = params;
+  a.grads = grads;
+  a.copies = copies;
+  a.hyper = hyper;
+  a.segments = segments;
+  a.ntensors = ntensors;
+  a.m = m;
+  a.v = v;
+  a.m_scale = m_scale;
+  a.v_scale = v_scale;
+  a.grad_scale = grad_scale;
+  a.lr = (float)lr;
+  a.beta1 = (float)beta1;
+  a.omb1 = 1.0 - beta1;
+  a.beta2 = (float)beta2;
+  a.omb2 = 1.0 - beta2;
+  a.eps = (float)eps;
+  a.rbc1 = (float)(1.0 / (1.0 - std::pow(beta1, step)));
+  a.rsbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, step)));
+  a.key = step_key(seed, step);
+  a.param_bf16 = param_dtype == SHAMPOO_T_BF16;
+  a.grad_bf16 = grad_dtype == SHAMPOO_T_BF16;
+  a.mx8 = mx8;
+  hipLaunchKernelGGL(adamw_kernel, dim3((uint32_t)nsegments), dim3(256), 0, stream, a);
+  return check_launch();
+}
+
+int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
+                          int64_t n, void* m_out, void* v_out, int dtype, hipStream_t stream) {
+  if (n < 0 || n % kGroup != 0) return SHAMPOO_EINVAL;
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  if ((m == nullptr) != (m_scale == nullptr) || (m == nullptr) != (m_out == nullptr)) return SHAMPOO_EINVAL;
+  if ((v == nullptr) != (v_scale == nullptr) || (v == nullptr) != (v_out == nullptr)) return SHAMPOO_EINVAL;
+  if (n == 0) return SHAMPOO_OK;
+  const int64_t blocks = (n + 255) / 256;
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  const int bf16 = dtype == SHAMPOO_T_BF16;
+  if (m != nullptr)
+    hipLaunchKernelGGL(mx8_decode_kernel<MomentM>, dim3((uint32_t)blocks), dim3(256), 0, stream, m, m_scale, n, m_out,
+                       bf16);
+  if (v != nullptr)
+    hipLaunchKernelGGL(mx8_decode_kernel<MomentV>, dim3((uint32_t)blocks), dim3(256), 0, stream, v, v_scale, n, v_out,
+                       bf16);
+  return check_launch();
+}
+
+}  // extern "C"

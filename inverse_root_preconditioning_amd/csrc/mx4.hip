@@ -1,0 +1,154 @@
+// C entry points of the MX4 quantisation and products (gfx950): arguments are
+// checked on the host, kernels enqueued on the caller's stream; nothing is
+// allocated and nothing synchronises.
+#include <cmath>
+
+#include "kernels_mx4.h"
+
+using namespace shp;
+
+namespace {
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxSide = (int64_t)1 << 31;  // rows and columns of a matrix
+
+int check_launch() { return hipGetLastError() == hipSuccess ? SHAMPOO_OK : SHAMPOO_EHIP; }
+
+bool valid_type(int t) { return t == SHAMPOO_T_F32 || t == SHAMPOO_T_BF16; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_sides(int64_t a, int64_t b, int64_t c) {
+  if (a < 0 || b < 0 || c < 0) return SHAMPOO_EINVAL;
+  if (a > kMaxSide || b > kMaxSide || c > kMaxSide) return SHAMPOO_EUNSUPPORTED;
+  return SHAMPOO_OK;
+}
+
+bool valid_mx4(const uint8_t* codes, const uint8_t* scales) {
+  return codes != nullptr && scales != nullptr && aligned16(codes) && aligned16(scales);
+}
+
+int quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_step, int64_t col_step,
+             uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  Mx4QuantArgs a;
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.row_step = row_step;
+  a.col_step = col_step;
+  a.padded = mx4_padded(cols);
+  a.codes = codes;
+  a.scales = scales;
+  a.bf16 = dtype == SHAMPOO_T_BF16;
+  const int64_t blocks = (rows * (a.padded / kMx4Group) + 7) / 8;
+  if (blocks == 0) return SHAMPOO_OK;
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  hipLaunchKernelGGL(mx4_quantize_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, a);
+  return check_launch();
+}
+
+int product(const Mx4ProductArgs& a, hipStream_t stream) {
+  const int64_t tiles = ((a.M + 15) / 16) * ((a.N + 15) / 16), blocks = (tiles + 3) / 4;
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  hipLaunchKernelGGL(mx4_product_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, a);
+  return check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+int shampoo_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                         uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, hipStream_t stream) {
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  const int rc = check_sides(rows, cols, 0);
+  if (rc != SHAMPOO_OK) return rc;
+  if (ld < cols) return SHAMPOO_EINVAL;
+  if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+    return SHAMPOO_EINVAL;
+  if (rows == 0 || cols == 0) return SHAMPOO_OK;
+  if (x == nullptr || (codes == nullptr && codes_t == nullptr)) return SHAMPOO_EINVAL;
+  if ((codes != nullptr && !valid_mx4(codes, scales)) || (codes_t != nullptr && !valid_mx4(codes_t, scales_t)))
+    return SHAMPOO_EINVAL;
+  int done = SHAMPOO_OK;
+  if (codes != nullptr) done = quantize(x, dtype, rows, cols, ld, 1, codes, scales, stream);
+  if (done == SHAMPOO_OK && codes_t != nullptr) done = quantize(x, dtype, cols, rows, 1, ld, codes_t, scales_t, stream);
+  return done;
+}
+
+int shampoo_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                           int dtype, int64_t ld, hipStream_t stream) {
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  const int rc = check_sides(rows, cols, 0);
+  if (rc != SHAMPOO_OK) return rc;
+  if (ld < cols) return SHAMPOO_EINVAL;
+  if (rows == 0 || cols == 0) return SHAMPOO_OK;
+  if (!valid_mx4(codes, scales) || out == nullptr) return SHAMPOO_EINVAL;
+  const int64_t padded = mx4_padded(cols), blocks = (rows * (padded / 2) + 255) / 256;
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  hipLaunchKernelGGL(mx4_dequantize_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, codes, scales, rows, cols,
+                     padded, out, dtype == SHAMPOO_T_BF16, ld);
+  return check_launch();
+}
+
+size_t shampoo_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
+
+int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                        const uint8_t* b_scales, int64_t M, int64_t N, int64_t K, float alpha, float beta, void* c,
+                        int dtype, int64_t ldc, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  const int rc = check_sides(M, N, K);
+  if (rc != SHAMPOO_OK) return rc;
+  if (ldc < N || !std::isfinite(alpha) || !std::isfinite(beta)) return SHAMPOO_EINVAL;
+  if (M == 0 || N == 0) return SHAMPOO_OK;
+  if (c == nullptr || (K > 0 && (!valid_mx4(a_codes, a_scales) || !valid_mx4(b_codes, b_scales))))
+    return SHAMPOO_EINVAL;
+  const size_t need = shampoo_mx4_workspace_bytes(M, N, K);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
+  Mx4ProductArgs a;
+  a.a = a_codes;
+  a.as = a_scales;
+  a.b = b_codes;
+  a.bs = b_scales;
+  a.M = M;
+  a.N = N;
+  a.padded = mx4_padded(K);
+  a.c = c;
+  a.ldc = ldc;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.bf16 = dtype == SHAMPOO_T_BF16;
+  return product(a, stream);
+}
+
+size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_sides(M, N, K) != SHAMPOO_OK) return 0;
+  const size_t elems = (size_t)M * (size_t)mx4_padded(K);
+  return align_up(elems / 2) + align_up(elems / kMx4Group) + shampoo_mx4_workspace_bytes(M, N, K);
+}
+
+int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const uint8_t* w_scales, int64_t M,
+                       int64_t N, int64_t K, void* y, int64_t ldy, int dtype, void* ws, size_t ws_bytes,
+                       hipStream_t stream) {
+  if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
+  int rc = check_sides(M, N, K);
+  if (rc != SHAMPOO_OK) return rc;
+  if (ldx < K || ldy < N) return SHAMPOO_EINVAL;
+  if (M == 0 || N == 0) return SHAMPOO_OK;
+  if (y == nullptr || (K > 0 && (x == nullptr || !valid_mx4(w_codes, w_scales)))) return SHAMPOO_EINVAL;
+  const size_t need = shampoo_mx4_linear_workspace_bytes(M, N, K);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
+  if (!aligned16(ws)) return SHAMPOO_EINVAL;
+  const size_t elems = (size_t)M * (size_t)mx4_padded(K);
+  uint8_t* codes = static_cast<uint8_t*>(ws);
+  uint8_t* scales = codes + align_up(elems / 2);
+  uint8_t* rest = scales + align_up(elems / kMx4Group);
+  if (K > 0) rc = shampoo_mx4_quantize(x, dtype, M, K, ldx, codes, scales, nullptr, nullptr, stream);
+  if (rc != SHAMPOO_OK) return rc;
+  return shampoo_mx4_product(codes, scales, w_codes, w_scales, M, N, K, 1.f, 0.f, y, dtype, ldy, rest,
+                             ws_bytes - (size_t)(rest - codes), stream);
+}
+
+}  // extern "C"
