@@ -44,6 +44,19 @@ __device__ __forceinline__ void stg(T* p, const T& v) {
   *(__attribute__((address_space(1))) T*)p = v;
 }
 
+// The same for a vector at an address aligned to ALIGN bytes only (global
+// memory takes vector accesses at any element's address).
+template <class V, int ALIGN>
+__device__ __forceinline__ V ldg_any(const void* p) {
+  typedef V U __attribute__((aligned(ALIGN)));
+  return *(const __attribute__((address_space(1))) U*)p;
+}
+template <class V, int ALIGN>
+__device__ __forceinline__ void stg_any(void* p, const V& v) {
+  typedef V U __attribute__((aligned(ALIGN)));
+  *(__attribute__((address_space(1))) U*)p = v;
+}
+
 // f(std::integral_constant<int, i>) for i = 0..N-1, expanded at compile time
 // (indices stay constants even where a loop would be too large to unroll).
 template <class F, int... I>

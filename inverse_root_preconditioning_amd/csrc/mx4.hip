@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr int64_t kMaxSide = (int64_t)1 << 31;  // rows and columns of a matrix
+constexpr int64_t kMaxK = (int64_t)1 << 24;     // columns a product sums over (32-bit offsets within a tile)
 
 int check_launch() { return hipGetLastError() == hipSuccess ? SHAMPOO_OK : SHAMPOO_EHIP; }
 
@@ -49,11 +50,33 @@ int quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_s
   return check_launch();
 }
 
-int product(const Mx4ProductArgs& a, hipStream_t stream) {
-  const int64_t tiles = ((a.M + 15) / 16) * ((a.N + 15) / 16), blocks = (tiles + 3) / 4;
-  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
-  hipLaunchKernelGGL(mx4_product_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, a);
+template <int T>
+int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
+  const int64_t tm = (a.M + 64 * T - 1) / (64 * T), tn = (a.N + 64 * T - 1) / (64 * T);
+  if (tm * tn > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  a.tiles_m = (uint32_t)tm;
+  a.tiles_n = (uint32_t)tn;
+  const dim3 grid((uint32_t)(tm * tn)), block(256);
+  const bool beta = a.beta != 0.f;
+  if (a.bf16 && beta) {
+    hipLaunchKernelGGL((mx4_product_kernel<T, true, true>), grid, block, 0, stream, a);
+  } else if (a.bf16) {
+    hipLaunchKernelGGL((mx4_product_kernel<T, true, false>), grid, block, 0, stream, a);
+  } else if (beta) {
+    hipLaunchKernelGGL((mx4_product_kernel<T, false, true>), grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((mx4_product_kernel<T, false, false>), grid, block, 0, stream, a);
+  }
   return check_launch();
+}
+
+// Tile edge: the largest of 256, 128 and 64 whose grid still occupies most of
+// the 256 compute units.
+int product(const Mx4ProductArgs& a, hipStream_t stream) {
+  auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
+  if (tiles(256) >= 192) return product_tiles<4>(a, stream);
+  if (tiles(128) >= 192) return product_tiles<2>(a, stream);
+  return product_tiles<1>(a, stream);
 }
 
 }  // namespace
@@ -101,6 +124,7 @@ int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const u
   if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
   const int rc = check_sides(M, N, K);
   if (rc != SHAMPOO_OK) return rc;
+  if (K > kMaxK) return SHAMPOO_EUNSUPPORTED;
   if (ldc < N || !std::isfinite(alpha) || !std::isfinite(beta)) return SHAMPOO_EINVAL;
   if (M == 0 || N == 0) return SHAMPOO_OK;
   if (c == nullptr || (K > 0 && (!valid_mx4(a_codes, a_scales) || !valid_mx4(b_codes, b_scales))))
@@ -135,6 +159,7 @@ int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const
   if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
   int rc = check_sides(M, N, K);
   if (rc != SHAMPOO_OK) return rc;
+  if (K > kMaxK) return SHAMPOO_EUNSUPPORTED;
   if (ldx < K || ldy < N) return SHAMPOO_EINVAL;
   if (M == 0 || N == 0) return SHAMPOO_OK;
   if (y == nullptr || (K > 0 && (x == nullptr || !valid_mx4(w_codes, w_scales)))) return SHAMPOO_EINVAL;
