@@ -123,84 +123,36 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 
 // ---------------------------------------------------------------------------
 // C = alpha A B^T + beta C on tiles of 64 T x 64 T: 4 waves (2 x 2), each T x T
-// blocks of the 32 x 32 x 64 scaled MFMA.  Chunks of 256 columns (128 bytes a row,
-// 8 scale bytes) go straight into one of two LDS buffers
-// (global_load_lds_dwordx4) while the other is multiplied.
+// blocks of the 32 x 32 x 64 scaled MFMA.  Chunks of 256 columns (128 bytes a row)
+// go straight into one of two LDS buffers (global_load_lds_dwordx4) while the
+// other is multiplied.
 //
 //  - Within a chunk lane half h takes the 32-column groups 4 h + s at step s
 //    = 0 ... 3, in both operands, so that its 4 scale bytes of a chunk are one
 //    dword and the MFMA picks byte s.  (The order of the sum over k is free.)
+//  - Scales are staged 1024 columns at a time, a quarter of the next block in
+//    each chunk: 8 lanes read 32 bytes of a row.  Taken chunk by chunk (8 bytes a
+//    row, 32 cache lines a load) they cost as much of the vector cache's time
+//    as half of the codes.
 //  - Fragments of the next step are read while the current one multiplies; the
 //    barrier between chunks stands before the last step, whose fragments are
-//    then in registers: it frees the chunk's buffer for the loads after next
-//    and lets the next chunk's first fragments be read under that step's MFMAs.
+//    then in registers.  It frees the chunk's buffer: A's half of the chunk
+//    after next is loaded into it under this step's MFMAs, B's under the next's.
 //  - 16-byte pieces of a row are permuted by the row (mx4_swz_a, mx4_swz_b), so
 //    that the 8 rows a fragment read takes per clock lie in different banks.
 //  - B is the MFMA's first operand and its rows are assigned to MFMA rows so
-//    that a lane ends with 16 consecutive columns of one row of C.
+//    that a lane ends with 16 consecutive columns of one row of C.  Each wave
+//    turns its 32-row slices through LDS into stores of whole rows.
 // ---------------------------------------------------------------------------
 constexpr int kMx4Chunk = 256;              // columns
 constexpr int kMx4RowBytes = kMx4Chunk / 2;
-constexpr int kMx4RowScales = kMx4Chunk / kMx4Group;
+constexpr int kMx4ScaleDwords = 8;          // of a row and block: 4 chunks
 
 __device__ __forceinline__ int mx4_swz_a(int row) { return (row ^ ((row >> 3) & 3)) & 7; }
 // Row of B that MFMA row r (0 ... 31) of a block takes, and its permutation:
 // 8 consecutive r cover rows 0-3 and 16-19 of the block (plus a multiple of 4).
 __device__ __forceinline__ int mx4_row_b(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 __device__ __forceinline__ int mx4_swz_b(int row) { return (row & 3) | ((row >> 2) & 4); }
-
-// 16 consecutive elements of a row of C at column n (all of them, or those below N).
-template <bool BF16, bool BETA, bool WHOLE>
-__device__ __forceinline__ void mx4_store16(const Mx4ProductArgs& P, int64_t m, int64_t n, const floatx16& v) {
-  const int64_t at = m * P.ldc + n;
-  uint16_t* const ch = static_cast<uint16_t*>(P.c) + at;
-  float* const cf = static_cast<float*>(P.c) + at;
-  if constexpr (!WHOLE) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (n + e < P.N) {
-        float o = P.alpha * v[e];
-        if constexpr (BF16) {
-          if constexpr (BETA) o += P.beta * __builtin_bit_cast(float, (uint32_t)ldg(ch + e) << 16);
-          stg(ch + e, f32_to_bf16_bits(o));
-        } else {
-          if constexpr (BETA) o += P.beta * ldg(cf + e);
-          stg(cf + e, o);
-        }
-      }
-    }
-  } else if constexpr (BF16) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      u32x4 old = {0, 0, 0, 0};
-      if constexpr (BETA) old = ldg_any<u32x4, 2>(ch + 8 * q);
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float lo = P.alpha * v[8 * q + 2 * e], hi = P.alpha * v[8 * q + 2 * e + 1];
-        if constexpr (BETA) {
-          lo += P.beta * __builtin_bit_cast(float, old[e] << 16);
-          hi += P.beta * __builtin_bit_cast(float, old[e] & 0xffff0000u);
-        }
-        w[e] = pack_bf16x2(lo, hi);
-      }
-      stg_any<u32x4, 2>(ch + 8 * q, w);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      floatx4 o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = P.alpha * v[4 * q + e];
-      if constexpr (BETA) {
-        const floatx4 old = ldg_any<floatx4, 4>(cf + 4 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += P.beta * old[e];
-      }
-      stg_any<floatx4, 4>(cf + 4 * q, o);
-    }
-  }
-}
 
 // 16 (4) bytes a lane from memory to consecutive places in LDS.
 __device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
@@ -212,15 +164,58 @@ __device__ __forceinline__ void to_lds4(const uint8_t* from, uint8_t* to) {
                                    (__attribute__((address_space(3))) void*)to, 4, 0, 0);
 }
 
+// 4 elements of a row of C at column n (all of them, or those below N).
+template <bool BF16, bool BETA, bool WHOLE>
+__device__ __forceinline__ void mx4_store4(const Mx4ProductArgs& P, int64_t m, int64_t n, const floatx4& v) {
+  const int64_t at = m * P.ldc + n;
+  uint16_t* const ch = static_cast<uint16_t*>(P.c) + at;
+  float* const cf = static_cast<float*>(P.c) + at;
+  if (!WHOLE && n + 4 > P.N) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e < P.N) {
+        float o = P.alpha * v[e];
+        if constexpr (BF16) {
+          if constexpr (BETA) o += P.beta * __builtin_bit_cast(float, (uint32_t)ldg(ch + e) << 16);
+          stg(ch + e, f32_to_bf16_bits(o));
+        } else {
+          if constexpr (BETA) o += P.beta * ldg(cf + e);
+          stg(cf + e, o);
+        }
+      }
+    }
+    return;
+  }
+  floatx4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = P.alpha * v[e];
+  if constexpr (BF16) {
+    if constexpr (BETA) {
+      const u32x2 old = ldg_any<u32x2, 2>(ch);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] += P.beta * __builtin_bit_cast(float, (e & 1) ? (old[e / 2] & 0xffff0000u) : (old[e / 2] << 16));
+    }
+    stg_any<u32x2, 2>(ch, u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])});
+  } else {
+    if constexpr (BETA) {
+      const floatx4 old = ldg_any<floatx4, 4>(cf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += P.beta * old[e];
+    }
+    stg_any<floatx4, 4>(cf, o);
+  }
+}
+
 template <int T, bool BF16, bool BETA>
 __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArgs P) {
   constexpr int BT = 64 * T;                                   // tile edge
-  constexpr int kData = BT * kMx4RowBytes, kScale = BT * kMx4RowScales;
-  constexpr int kStage = 2 * (kData + kScale);                 // A, B, their scales
+  constexpr int kData = BT * kMx4RowBytes, kStage = 2 * kData;
+  constexpr int kScale = BT * 4 * kMx4ScaleDwords;             // one operand's scale block
   constexpr int LD = kData / (256 * 16);                       // 16-byte loads a thread, operand and chunk
-  constexpr int kScaleLoads = 2 * kScale / (256 * 4);          // of both operands
-  static_assert(LD * 256 * 16 == kData && kScaleLoads * 256 * 4 == 2 * kScale, "chunking");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  constexpr int kSlice = 32 * T + 4;                           // floats: pitch of a wave's output slice
+  static_assert(4 * 32 * kSlice * 4 <= 2 * kStage, "the output slices fit");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 4 * kScale];
 
   // Tiles in groups of 8 tile rows, column by column within a group: the 32
   // tiles that an XCD runs at a time share 8 panels of A and 4 of B.
@@ -241,51 +236,52 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   const int ma = (int)min<int64_t>(BT, P.M - m0) - 1, nb = (int)min<int64_t>(BT, P.N - n0) - 1;  // last valid rows
 
   // Piece c of an operand's chunk: row c / 8, permuted 16-byte column c % 8.
-  uint32_t offA[LD], offB[LD], offS[kScaleLoads];
+  // Rows past the last one repeat it; they end in rows of C that are not stored.
+  uint32_t offA[LD], offB[LD];
 #pragma unroll
   for (int it = 0; it < LD; ++it) {
     const int c = it * 256 + tid, row = c >> 3;
     offA[it] = (uint32_t)min(row, ma) * pitch + 16 * ((c & 7) ^ mx4_swz_a(row));
     offB[it] = (uint32_t)min(row, nb) * pitch + 16 * ((c & 7) ^ mx4_swz_b(row));
   }
-#pragma unroll
-  for (int it = 0; it < kScaleLoads; ++it) {
-    const int d = it * 256 + tid;  // dword d: row d / 2 of A, then of B
-    offS[it] = (uint32_t)(d < 2 * BT ? min(d >> 1, ma) : min((d >> 1) - BT, nb)) * spitch + 4 * (d & 1);
-  }
   const int steps = (int)(P.padded / 128);  // 128-column halves of chunks
   const int full = steps / 2;               // whole chunks
-  // With one dword a thread covers both operands' scales when T = 1: the
-  // operand then differs between the waves, which is uniform within one.
-  auto scale_base = [&](int it) __attribute__((always_inline)) { return it * 256 + wave * 64 < 2 * BT ? As : Bs; };
-  auto issue_a = [&](uint8_t* base, int chunk) __attribute__((always_inline)) {
+  auto issue_a = [&](int buf, int chunk) __attribute__((always_inline)) {
     const uint8_t* const a = A + (int64_t)chunk * kMx4RowBytes;
 #pragma unroll
-    for (int it = 0; it < LD; ++it) to_lds16(a + offA[it], base + (it * 256 + wave * 64) * 16);
+    for (int it = 0; it < LD; ++it) to_lds16(a + offA[it], lds + buf + (it * 256 + wave * 64) * 16);
   };
-  auto issue_b = [&](uint8_t* base, int chunk) __attribute__((always_inline)) {
+  auto issue_b = [&](int buf, int chunk) __attribute__((always_inline)) {
     const uint8_t* const b = B + (int64_t)chunk * kMx4RowBytes;
 #pragma unroll
-    for (int it = 0; it < LD; ++it) to_lds16(b + offB[it], base + kData + (it * 256 + wave * 64) * 16);
-#pragma unroll
-    for (int it = 0; it < kScaleLoads; ++it)
-      to_lds4(scale_base(it) + (int64_t)chunk * kMx4RowScales + offS[it],
-             base + 2 * kData + (it * 256 + wave * 64) * 4);
+    for (int it = 0; it < LD; ++it) to_lds16(b + offB[it], lds + buf + kData + (it * 256 + wave * 64) * 16);
   };
-  // The 128 columns after the whole chunks: pieces and scales of the missing
-  // half re-read the first one and are not used.
-  auto issue_half = [&](uint8_t* base) __attribute__((always_inline)) {
-    const int64_t k = (int64_t)full * kMx4RowBytes, ks = (int64_t)full * kMx4RowScales;
+  // Quarter q of scale block blk: 32 T rows of A (q = 0, 1) or B.  Dword p of a
+  // row goes to place p ^ 2 ((row / 8) % 4), so that the rows of a read, 8
+  // dwords apart, spread over the banks.
+  const int last = (int)(spitch / 4) - 1;
+  auto issue_scales = [&](int blk, int q) __attribute__((always_inline)) {
+    const uint8_t* const from = q < 2 ? As : Bs;
+    const int limit = q < 2 ? ma : nb;
+    const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * wave)), last);
+    uint8_t* const to = lds + 2 * kStage + (blk & 1) * 2 * kScale;
+#pragma unroll
+    for (int it = 0; it < T; ++it) {
+      const uint32_t row = (uint32_t)min(((q & 1) * T + it) * 32 + (tid >> 3), limit);
+      to_lds4(from + row * spitch + col, to + ((q * T + it) * 256 + wave * 64) * 4);
+    }
+  };
+  // The 128 columns after the whole chunks: pieces of the missing half re-read
+  // the first one and are not used.  Their scales are the last dword of a row.
+  auto issue_half = [&](int buf) __attribute__((always_inline)) {
+    const int64_t k = (int64_t)full * kMx4RowBytes;
 #pragma unroll
     for (int it = 0; it < LD; ++it) {
       const int c = it * 256 + tid, row = c >> 3;
       const uint32_t upA = (c ^ mx4_swz_a(row)) & 4, upB = (c ^ mx4_swz_b(row)) & 4;
-      to_lds16(A + k + (offA[it] - 16 * upA), base + (it * 256 + wave * 64) * 16);
-      to_lds16(B + k + (offB[it] - 16 * upB), base + kData + (it * 256 + wave * 64) * 16);
+      to_lds16(A + k + (offA[it] - 16 * upA), lds + buf + (it * 256 + wave * 64) * 16);
+      to_lds16(B + k + (offB[it] - 16 * upB), lds + buf + kData + (it * 256 + wave * 64) * 16);
     }
-#pragma unroll
-    for (int it = 0; it < kScaleLoads; ++it)
-      to_lds4(scale_base(it) + ks + offS[it] - 4 * (tid & 1), base + 2 * kData + (it * 256 + wave * 64) * 4);
   };
 
   floatx16 acc[T][T];
@@ -297,12 +293,32 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
   const int rb = mx4_row_b(r32);
-  // LDS offsets of this lane's fragments (piece 0 of its half) and scales
-  const int fragA = (wm + r32) * kMx4RowBytes, swzA = mx4_swz_a(r32);
-  const int fragB = kData + (wn + rb) * kMx4RowBytes, swzB = mx4_swz_b(rb);
-  const int scaleA = 2 * kData + (wm + r32) * kMx4RowScales, scaleB = 2 * kData + kScale + (wn + rb) * kMx4RowScales;
-  constexpr int kBlock = 32 * kMx4RowBytes, kBlockScales = 32 * kMx4RowScales;
+  // LDS offsets of this lane's rows in a stage and in a scale block
+  const int rowA = (wm + r32) * kMx4RowBytes, rowB = kData + (wn + rb) * kMx4RowBytes;
+  const int swzA = mx4_swz_a(r32), swzB = mx4_swz_b(rb);
+  const int scaleA = 2 * kStage + (wm + r32) * 4 * kMx4ScaleDwords;
+  const int scaleB = 2 * kStage + kScale + (wn + rb) * 4 * kMx4ScaleDwords;
+  constexpr int kBlock = 32 * kMx4RowBytes, kBlockScales = 32 * 4 * kMx4ScaleDwords;
 
+  intx4 fa[2][T], fb[2][T];
+  int sa[T], sb[T];
+  auto read = [&](int buf, int slot, int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+      fa[slot][i] = *reinterpret_cast<const intx4*>(lds + buf + rowA + i * kBlock + 16 * (q ^ swzA));
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+      fb[slot][j] = *reinterpret_cast<const intx4*>(lds + buf + rowB + j * kBlock + 16 * (q ^ swzB));
+  };
+  // This lane's scales at dword p of scale block parity blk.
+  auto read_scales = [&](int blk, int p) __attribute__((always_inline)) {
+    const int base = (blk & 1) * 2 * kScale;
+    const int pa = 4 * (p ^ (2 * ((r32 >> 3) & 3))), pb = 4 * (p ^ (2 * ((rb >> 3) & 3)));
+#pragma unroll
+    for (int i = 0; i < T; ++i) sa[i] = *reinterpret_cast<const int*>(lds + base + scaleA + i * kBlockScales + pa);
+#pragma unroll
+    for (int j = 0; j < T; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
+  };
   constexpr int kWaitAll = 0 | (7 << 4);  // vmcnt(0) lgkmcnt(0)
   auto meet = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(kWaitAll);
@@ -310,34 +326,28 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
-  intx4 fa[2][T], fb[2][T];
-  int sa[T], sb[T];
-  auto read = [&](const uint8_t* base, int slot, int q) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-      fa[slot][i] = *reinterpret_cast<const intx4*>(base + fragA + i * kBlock + 16 * (q ^ swzA));
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-      fb[slot][j] = *reinterpret_cast<const intx4*>(base + fragB + j * kBlock + 16 * (q ^ swzB));
-  };
 
   if (full > 0) {
-    issue_a(lds, 0);
-    issue_b(lds, 0);
+    issue_a(0, 0);
+    issue_b(0, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) issue_scales(0, q);
   }
-  if (steps & 1) issue_half(lds + kStage);
+  if (steps & 1) {
+    issue_half(kStage);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) issue_scales((full / 4) | 1, q);  // odd: block 1's place; clamped to the last dword
+  }
   meet();
   if (steps & 1) {  // lane half h takes groups 2 h and 2 h + 1
-    const uint8_t* const base = lds + kStage;
+    read_scales(1, min((((full / 4) | 1) * kMx4ScaleDwords), last) == last ? 0 : 2 * (full % 4));
 #pragma unroll
-    for (int i = 0; i < T; ++i)
-      sa[i] = *reinterpret_cast<const uint16_t*>(base + scaleA + i * kBlockScales + 2 * h);
+    for (int i = 0; i < T; ++i) sa[i] = sa[i] >> (16 * h);
 #pragma unroll
-    for (int j = 0; j < T; ++j)
-      sb[j] = *reinterpret_cast<const uint16_t*>(base + scaleB + j * kBlockScales + 2 * h);
+    for (int j = 0; j < T; ++j) sb[j] = sb[j] >> (16 * h);
     static_for<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = decltype(S)::value;
-      read(base, s, 2 * h + s);
+      read(kStage, s, 2 * h + s);
 #pragma unroll
       for (int i = 0; i < T; ++i)
 #pragma unroll
@@ -347,22 +357,12 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   }
   if (full > 0) {
     // Loads past the last chunk repeat it into the buffer that nothing reads any more.
-    issue_a(lds + kStage, min(1, full - 1));
-    issue_b(lds + kStage, min(1, full - 1));
-    uint32_t cur = 0;
-    auto read_scales = [&](const uint8_t* base) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < T; ++i)
-        sa[i] = *reinterpret_cast<const int*>(base + scaleA + i * kBlockScales + 4 * h);
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-        sb[j] = *reinterpret_cast<const int*>(base + scaleB + j * kBlockScales + 4 * h);
-    };
-    read_scales(lds);
-    read(lds, 0, 4 * h);
+    issue_a(kStage, min(1, full - 1));
+    int cur = 0;
+    read_scales(0, h);
+    read(0, 0, 4 * h);
     for (int c = 0; c < full; ++c) {
-      const uint8_t* const base = lds + cur;
-      uint8_t* const other = lds + (kStage - cur);
+      const int other = kStage - cur;
       int ta[T], tb[T];
 #pragma unroll
       for (int i = 0; i < T; ++i) ta[i] = sa[i];
@@ -370,14 +370,16 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
       for (int j = 0; j < T; ++j) tb[j] = sb[j];
       static_for<4>([&](auto S) __attribute__((always_inline)) {
         constexpr int s = decltype(S)::value;
+        constexpr int kReads = 2 * T, kMfma = T * T;
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (s == 0) issue_b(other, min(c + 1, full - 1));
+        if constexpr (s == 1) issue_scales(c / 4 + 1, c % 4);
         if constexpr (s < 3) {
-          read(base, (s + 1) & 1, 4 * h + s + 1);
+          read(cur, (s + 1) & 1, 4 * h + s + 1);
         } else {
           meet();
-          issue_a(lds + cur, min(c + 2, full - 1));
-          issue_b(lds + cur, min(c + 2, full - 1));
-          read_scales(other);
+          issue_a(cur, min(c + 2, full - 1));
+          read_scales((c + 1) / 4, 2 * ((c + 1) % 4) + h);
           read(other, 0, 4 * h);
         }
 #pragma unroll
@@ -385,33 +387,59 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
 #pragma unroll
           for (int j = 0; j < T; ++j)
             acc[i][j] = mfma_mx4<s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], tb[j], ta[i]);
-        if constexpr (s < 3) {
-          constexpr int kPairs = 2 * T < T * T ? 2 * T : T * T;
-          static_for<kPairs>([&](auto) __attribute__((always_inline)) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          });
-          if constexpr (T * T > kPairs) __builtin_amdgcn_sched_group_barrier(0x008, T * T - kPairs, 0);
-        }
+        // one MFMA, one LDS read, and so on; then the loads
+        static_for<(kReads < kMfma ? kReads : kMfma)>([&](auto) __attribute__((always_inline)) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, s < 3 ? 1 : 2, 0);
+        });
+        static_for<4>([&](auto) __attribute__((always_inline)) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, s == 1 ? (T + 3) / 4 : (LD + 3) / 4, 0);
+        });
         __builtin_amdgcn_sched_barrier(0);
       });
-      cur = kStage - cur;
+      cur = other;
     }
   }
 
-  const bool whole = m0 + BT <= P.M && n0 + BT <= P.N;
+  // Output: 32 rows of C at a time through this wave's slice of LDS.
+  meet();
+  float* const slice = reinterpret_cast<float*>(lds) + wave * 32 * kSlice;
+  auto output = [&](auto WHOLE) __attribute__((always_inline)) {
+    constexpr bool kWhole = decltype(WHOLE)::value;
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const int64_t m = m0 + wm + 32 * i + r32;
+    for (int i = 0; i < T; ++i) {
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int64_t n = n0 + wn + 32 * j + 16 * h;
-      if (whole) {
-        mx4_store16<BF16, BETA, true>(P, m, n, acc[i][j]);
-      } else if (m < P.M && n < P.N) {
-        mx4_store16<BF16, BETA, false>(P, m, n, acc[i][j]);
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<floatx4*>(slice + r32 * kSlice + 32 * j + 16 * h + 4 * q) =
+              floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      constexpr int kLanes = 8 * T, kRows = 64 / kLanes;  // lanes that hold a row, 4 elements each
+      const int col = 4 * (lane % kLanes);
+      const int64_t n = n0 + wn + col;
+      if constexpr (kWhole) {
+#pragma unroll
+        for (int r = 0; r < 32; r += kRows) {
+          const int row = r + lane / kLanes;
+          mx4_store4<BF16, BETA, true>(P, m0 + wm + 32 * i + row, n,
+                                       *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
+        }
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < 32; r += kRows) {
+          const int row = r + lane / kLanes;
+          const int64_t m = m0 + wm + 32 * i + row;
+          if (m < P.M && n < P.N)
+            mx4_store4<BF16, BETA, false>(P, m, n, *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
+        }
       }
     }
+  };
+  if (m0 + BT <= P.M && n0 + BT <= P.N) {
+    output(std::true_type{});
+  } else {
+    output(std::false_type{});
   }
 }
 
