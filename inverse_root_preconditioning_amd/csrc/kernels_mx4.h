@@ -122,7 +122,7 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 }
 
 // ---------------------------------------------------------------------------
-// C = alpha A B^T + beta C on tiles of 64 T x 64 T: 4 waves (2 x 2), each T x T
+// C = alpha A B^T + beta C on tiles of 64 T x 64 T: W / 2 x 2 waves, each 4 T / W x T
 // blocks of the 32 x 32 x 64 scaled MFMA.  Chunks of 256 columns (128 bytes a row)
 // go straight into one of two LDS buffers (global_load_lds_dwordx4) while the
 // other is multiplied.
@@ -207,15 +207,19 @@ __device__ __forceinline__ void mx4_store4(const Mx4ProductArgs& P, int64_t m, i
   }
 }
 
-template <int T, bool BF16, bool BETA>
-__global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArgs P) {
-  constexpr int BT = 64 * T;                                   // tile edge
+template <int T, int W, bool BF16, bool BETA>
+__global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4ProductArgs P) {
+  constexpr int BT = 64 * T, NT = 64 * W;                      // tile edge, threads
+  constexpr int TM = 4 * T / W, TN = T;                        // blocks of a wave: W / 2 x 2 waves
   constexpr int kData = BT * kMx4RowBytes, kStage = 2 * kData;
   constexpr int kScale = BT * 4 * kMx4ScaleDwords;             // one operand's scale block
-  constexpr int LD = kData / (256 * 16);                       // 16-byte loads a thread, operand and chunk
-  constexpr int kSlice = 32 * T + 4;                           // floats: pitch of a wave's output slice
-  static_assert(4 * 32 * kSlice * 4 <= 2 * kStage, "the output slices fit");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 4 * kScale];
+  constexpr int LD = kData / (NT * 16);                       // 16-byte loads a thread, operand and chunk
+  constexpr int LS = kScale / 2 / (NT * 4);                    // 4-byte scale loads likewise
+  constexpr int kSlice = 32 * TN + 4;                          // floats: pitch of a wave's output slice
+  constexpr int kLds = 2 * kStage + 4 * kScale;
+  static_assert(LD * NT * 16 == kData && LS * NT * 8 == kScale, "chunking");
+  static_assert(W * 32 * kSlice * 4 <= kLds && kLds <= 160 * 1024, "fits the LDS");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
 
   // Tiles in groups of 8 tile rows, column by column within a group: the 32
   // tiles that an XCD runs at a time share 8 panels of A and 4 of B.
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   const int64_t m0 = (int64_t)(8 * group + in_group % rows_here) * BT, n0 = (int64_t)(in_group / rows_here) * BT;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wave >> 1) * 32 * T, wn = (wave & 1) * 32 * T;
+  const int wm = (wave >> 1) * 32 * TM, wn = (wave & 1) * 32 * TN;
   const int r32 = lane & 31, h = lane >> 5;
 
   const uint32_t pitch = (uint32_t)(P.padded / 2), spitch = (uint32_t)(P.padded / kMx4Group);
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   uint32_t offA[LD], offB[LD];
 #pragma unroll
   for (int it = 0; it < LD; ++it) {
-    const int c = it * 256 + tid, row = c >> 3;
+    const int c = it * NT + tid, row = c >> 3;
     offA[it] = (uint32_t)min(row, ma) * pitch + 16 * ((c & 7) ^ mx4_swz_a(row));
     offB[it] = (uint32_t)min(row, nb) * pitch + 16 * ((c & 7) ^ mx4_swz_b(row));
   }
@@ -249,12 +253,12 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   auto issue_a = [&](int buf, int chunk) __attribute__((always_inline)) {
     const uint8_t* const a = A + (int64_t)chunk * kMx4RowBytes;
 #pragma unroll
-    for (int it = 0; it < LD; ++it) to_lds16(a + offA[it], lds + buf + (it * 256 + wave * 64) * 16);
+    for (int it = 0; it < LD; ++it) to_lds16(a + offA[it], lds + buf + (it * NT + wave * 64) * 16);
   };
   auto issue_b = [&](int buf, int chunk) __attribute__((always_inline)) {
     const uint8_t* const b = B + (int64_t)chunk * kMx4RowBytes;
 #pragma unroll
-    for (int it = 0; it < LD; ++it) to_lds16(b + offB[it], lds + buf + kData + (it * 256 + wave * 64) * 16);
+    for (int it = 0; it < LD; ++it) to_lds16(b + offB[it], lds + buf + kData + (it * NT + wave * 64) * 16);
   };
   // Quarter q of scale block blk: 32 T rows of A (q = 0, 1) or B.  Dword p of a
   // row goes to place p ^ 2 ((row / 8) % 4), so that the rows of a read, 8
@@ -263,12 +267,12 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   auto issue_scales = [&](int blk, int q) __attribute__((always_inline)) {
     const uint8_t* const from = q < 2 ? As : Bs;
     const int limit = q < 2 ? ma : nb;
-    const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * wave)), last);
+    const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * (wave & 3))), last);
     uint8_t* const to = lds + 2 * kStage + (blk & 1) * 2 * kScale;
 #pragma unroll
-    for (int it = 0; it < T; ++it) {
-      const uint32_t row = (uint32_t)min(((q & 1) * T + it) * 32 + (tid >> 3), limit);
-      to_lds4(from + row * spitch + col, to + ((q * T + it) * 256 + wave * 64) * 4);
+    for (int it = 0; it < LS; ++it) {
+      const uint32_t row = (uint32_t)min(((q & 1) * LS + it) * (NT / 8) + (tid >> 3), limit);
+      to_lds4(from + row * spitch + col, to + ((q * LS + it) * NT + wave * 64) * 4);
     }
   };
   // The 128 columns after the whole chunks: pieces of the missing half re-read
@@ -277,18 +281,18 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     const int64_t k = (int64_t)full * kMx4RowBytes;
 #pragma unroll
     for (int it = 0; it < LD; ++it) {
-      const int c = it * 256 + tid, row = c >> 3;
+      const int c = it * NT + tid, row = c >> 3;
       const uint32_t upA = (c ^ mx4_swz_a(row)) & 4, upB = (c ^ mx4_swz_b(row)) & 4;
-      to_lds16(A + k + (offA[it] - 16 * upA), lds + buf + (it * 256 + wave * 64) * 16);
-      to_lds16(B + k + (offB[it] - 16 * upB), lds + buf + kData + (it * 256 + wave * 64) * 16);
+      to_lds16(A + k + (offA[it] - 16 * upA), lds + buf + (it * NT + wave * 64) * 16);
+      to_lds16(B + k + (offB[it] - 16 * upB), lds + buf + kData + (it * NT + wave * 64) * 16);
     }
   };
 
-  floatx16 acc[T][T];
+  floatx16 acc[TM][TN];
 #pragma unroll
-  for (int i = 0; i < T; ++i)
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < T; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
@@ -300,14 +304,14 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   const int scaleB = 2 * kStage + kScale + (wn + rb) * 4 * kMx4ScaleDwords;
   constexpr int kBlock = 32 * kMx4RowBytes, kBlockScales = 32 * 4 * kMx4ScaleDwords;
 
-  intx4 fa[2][T], fb[2][T];
-  int sa[T], sb[T];
+  intx4 fa[2][TM], fb[2][TN];
+  int sa[TM], sb[TN];
   auto read = [&](int buf, int slot, int q) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int i = 0; i < TM; ++i)
       fa[slot][i] = *reinterpret_cast<const intx4*>(lds + buf + rowA + i * kBlock + 16 * (q ^ swzA));
 #pragma unroll
-    for (int j = 0; j < T; ++j)
+    for (int j = 0; j < TN; ++j)
       fb[slot][j] = *reinterpret_cast<const intx4*>(lds + buf + rowB + j * kBlock + 16 * (q ^ swzB));
   };
   // This lane's scales at dword p of scale block parity blk.
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     const int base = (blk & 1) * 2 * kScale;
     const int pa = 4 * (p ^ (2 * ((r32 >> 3) & 3))), pb = 4 * (p ^ (2 * ((rb >> 3) & 3)));
 #pragma unroll
-    for (int i = 0; i < T; ++i) sa[i] = *reinterpret_cast<const int*>(lds + base + scaleA + i * kBlockScales + pa);
+    for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const int*>(lds + base + scaleA + i * kBlockScales + pa);
 #pragma unroll
-    for (int j = 0; j < T; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
+    for (int j = 0; j < TN; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
   };
   constexpr int kWaitAll = 0 | (7 << 4);  // vmcnt(0) lgkmcnt(0)
   auto meet = [&]() __attribute__((always_inline)) {
@@ -342,16 +346,16 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   if (steps & 1) {  // lane half h takes groups 2 h and 2 h + 1
     read_scales(1, min((((full / 4) | 1) * kMx4ScaleDwords), last) == last ? 0 : 2 * (full % 4));
 #pragma unroll
-    for (int i = 0; i < T; ++i) sa[i] = sa[i] >> (16 * h);
+    for (int i = 0; i < TM; ++i) sa[i] = sa[i] >> (16 * h);
 #pragma unroll
-    for (int j = 0; j < T; ++j) sb[j] = sb[j] >> (16 * h);
+    for (int j = 0; j < TN; ++j) sb[j] = sb[j] >> (16 * h);
     static_for<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = decltype(S)::value;
       read(kStage, s, 2 * h + s);
 #pragma unroll
-      for (int i = 0; i < T; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < T; ++j) acc[i][j] = mfma_mx4<s>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i]);
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_mx4<s>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i]);
     });
     meet();
   }
@@ -363,14 +367,14 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     read(0, 0, 4 * h);
     for (int c = 0; c < full; ++c) {
       const int other = kStage - cur;
-      int ta[T], tb[T];
+      int ta[TM], tb[TN];
 #pragma unroll
-      for (int i = 0; i < T; ++i) ta[i] = sa[i];
+      for (int i = 0; i < TM; ++i) ta[i] = sa[i];
 #pragma unroll
-      for (int j = 0; j < T; ++j) tb[j] = sb[j];
+      for (int j = 0; j < TN; ++j) tb[j] = sb[j];
       static_for<4>([&](auto S) __attribute__((always_inline)) {
         constexpr int s = decltype(S)::value;
-        constexpr int kReads = 2 * T, kMfma = T * T;
+        constexpr int kReads = TM + TN, kMfma = TM * TN;
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (s == 0) issue_b(other, min(c + 1, full - 1));
         if constexpr (s == 1) issue_scales(c / 4 + 1, c % 4);
@@ -383,9 +387,9 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
           read(other, 0, 4 * h);
         }
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < T; ++j)
+          for (int j = 0; j < TN; ++j)
             acc[i][j] = mfma_mx4<s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], tb[j], ta[i]);
         // one MFMA, one LDS read, and so on; then the loads
         static_for<(kReads < kMfma ? kReads : kMfma)>([&](auto) __attribute__((always_inline)) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
         });
         static_for<4>([&](auto) __attribute__((always_inline)) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x020, s == 1 ? (T + 3) / 4 : (LD + 3) / 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, s == 1 ? (LS + 3) / 4 : (LD + 3) / 4, 0);
         });
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -408,14 +412,14 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   auto output = [&](auto WHOLE) __attribute__((always_inline)) {
     constexpr bool kWhole = decltype(WHOLE)::value;
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int j = 0; j < T; ++j)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<floatx4*>(slice + r32 * kSlice + 32 * j + 16 * h + 4 * q) =
               floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-      constexpr int kLanes = 8 * T, kRows = 64 / kLanes;  // lanes that hold a row, 4 elements each
+      constexpr int kLanes = 8 * TN, kRows = 64 / kLanes;  // lanes that hold a row, 4 elements each
       const int col = 4 * (lane % kLanes);
       const int64_t n = n0 + wn + col;
       if constexpr (kWhole) {

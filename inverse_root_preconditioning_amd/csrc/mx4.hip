@@ -50,22 +50,22 @@ int quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_s
   return check_launch();
 }
 
-template <int T>
+template <int T, int W>
 int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
   const int64_t tm = (a.M + 64 * T - 1) / (64 * T), tn = (a.N + 64 * T - 1) / (64 * T);
   if (tm * tn > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
   a.tiles_m = (uint32_t)tm;
   a.tiles_n = (uint32_t)tn;
-  const dim3 grid((uint32_t)(tm * tn)), block(256);
+  const dim3 grid((uint32_t)(tm * tn)), block(64 * W);
   const bool beta = a.beta != 0.f;
   if (a.bf16 && beta) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, true, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, W, true, true>), grid, block, 0, stream, a);
   } else if (a.bf16) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, true, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, W, true, false>), grid, block, 0, stream, a);
   } else if (beta) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, false, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, W, false, true>), grid, block, 0, stream, a);
   } else {
-    hipLaunchKernelGGL((mx4_product_kernel<T, false, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, W, false, false>), grid, block, 0, stream, a);
   }
   return check_launch();
 }
@@ -74,9 +74,9 @@ int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
 // the 256 compute units.
 int product(const Mx4ProductArgs& a, hipStream_t stream) {
   auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
-  if (tiles(256) >= 192) return product_tiles<4>(a, stream);
-  if (tiles(128) >= 192) return product_tiles<2>(a, stream);
-  return product_tiles<1>(a, stream);
+  if (tiles(256) >= 192) return product_tiles<4, 8>(a, stream);
+  if (tiles(128) >= 192) return product_tiles<2, 4>(a, stream);
+  return product_tiles<1, 4>(a, stream);
 }
 
 }  // namespace
