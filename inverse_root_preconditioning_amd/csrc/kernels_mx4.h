@@ -14,88 +14,295 @@ typedef int intx8 __attribute__((ext_vector_type(8)));
 
 __host__ __device__ __forceinline__ int64_t mx4_padded(int64_t k) { return (k + kMx4Pad - 1) / kMx4Pad * kMx4Pad; }
 
-// 2^(s - 127) for a scale byte s <= 254 (s = 0 is a subnormal float).
-__device__ __forceinline__ float mx4_pow2(int s) {
-  return __builtin_bit_cast(float, s == 0 ? 0x00400000u : (uint32_t)s << 23);
-}
-
-// Scale byte of a group from the bits of its largest magnitude.
-__device__ __forceinline__ int mx4_scale(uint32_t top_bits) {
+// Scale byte of a group from the bits of its largest magnitude (as fp32).
+__device__ __forceinline__ uint32_t mx4_scale(uint32_t top_bits) {
   const int e = (int)(top_bits >> 23);
-  return e == 255 ? 255 : max(e - 2, 0);
+  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
 }
 
-// E2M1 code of x / 2^(s - 127), to nearest even, at most 6.
-__device__ __forceinline__ uint32_t mx4_encode(float x, int s) {
-  if (s == 255) return 0;
-  const float a = fabsf(x) * __builtin_bit_cast(float, (uint32_t)(254 - s) << 23);
-  uint32_t c;
-  if (a < 2.f) {
-    c = (uint32_t)rintf(2.f * a);
-  } else if (a < 4.f) {
-    c = (uint32_t)rintf(a) + 2;
-  } else {
-    c = min((uint32_t)rintf(0.5f * a) + 4, 7u);
-  }
-  return c | (x < 0.f ? 8u : 0u);
+// The conversions take 2^(s - 127) as a float of exponent field s, also where
+// that is a subnormal (s = 0): they use the field alone.  They round to
+// nearest even and saturate at 6.
+__device__ __forceinline__ float mx4_scale_float(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+
+// Largest of v over groups of 4 (8) consecutive lanes, in every lane.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  static_assert(LANES == 4 || LANES == 8, "lanes of a group");
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));  // quad_perm 1 0 3 2
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));  // quad_perm 2 3 0 1
+  if constexpr (LANES == 8)
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror
+  return v;
 }
 
-__device__ __forceinline__ float mx4_value(uint32_t code, int s) {
-  const uint32_t c = code & 7;
-  // 0, 0.5, then 1 and a mantissa bit below the exponent c >> 1
-  float v = c < 2 ? 0.5f * (float)c : __builtin_bit_cast(float, ((126u + (c >> 1)) << 23) | ((c & 1u) << 22));
-  if (code & 8) v = -v;
-  return s == 255 ? __builtin_nanf("") : v * mx4_pow2(s);
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t abs_halves(uint32_t a) { return a & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+
+// Byte SEL of `old` replaced by the codes of two values.
+template <int SEL>
+__device__ __forceinline__ uint32_t mx4_codes_bf16(uint32_t old, uint32_t pair, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2_t, pair), scale, SEL);
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t mx4_codes_f32(uint32_t old, float a, float b, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, SEL);
 }
 
 struct Mx4QuantArgs {
   const void* x;
-  int64_t rows, cols;       // of the quantised matrix
-  int64_t row_step, col_step;  // element strides of x along them
-  int64_t padded;           // mx4_padded(cols)
-  uint8_t *codes, *scales;
-  int bf16;
+  int64_t rows, cols, ld;
+  int64_t padded_cols, padded_rows;  // mx4_padded
+  uint8_t *codes, *scales;           // of x
+  uint8_t *codes_t, *scales_t;       // of its transpose
+  uint32_t col_blocks;
+  int lanes_log2;                    // rows kernel: lanes on a row (8 elements each)
 };
 
-// One lane an element, 32 lanes a group.
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantArgs P) {
-  const int64_t groups = P.padded / kMx4Group;
-  const int64_t id = (int64_t)blockIdx.x * 8 + threadIdx.x / kMx4Group;
-  const int lane = threadIdx.x % kMx4Group;
-  const bool in = id < P.rows * groups;
-  const int64_t r = in ? id / groups : 0, k = in ? (id - r * groups) * kMx4Group + lane : 0;
-  float x = 0.f;
-  if (in && k < P.cols) {
-    const int64_t at = r * P.row_step + k * P.col_step;
-    x = P.bf16 ? __builtin_bit_cast(float, (uint32_t)ldg(static_cast<const uint16_t*>(P.x) + at) << 16)
-               : ldg(static_cast<const float*>(P.x) + at);
-  }
-  uint32_t top = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+// 8 consecutive bf16 (16 bytes) or 4 consecutive floats of a row, those from
+// `left` on as zero.
+template <bool BF16>
+struct Mx4Piece;
+template <>
+struct Mx4Piece<true> {
+  static constexpr int kElems = 8;
+  u32x4 w;
+  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left) {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+    if (left >= 8) {
+      w = ldg_any<u32x4, 2>(p);
+    } else {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
-  const int s = mx4_scale(top);
-  const uint32_t c = mx4_encode(x, s), hi = (uint32_t)__shfl_xor((int)c, 1, kWave);
-  if (!in) return;
-  if ((lane & 1) == 0) stg(P.codes + r * (P.padded / 2) + k / 2, (uint8_t)(c | (hi << 4)));
-  if (lane == 0) stg(P.scales + id, (uint8_t)s);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = 2 * e < left ? ldg(p + 2 * e) : 0u, hi = 2 * e + 1 < left ? ldg(p + 2 * e + 1) : 0u;
+        w[e] = lo | (hi << 16);
+      }
+    }
+  }
+  // Bits, as fp32, of the largest magnitude.
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = max_halves(max_halves(abs_halves(w[0]), abs_halves(w[1])),
+                                  max_halves(abs_halves(w[2]), abs_halves(w[3])));
+    return max(m & 0xffff0000u, m << 16);
+  }
+  __device__ __forceinline__ uint32_t encode(float scale) const {
+    uint32_t c = mx4_codes_bf16<0>(0u, w[0], scale);
+    c = mx4_codes_bf16<1>(c, w[1], scale);
+    c = mx4_codes_bf16<2>(c, w[2], scale);
+    return mx4_codes_bf16<3>(c, w[3], scale);
+  }
+};
+template <>
+struct Mx4Piece<false> {
+  static constexpr int kElems = 4;
+  floatx4 w;
+  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left) {
+    const float* p = static_cast<const float*>(x) + at;
+    if (left >= 4) {
+      w = ldg_any<floatx4, 4>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = e < left ? ldg(p + e) : 0.f;
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(abs_bits(w[0]), abs_bits(w[1])), max(abs_bits(w[2]), abs_bits(w[3])));
+  }
+  __device__ __forceinline__ uint32_t encode(float scale) const {  // two bytes
+    const uint32_t c = mx4_codes_f32<0>(0u, w[0], w[1], scale);
+    return mx4_codes_f32<1>(c, w[2], w[3], scale);
+  }
+};
+
+// Rows only: 8 elements a lane, 4 lanes a group; a workgroup takes `lanes` x 8
+// columns of 4 x 256 / lanes rows.  Memory-bound.
+template <bool BF16>
+__global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantArgs P) {
+  constexpr int kPasses = 4, kPieces = 8 / Mx4Piece<BF16>::kElems;
+  const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
+  const int lanes = 1 << P.lanes_log2, per_pass = 256 >> P.lanes_log2;
+  const int64_t col = ((int64_t)cb * lanes + (threadIdx.x & (lanes - 1))) * 8;
+  const int64_t row0 = (int64_t)rb * kPasses * per_pass + (threadIdx.x >> P.lanes_log2);
+  Mx4Piece<BF16> x[kPasses][kPieces];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = row0 + i * per_pass;
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const int64_t c = col + q * Mx4Piece<BF16>::kElems;
+      x[i][q].load(P.x, r * P.ld + c, r < P.rows ? P.cols - c : 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = row0 + i * per_pass;
+    uint32_t top = x[i][0].top();
+    if constexpr (kPieces == 2) top = max(top, x[i][1].top());
+    const uint32_t s = mx4_scale(group_max<4>(top));
+    const float scale = mx4_scale_float(s);
+    uint32_t c = x[i][0].encode(scale);
+    if constexpr (kPieces == 2) c = (c & 0xffffu) | (x[i][1].encode(scale) << 16);
+    if (s == 255) c = 0;
+    if (r < P.rows && col < P.padded_cols) {
+      stg(reinterpret_cast<uint32_t*>(P.codes + r * (P.padded_cols / 2) + col / 2), c);
+      if ((threadIdx.x & 3) == 0) stg(P.scales + r * (P.padded_cols / kMx4Group) + col / kMx4Group, (uint8_t)s);
+    }
+  }
 }
 
-__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                             int64_t rows, int64_t cols, int64_t padded, void* out,
-                                                             int bf16, int64_t ld) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = id / (padded / 2), b = id - r * (padded / 2);
-  if (r >= rows) return;
-  const uint32_t c = ldg(codes + id);
-  const int s = ldg(scales + r * (padded / kMx4Group) + 2 * b / kMx4Group);
-  for (int h = 0; h < 2; ++h) {
-    const int64_t k = 2 * b + h;
-    if (k >= cols) return;
-    const float v = mx4_value((c >> (4 * h)) & 15u, s);
-    if (bf16) {
-      stg(static_cast<uint16_t*>(out) + r * ld + k, f32_to_bf16_bits(v));
+// Columns, and rows as well with ROWS, from one reading: a wave holds 32 rows of
+// 64 pieces in registers, so that a group along a column lies within a lane
+// and one along a row within 4 (bf16) or 8 lanes.  The 4 waves of a workgroup
+// are stacked, which brings the 16 bytes that a lane has for a column of the
+// transpose beside its neighbours' (64 bytes).  Rows up to padded_rows are
+// zero groups.
+template <bool BF16, bool ROWS>
+__global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4QuantArgs P) {
+  constexpr int V = Mx4Piece<BF16>::kElems, kLanes = kMx4Group / V;
+  const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int64_t row0 = (int64_t)rb * 128 + wave * 32, col = ((int64_t)cb * kWave + lane) * V;
+  Mx4Piece<BF16> x[32];
+  if (row0 + 32 <= P.rows && ((int64_t)cb + 1) * kWave * V <= P.cols) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) x[r].load(P.x, (row0 + r) * P.ld + col, V);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) x[r].load(P.x, (row0 + r) * P.ld + col, row0 + r < P.rows ? P.cols - col : 0);
+  }
+  if constexpr (ROWS) {
+    const int part = lane % kLanes;
+    uint8_t* codes = P.codes + row0 * (P.padded_cols / 2) + col * 4 / 8;
+    uint8_t* scales = P.scales + row0 * (P.padded_cols / kMx4Group) + col / kMx4Group;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t s = mx4_scale(group_max<kLanes>(x[r].top()));
+      uint32_t c = x[r].encode(mx4_scale_float(s));
+      if (s == 255) c = 0;
+      const bool in = row0 + r < P.rows && col < P.padded_cols;
+      if (in) {
+        if constexpr (BF16) {
+          stg(reinterpret_cast<uint32_t*>(codes + r * (P.padded_cols / 2)), c);
+        } else {
+          stg(reinterpret_cast<uint16_t*>(codes + r * (P.padded_cols / 2)), (uint16_t)c);
+        }
+      }
+      // each lane of a group keeps the scale of one of kLanes rows, then all store
+      if (part == r % kLanes) mine = s;
+      if (r % kLanes == kLanes - 1) {
+        const int q = r - (kLanes - 1) + part;
+        if (row0 + q < P.rows && col < P.padded_cols) stg(scales + q * (P.padded_cols / kMx4Group), (uint8_t)mine);
+      }
+    }
+  }
+  const int64_t pitch = P.padded_rows / 2, spitch = P.padded_rows / kMx4Group;
+  static_for<V>([&](auto I) __attribute__((always_inline)) {
+    constexpr int i = decltype(I)::value;
+    uint32_t top = 0;
+    u32x4 out;
+    if constexpr (BF16) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) m = max_halves(m, abs_halves(x[r].w[i / 2]));
+      top = (i & 1) ? m & 0xffff0000u : m << 16;
     } else {
-      stg(static_cast<float*>(out) + r * ld + k, v);
+#pragma unroll
+      for (int r = 0; r < 32; ++r) top = max(top, abs_bits(x[r].w[i]));
+    }
+    const uint32_t s = mx4_scale(top);
+    const float scale = mx4_scale_float(s);
+    static_for<4>([&](auto D) __attribute__((always_inline)) {
+      constexpr int d = decltype(D)::value;
+      uint32_t c = 0;
+      static_for<4>([&](auto B) __attribute__((always_inline)) {
+        constexpr int b = decltype(B)::value, r = 8 * d + 2 * b;
+        if constexpr (BF16) {
+          // rows r and r + 1 of this column: both low or both high halves
+          const uint32_t pair = __builtin_amdgcn_perm(x[r + 1].w[i / 2], x[r].w[i / 2],
+                                                      (i & 1) ? 0x07060302u : 0x05040100u);
+          c = mx4_codes_bf16<b>(c, pair, scale);
+        } else {
+          c = mx4_codes_f32<b>(c, x[r].w[i], x[r + 1].w[i], scale);
+        }
+      });
+      out[d] = s == 255 ? 0u : c;
+    });
+    if (col + i < P.cols) {
+      stg(reinterpret_cast<u32x4*>(P.codes_t + (col + i) * pitch + row0 / 2), out);
+      stg(P.scales_t + (col + i) * spitch + row0 / kMx4Group, (uint8_t)s);
+    }
+  });
+}
+
+struct Mx4DequantArgs {
+  const uint8_t *codes, *scales;
+  int64_t rows, cols, padded, ld;
+  void* out;
+  uint32_t col_blocks;
+  int lanes_log2;
+};
+
+// 8 codes a lane, the rows kernel's shape.
+template <bool BF16>
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs P) {
+  constexpr int kPasses = 4;
+  const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
+  const int lanes = 1 << P.lanes_log2, per_pass = 256 >> P.lanes_log2;
+  const int64_t col = ((int64_t)cb * lanes + (threadIdx.x & (lanes - 1))) * 8;
+  const int64_t row0 = (int64_t)rb * kPasses * per_pass + (threadIdx.x >> P.lanes_log2);
+  if (col >= P.cols) return;
+  uint32_t c[kPasses], s[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = min(row0 + i * per_pass, P.rows - 1);
+    c[i] = ldg(reinterpret_cast<const uint32_t*>(P.codes + r * (P.padded / 2) + col / 2));
+    s[i] = ldg(P.scales + r * (P.padded / kMx4Group) + col / kMx4Group);
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = row0 + i * per_pass;
+    if (r >= P.rows) return;
+    const float scale = mx4_scale_float(s[i]);
+    const bool bad = s[i] == 255;
+    const int64_t at = r * P.ld + col;
+    if constexpr (BF16) {
+      u32x4 w;
+      w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 0));
+      w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 1));
+      w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 2));
+      w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 3));
+      if (bad) w = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+      uint16_t* const o = static_cast<uint16_t*>(P.out) + at;
+      if (col + 8 <= P.cols) {
+        stg_any<u32x4, 2>(o, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < P.cols) stg(o + e, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
+      }
+    } else {
+      floatx4 v[2];
+      static_for<4>([&](auto B) __attribute__((always_inline)) {
+        constexpr int b = decltype(B)::value;
+        const f32x2_t t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], scale, b);
+        v[b / 2][2 * (b & 1)] = bad ? __builtin_nanf("") : t[0];
+        v[b / 2][2 * (b & 1) + 1] = bad ? __builtin_nanf("") : t[1];
+      });
+      float* const o = static_cast<float*>(P.out) + at;
+      if (col + 8 <= P.cols) {
+        stg_any<floatx4, 4>(o, v[0]);
+        stg_any<floatx4, 4>(o + 4, v[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < P.cols) stg(o + e, v[e / 4][e & 3]);
+      }
     }
   }
 }

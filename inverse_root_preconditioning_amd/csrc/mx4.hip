@@ -31,22 +31,49 @@ bool valid_mx4(const uint8_t* codes, const uint8_t* scales) {
   return codes != nullptr && scales != nullptr && aligned16(codes) && aligned16(scales);
 }
 
-int quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_step, int64_t col_step,
-             uint8_t* codes, uint8_t* scales, hipStream_t stream) {
-  Mx4QuantArgs a;
-  a.x = x;
-  a.rows = rows;
-  a.cols = cols;
-  a.row_step = row_step;
-  a.col_step = col_step;
-  a.padded = mx4_padded(cols);
-  a.codes = codes;
-  a.scales = scales;
-  a.bf16 = dtype == SHAMPOO_T_BF16;
-  const int64_t blocks = (rows * (a.padded / kMx4Group) + 7) / 8;
-  if (blocks == 0) return SHAMPOO_OK;
-  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
-  hipLaunchKernelGGL(mx4_quantize_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, a);
+// Lanes (a power of two, 16 to 256) that take a row of 8-element pieces, and how
+// many such stretches a row has.
+void row_shape(int64_t padded, int* lanes_log2, int64_t* col_blocks) {
+  int k = 4;
+  while (k < 8 && ((int64_t)8 << k) < padded) ++k;
+  *lanes_log2 = k;
+  *col_blocks = (padded + ((int64_t)8 << k) - 1) / ((int64_t)8 << k);
+}
+
+int quantize(Mx4QuantArgs a, bool bf16, hipStream_t stream) {
+  const bool rows = a.codes != nullptr, cols = a.codes_t != nullptr;
+  a.padded_cols = mx4_padded(a.cols);
+  a.padded_rows = mx4_padded(a.rows);
+  int64_t col_blocks, row_blocks;
+  if (cols) {
+    const int64_t width = kWave * (bf16 ? 8 : 4);
+    col_blocks = ((rows ? a.padded_cols : a.cols) + width - 1) / width;
+    row_blocks = a.padded_rows / 128;
+  } else {
+    row_shape(a.padded_cols, &a.lanes_log2, &col_blocks);
+    const int64_t per_block = 4 * (256 >> a.lanes_log2);
+    row_blocks = (a.rows + per_block - 1) / per_block;
+  }
+  if (col_blocks * row_blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  a.col_blocks = (uint32_t)col_blocks;
+  const dim3 grid((uint32_t)(col_blocks * row_blocks)), block(256);
+  if (!cols) {
+    if (bf16) {
+      hipLaunchKernelGGL(mx4_quantize_rows_kernel<true>, grid, block, 0, stream, a);
+    } else {
+      hipLaunchKernelGGL(mx4_quantize_rows_kernel<false>, grid, block, 0, stream, a);
+    }
+  } else if (rows) {
+    if (bf16) {
+      hipLaunchKernelGGL((mx4_quantize_cols_kernel<true, true>), grid, block, 0, stream, a);
+    } else {
+      hipLaunchKernelGGL((mx4_quantize_cols_kernel<false, true>), grid, block, 0, stream, a);
+    }
+  } else if (bf16) {
+    hipLaunchKernelGGL((mx4_quantize_cols_kernel<true, false>), grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((mx4_quantize_cols_kernel<false, false>), grid, block, 0, stream, a);
+  }
   return check_launch();
 }
 
@@ -95,10 +122,16 @@ int shampoo_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, i
   if (x == nullptr || (codes == nullptr && codes_t == nullptr)) return SHAMPOO_EINVAL;
   if ((codes != nullptr && !valid_mx4(codes, scales)) || (codes_t != nullptr && !valid_mx4(codes_t, scales_t)))
     return SHAMPOO_EINVAL;
-  int done = SHAMPOO_OK;
-  if (codes != nullptr) done = quantize(x, dtype, rows, cols, ld, 1, codes, scales, stream);
-  if (done == SHAMPOO_OK && codes_t != nullptr) done = quantize(x, dtype, cols, rows, 1, ld, codes_t, scales_t, stream);
-  return done;
+  Mx4QuantArgs a = {};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.codes = codes;
+  a.scales = scales;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  return quantize(a, dtype == SHAMPOO_T_BF16, stream);
 }
 
 int shampoo_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
@@ -109,10 +142,25 @@ int shampoo_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
   if (ld < cols) return SHAMPOO_EINVAL;
   if (rows == 0 || cols == 0) return SHAMPOO_OK;
   if (!valid_mx4(codes, scales) || out == nullptr) return SHAMPOO_EINVAL;
-  const int64_t padded = mx4_padded(cols), blocks = (rows * (padded / 2) + 255) / 256;
-  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
-  hipLaunchKernelGGL(mx4_dequantize_kernel, dim3((uint32_t)blocks), dim3(256), 0, stream, codes, scales, rows, cols,
-                     padded, out, dtype == SHAMPOO_T_BF16, ld);
+  Mx4DequantArgs a;
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = cols;
+  a.padded = mx4_padded(cols);
+  a.ld = ld;
+  a.out = out;
+  int64_t col_blocks;
+  row_shape(a.padded, &a.lanes_log2, &col_blocks);
+  const int64_t per_block = 4 * (256 >> a.lanes_log2), row_blocks = (rows + per_block - 1) / per_block;
+  if (col_blocks * row_blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  a.col_blocks = (uint32_t)col_blocks;
+  const dim3 grid((uint32_t)(col_blocks * row_blocks)), block(256);
+  if (dtype == SHAMPOO_T_BF16) {
+    hipLaunchKernelGGL(mx4_dequantize_kernel<true>, grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL(mx4_dequantize_kernel<false>, grid, block, 0, stream, a);
+  }
   return check_launch();
 }
 
