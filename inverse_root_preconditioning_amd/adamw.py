@@ -10,7 +10,7 @@ All the arithmetic runs in the HIP library (see capi and include/shampoo.h).
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 
 import numpy as np
 import torch
@@ -21,9 +21,19 @@ _TYPES = {torch.float32: capi.T_F32, torch.bfloat16: capi.T_BF16}
 _STATES = {"f32": capi.STATE_F32, "mx8": capi.STATE_MX8}
 
 
-def _on(stream):
-    """Context in which allocations belong to the stream that uses them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without the Python objects
+
+
+def _on_stream(fn):
+    """Lets fn(...) be called with stream=...: its work and its allocations then
+    belong to that stream (else to the current one)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
 
 
 def _dense(t):
@@ -67,6 +77,7 @@ class TensorTable:
         self.dtype = dtype
         self.type = _TYPES[dtype]
         self.device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+        self.index = self.device.index
         self.layouts = [_layout(t) for t in tensors]
         self._keep = tensors
         sizes = np.array([t.numel() for t in tensors], dtype=np.int64)
@@ -92,20 +103,20 @@ class TensorTable:
         self._norm_ws = capi.shampoo_grad_norm_workspace_bytes(self.nsegments)
 
 
-def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
+@_on_stream
+def grad_norm(table, max_norm=float("inf"), out=None):
     """float32 [2] on the device: the Euclidean norm of all the table's tensors
     as one vector, and min(1, max_norm / norm) (NaN if the norm is not finite,
     which makes AdamW.step change nothing)."""
-    with _on(stream):
-        if out is None:
-            out = torch.empty(2, dtype=torch.float32, device=table.device)
-        elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2):
-            raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements")
-        ws = torch.empty(table._norm_ws, dtype=torch.uint8, device=table.device)
-        handle = torch.cuda.current_stream(table.device).cuda_stream
-        capi.check(capi.shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
-                                          out.data_ptr(), ws.data_ptr(), table._norm_ws, handle),
-                   "shampoo_grad_norm")
+    if out is None:
+        out = table.tensor.new_empty(2, dtype=torch.float32)
+    elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2):
+        raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements")
+    need = table._norm_ws
+    ws = table.tensor.new_empty(need, dtype=torch.uint8) if need else None
+    capi.check(capi.shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
+                                      out.data_ptr(), ws.data_ptr() if need else 0, need, _raw_stream(table.index)),
+               "shampoo_grad_norm")
     return out
 
 
@@ -145,7 +156,7 @@ class AdamW:
         self.state = state
         p, dev = self.params, self.params.device
         self.offsets = p.offsets
-        self.copies = None
+        self.copies = self._checked = None
         if copies is not None:
             self.copies = copies if isinstance(copies, TensorTable) else TensorTable(copies)
             if p.dtype != torch.float32 or self.copies.dtype != torch.bfloat16:
@@ -162,12 +173,16 @@ class AdamW:
         self.v_scale = torch.zeros(p.total // capi.GROUP, dtype=torch.uint8, device=dev) if low else None
 
     def _same(self, table, name):
+        if table is self._checked:
+            return                     # neither its layouts nor its device change
         if table.layouts != self.params.layouts:
             raise ValueError(f"{name} differ from the parameters in number, size or layout")
         if table.device != self.params.device:
             raise ValueError(f"{name} are on another device than the parameters")
+        self._checked = table
 
-    def step(self, grads, lr=None, grad_scale=None, stream=None):
+    @_on_stream
+    def step(self, grads, lr=None, grad_scale=None):
         """One step with the gradients of a TensorTable (or a list of tensors).
         grad_scale: float32 tensor of one element on the device that multiplies
         the gradients; if it is not finite, nothing changes but `t`."""
@@ -181,28 +196,25 @@ class AdamW:
                 raise ValueError("grad_scale must be a float32 CUDA tensor of one element")
             scale_ptr = grad_scale.data_ptr()
         low = self.m_scale is not None
-        handle = (stream or torch.cuda.current_stream(p.device)).cuda_stream
         capi.check(capi.shampoo_adamw(
             p.ptr, grads.ptr, self.copies.ptr if self.copies is not None else 0, self.hyper.data_ptr(), p.n,
             p.segments_ptr, p.nsegments, p.type, grads.type, _STATES[self.state], self.m.data_ptr(), self.v.data_ptr(),
             self.m_scale.data_ptr() if low else 0, self.v_scale.data_ptr() if low else 0,
             self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.t + 1, self.seed, scale_ptr,
-            handle), "shampoo_adamw")
+            _raw_stream(p.index)), "shampoo_adamw")
         self.t += 1
 
-    def moments(self, dtype=torch.float32, stream=None):
+    @_on_stream
+    def moments(self, dtype=torch.float32):
         """The values of (m, v) as flat tensors in the state's layout."""
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
         if self.m_scale is None:
-            with _on(stream):
-                return self.m.to(dtype), self.v.to(dtype)
-        with _on(stream):
-            m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
-            capi.check(capi.shampoo_adamw_moments(
-                self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), m.numel(),
-                m.data_ptr(), v.data_ptr(), _TYPES[dtype], torch.cuda.current_stream(m.device).cuda_stream),
-                "shampoo_adamw_moments")
+            return self.m.to(dtype), self.v.to(dtype)
+        m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
+        capi.check(capi.shampoo_adamw_moments(
+            self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), m.numel(),
+            m.data_ptr(), v.data_ptr(), _TYPES[dtype], _raw_stream(self.params.index)), "shampoo_adamw_moments")
         return m, v
 
     def state_dict(self):

@@ -158,13 +158,15 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantAr
 // Columns, and rows as well with ROWS, from one reading: a wave holds 32 rows of
 // 64 pieces in registers, so that a group along a column lies within a lane
 // and one along a row within 4 (bf16) or 8 lanes.  The 4 waves of a workgroup
-// are stacked, which brings the 16 bytes that a lane has for a column of the
-// transpose beside its neighbours' (64 bytes).  Rows up to padded_rows are
-// zero groups.
+// are stacked, and the 16 bytes that a lane has for a column of the transpose
+// meet its neighbours' in LDS, so that 64 bytes are stored at a time.  Rows up
+// to padded_rows are zero groups.
 template <bool BF16, bool ROWS>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4QuantArgs P) {
   constexpr int V = Mx4Piece<BF16>::kElems, kLanes = kMx4Group / V;
   const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
+  constexpr int kCols = kWave * V;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kCols * (64 + 4)];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int64_t row0 = (int64_t)rb * 128 + wave * 32, col = ((int64_t)cb * kWave + lane) * V;
   Mx4Piece<BF16> x[32];
@@ -233,11 +235,24 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4Quan
       });
       out[d] = s == 255 ? 0u : c;
     });
-    if (col + i < P.cols) {
-      stg(reinterpret_cast<u32x4*>(P.codes_t + (col + i) * pitch + row0 / 2), out);
-      stg(P.scales_t + (col + i) * spitch + row0 / kMx4Group, (uint8_t)s);
-    }
+    // place (wave + lane) % 4 of the column's four: lanes are V columns apart
+    *reinterpret_cast<u32x4*>(lds + (lane * V + i) * 64 + 16 * ((wave + lane) & 3)) = out;
+    lds[kCols * 64 + (lane * V + i) * 4 + wave] = (uint8_t)s;
   });
+  __syncthreads();
+  const int64_t base = (int64_t)rb * 128, col0 = (int64_t)cb * kCols;
+#pragma unroll
+  for (int q = threadIdx.x; q < kCols * 4; q += 256) {
+    const int c = q / 4, w = q % 4;
+    if (col0 + c < P.cols)
+      stg(reinterpret_cast<u32x4*>(P.codes_t + (col0 + c) * pitch + base / 2 + 16 * w),
+          *reinterpret_cast<const u32x4*>(lds + c * 64 + 16 * ((w + c / V) & 3)));
+  }
+#pragma unroll
+  for (int c = threadIdx.x; c < kCols; c += 256)
+    if (col0 + c < P.cols)
+      stg(reinterpret_cast<uint32_t*>(P.scales_t + (col0 + c) * spitch + base / kMx4Group),
+          *reinterpret_cast<const uint32_t*>(lds + kCols * 64 + c * 4));
 }
 
 struct Mx4DequantArgs {
@@ -651,6 +666,134 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
     output(std::true_type{});
   } else {
     output(std::false_type{});
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (M <= 16 MT): the weight-streaming form, bound by the bytes of B (or by
+// latency).  A workgroup takes 16 rows of B; its 8 waves split the columns and
+// add their partial sums through LDS in a fixed order.  Lane l holds, at each
+// 128-column step, columns 32 (l / 16) onwards of B's row l % 16 and of A's row
+// l % 16; A may be MX4 or still fp32 or bf16, then each wave quantises its part
+// of it beside B's loads, which saves a launch and A's way through memory.
+// ---------------------------------------------------------------------------
+enum { MX4_A_MX4 = 0, MX4_A_F32 = 1, MX4_A_BF16 = 2 };
+
+struct Mx4FewArgs {
+  Mx4ProductArgs p;
+  const void* x;  // A before quantisation
+  int64_t ldx, K;
+};
+
+__device__ __forceinline__ floatx4 mfma_mx4_16(const intx4& a, const intx4& b, const floatx4& c, int sa, int sb) {
+  const intx8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+}
+
+// 32 elements of a row (those from `left` on as zero) as codes and scale byte.
+template <bool BF16>
+__device__ __forceinline__ intx4 mx4_quantize32(const void* x, int64_t at, int64_t left, int* scale_byte) {
+  constexpr int V = Mx4Piece<BF16>::kElems, kPieces = 32 / V;
+  Mx4Piece<BF16> p[kPieces];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) p[i].load(x, at + i * V, left - i * V);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) top = max(top, p[i].top());
+  const uint32_t s = mx4_scale(top);
+  const float scale = mx4_scale_float(s);
+  intx4 c;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t w;
+    if constexpr (BF16) {
+      w = p[d].encode(scale);
+    } else {
+      w = (p[2 * d].encode(scale) & 0xffffu) | (p[2 * d + 1].encode(scale) << 16);
+    }
+    c[d] = s == 255 ? 0 : (int)w;
+  }
+  *scale_byte = (int)s;
+  return c;
+}
+
+template <int AM, int MT>
+__global__ void __launch_bounds__(512) mx4_few_rows_kernel(const Mx4FewArgs Q) {
+  const Mx4ProductArgs& P = Q.p;
+  constexpr int kWaves = 8;
+  __shared__ float part[kWaves][MT][16][17];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t brow = min(n0 + r16, P.N - 1) * P.padded;
+  const int steps = (int)(P.padded / 128);
+  const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
+  floatx4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // BATCH steps, B's loads first
+  auto batch = [&](int s, auto BATCH) __attribute__((always_inline)) {
+    constexpr int kBatch = decltype(BATCH)::value;
+    intx4 b[kBatch];
+    int sb[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t at = brow + (int64_t)(s + u) * 128 + 32 * g;
+      b[u] = ldg(reinterpret_cast<const intx4*>(P.b + at / 2));
+      sb[u] = ldg(P.bs + at / kMx4Group);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t k = (int64_t)(s + u) * 128 + 32 * g;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int64_t m = 16 * t + r16;
+        intx4 a;
+        int sa;
+        if constexpr (AM == MX4_A_MX4) {
+          const int64_t at = min(m, P.M - 1) * P.padded + k;
+          a = ldg(reinterpret_cast<const intx4*>(P.a + at / 2));
+          sa = ldg(P.as + at / kMx4Group);
+        } else {
+          a = mx4_quantize32<AM == MX4_A_BF16>(Q.x, m * Q.ldx + k, m < P.M ? Q.K - k : 0, &sa);
+        }
+        acc[t] = mfma_mx4_16(b[u], a, acc[t], sb[u], sa);
+      }
+    }
+  };
+  int s = s0;
+  for (; s + 4 <= s1; s += 4) batch(s, std::integral_constant<int, 4>{});
+  if (s + 2 <= s1) {
+    batch(s, std::integral_constant<int, 2>{});
+    s += 2;
+  }
+  if (s < s1) batch(s, std::integral_constant<int, 1>{});
+  // Lane l has columns n0 + 4 g ... of C's row l % 16.
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][t][r16][4 * g + e] = acc[t][e];
+  __syncthreads();
+#pragma unroll
+  for (int q = threadIdx.x; q < MT * 256; q += 512) {
+    const int t = q / 256, row = (q / 16) % 16, col = q % 16;
+    const int64_t m = 16 * t + row, n = n0 + col;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += part[w][t][row][col];
+    if (m >= P.M || n >= P.N) continue;
+    v *= P.alpha;
+    const int64_t at = m * P.ldc + n;
+    if (P.bf16) {
+      uint16_t* const c = static_cast<uint16_t*>(P.c) + at;
+      if (P.beta != 0.f) v += P.beta * __builtin_bit_cast(float, (uint32_t)ldg(c) << 16);
+      stg(c, f32_to_bf16_bits(v));
+    } else {
+      float* const c = static_cast<float*>(P.c) + at;
+      if (P.beta != 0.f) v += P.beta * ldg(c);
+      stg(c, v);
+    }
   }
 }
 

@@ -97,9 +97,30 @@ int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
   return check_launch();
 }
 
+constexpr int64_t kFewRows = 32;       // most rows of A that the weight-streaming form takes
+constexpr int64_t kFewRowsToQuantise = 16;  // and that it quantises by itself
+
+template <int AM>
+int few_rows(const Mx4FewArgs& a, hipStream_t stream) {
+  const int64_t blocks = (a.p.N + 15) / 16;
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  const dim3 grid((uint32_t)blocks), block(512);
+  if (a.p.M <= 16) {
+    hipLaunchKernelGGL((mx4_few_rows_kernel<AM, 1>), grid, block, 0, stream, a);
+  } else {
+    if constexpr (AM == MX4_A_MX4) hipLaunchKernelGGL((mx4_few_rows_kernel<AM, 2>), grid, block, 0, stream, a);
+  }
+  return check_launch();
+}
+
 // Tile edge: the largest of 256, 128 and 64 whose grid still occupies most of
 // the 256 compute units.
 int product(const Mx4ProductArgs& a, hipStream_t stream) {
+  if (a.M <= kFewRows) {
+    Mx4FewArgs f = {};
+    f.p = a;
+    return few_rows<MX4_A_MX4>(f, stream);
+  }
   auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
   if (tiles(256) >= 192) return product_tiles<4, 8>(a, stream);
   if (tiles(128) >= 192) return product_tiles<2, 4>(a, stream);
@@ -197,6 +218,7 @@ int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const u
 
 size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (check_sides(M, N, K) != SHAMPOO_OK) return 0;
+  if (M <= kFewRowsToQuantise) return 0;
   const size_t elems = (size_t)M * (size_t)mx4_padded(K);
   return align_up(elems / 2) + align_up(elems / kMx4Group) + shampoo_mx4_workspace_bytes(M, N, K);
 }
@@ -214,6 +236,22 @@ int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const
   const size_t need = shampoo_mx4_linear_workspace_bytes(M, N, K);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
   if (!aligned16(ws)) return SHAMPOO_EINVAL;
+  if (M <= kFewRowsToQuantise) {
+    Mx4FewArgs f = {};
+    f.p.b = w_codes;
+    f.p.bs = w_scales;
+    f.p.M = M;
+    f.p.N = N;
+    f.p.padded = mx4_padded(K);
+    f.p.c = y;
+    f.p.ldc = ldy;
+    f.p.alpha = 1.f;
+    f.p.bf16 = dtype == SHAMPOO_T_BF16;
+    f.x = x;
+    f.ldx = ldx;
+    f.K = K;
+    return dtype == SHAMPOO_T_BF16 ? few_rows<MX4_A_BF16>(f, stream) : few_rows<MX4_A_F32>(f, stream);
+  }
   const size_t elems = (size_t)M * (size_t)mx4_padded(K);
   uint8_t* codes = static_cast<uint8_t*>(ws);
   uint8_t* scales = codes + align_up(elems / 2);

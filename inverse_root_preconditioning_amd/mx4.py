@@ -14,7 +14,7 @@ import math
 import torch
 
 from . import capi
-from .adamw import _TYPES, _on
+from .adamw import _TYPES, _on_stream, _raw_stream
 
 
 def _padded(k):
@@ -23,16 +23,22 @@ def _padded(k):
 
 def _matrix(t, name):
     """t as (type, row stride); rows contiguous."""
-    if not t.is_cuda or t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None or not t.is_cuda:
         raise ValueError(f"{name} must be a float32 or bfloat16 CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    if t.is_contiguous():
+        return code, cols
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
+    if rows <= 1:
+        return code, cols
+    if ld < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return _TYPES[t.dtype], ld
+    return code, ld
 
 
 class MX4Matrix:
@@ -40,7 +46,7 @@ class MX4Matrix:
     values a byte; scales: uint8 [rows, padded / 32]; padded: cols rounded up
     to a multiple of 128."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("_buf", "_codes", "_scales", "codes_ptr", "scales_ptr", "rows", "cols", "device")
 
     def __init__(self, codes, scales, rows, cols):
         k = _padded(cols)
@@ -53,117 +59,135 @@ class MX4Matrix:
                 raise ValueError(f"{name} must be 16-byte aligned")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on one device")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self._buf, self._codes, self._scales = None, codes, scales
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self.rows, self.cols, self.device = rows, cols, codes.device
 
     @classmethod
-    def empty(cls, rows, cols, device):
-        """Uninitialised storage."""
-        k = _padded(cols)
+    def empty(cls, rows, cols, like):
+        """Uninitialised storage on the device of the tensor `like`: one buffer, scales after codes."""
         m = cls.__new__(cls)
-        m.codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
-        m.scales = torch.empty((rows, k // capi.GROUP), dtype=torch.uint8, device=device)
-        m.rows, m.cols = rows, cols
+        n = rows * _padded(cols) // 2             # a multiple of 64
+        m._buf = like.new_empty(n + n // 16, dtype=torch.uint8)
+        m._codes = m._scales = None
+        m.codes_ptr = m._buf.data_ptr()
+        m.scales_ptr = m.codes_ptr + n
+        m.rows, m.cols, m.device = rows, cols, like.device
         return m
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        if self._codes is None:
+            n = self.rows * _padded(self.cols) // 2
+            self._codes = self._buf[:n].view(self.rows, -1 if n else 0)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            n = self.rows * _padded(self.cols) // 2
+            self._scales = self._buf[n:].view(self.rows, -1 if n else 0)
+        return self._scales
 
     @property
     def shape(self):
         return (self.rows, self.cols)
 
 
-def _quantize(x, along_rows, along_cols, stream):
+def _quantize(x, along_rows, along_cols):
     if x.dim() == 2 and x.stride(1) != 1 and x.stride(0) == 1 and x.shape[1] > 1:
-        qt, q = _quantize(x.t(), along_cols, along_rows, stream)
+        qt, q = _quantize(x.t(), along_cols, along_rows)
         return q, qt
     dtype, ld = _matrix(x, "x")
     rows, cols = x.shape
-    with _on(stream):
-        q = MX4Matrix.empty(rows, cols, x.device) if along_rows else None
-        qt = MX4Matrix.empty(cols, rows, x.device) if along_cols else None
-        capi.check(capi.shampoo_mx4_quantize(
-            x.data_ptr(), dtype, rows, cols, ld, q.codes.data_ptr() if q else 0, q.scales.data_ptr() if q else 0,
-            qt.codes.data_ptr() if qt else 0, qt.scales.data_ptr() if qt else 0,
-            torch.cuda.current_stream(x.device).cuda_stream), "shampoo_mx4_quantize")
+    q = MX4Matrix.empty(rows, cols, x) if along_rows else None
+    qt = MX4Matrix.empty(cols, rows, x) if along_cols else None
+    capi.check(capi.shampoo_mx4_quantize(
+        x.data_ptr(), dtype, rows, cols, ld, q.codes_ptr if q else 0, q.scales_ptr if q else 0,
+        qt.codes_ptr if qt else 0, qt.scales_ptr if qt else 0, _raw_stream(x.device.index)), "shampoo_mx4_quantize")
     return q, qt
 
 
-def quantize(x, stream=None):
+@_on_stream
+def quantize(x):
     """x [rows, cols] (or a transposed view of such a matrix) as MX4, 32
     consecutive columns sharing a scale."""
-    return _quantize(x, True, False, stream)[0]
+    return _quantize(x, True, False)[0]
 
 
-def quantize_both(x, stream=None):
+@_on_stream
+def quantize_both(x):
     """(quantize(x), quantize(x.t())) from one reading of x."""
-    return _quantize(x, True, True, stream)
+    return _quantize(x, True, True)
 
 
-def dequantize(q, dtype=torch.float32, stream=None):
+@_on_stream
+def dequantize(q, dtype=torch.float32):
     """The values of q."""
     if dtype not in _TYPES:
         raise ValueError("dtype must be float32 or bfloat16")
-    with _on(stream):
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
-        capi.check(capi.shampoo_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, out.data_ptr(),
-                                               _TYPES[dtype], q.cols,
-                                               torch.cuda.current_stream(out.device).cuda_stream),
-                   "shampoo_mx4_dequantize")
+    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
+    capi.check(capi.shampoo_mx4_dequantize(q.codes_ptr, q.scales_ptr, q.rows, q.cols, out.data_ptr(), _TYPES[dtype],
+                                           q.cols, _raw_stream(q.device.index)), "shampoo_mx4_dequantize")
     return out
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _workspace(need, like):
+    """Scratch memory (kept alive by the caller's frame) and its address."""
+    if need == 0:
+        return None, 0
+    ws = like.new_empty(need, dtype=torch.uint8)
+    return ws, ws.data_ptr()
 
 
-def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=None):
+@_on_stream
+def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0):
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     if a.device != b.device or (out is not None and out.device != a.device):
         raise ValueError("the operands are on one device")
-    with _on(stream):
-        if out is None:
-            if beta != 0.0:
-                raise ValueError("beta needs out")
-            if dtype not in _TYPES:
-                raise ValueError("dtype must be float32 or bfloat16")
-            out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
-        ctype, ld = _matrix(out, "out")
-        if tuple(out.shape) != (a.rows, b.rows):
-            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(a.rows, b.rows)}")
-        need = capi.shampoo_mx4_workspace_bytes(a.rows, b.rows, a.cols)
-        ws = _workspace(need, a.device) if need else None
-        capi.check(capi.shampoo_mx4_product(
-            a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), a.rows, b.rows, a.cols,
-            alpha, beta, out.data_ptr(), ctype, ld, ws.data_ptr() if need else 0, need,
-            torch.cuda.current_stream(a.device).cuda_stream), "shampoo_mx4_product")
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta needs out")
+        if dtype not in _TYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
+    ctype, ld = _matrix(out, "out")
+    if tuple(out.shape) != (a.rows, b.rows):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(a.rows, b.rows)}")
+    need = capi.shampoo_mx4_workspace_bytes(a.rows, b.rows, a.cols)
+    ws, ws_ptr = _workspace(need, out)
+    capi.check(capi.shampoo_mx4_product(a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, a.rows, b.rows, a.cols,
+                                        alpha, beta, out.data_ptr(), ctype, ld, ws_ptr, need,
+                                        _raw_stream(a.device.index)), "shampoo_mx4_product")
     return out
 
 
-def linear(x, w, out=None, stream=None):
+@_on_stream
+def linear(x, w, out=None):
     """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type."""
-    if x.shape[-1] != w.cols:
-        raise ValueError(f"x has {x.shape[-1]} columns, w {w.cols}")
+    shape = x.shape
+    if shape[-1] != w.cols:
+        raise ValueError(f"x has {shape[-1]} columns, w {w.cols}")
     if x.device != w.device or (out is not None and out.device != w.device):
         raise ValueError("the operands are on one device")
-    rows = math.prod(x.shape[:-1])
-    flat = x if x.dim() == 2 else x.view(rows, w.cols)
+    rows = math.prod(shape[:-1])
+    flat = x if len(shape) == 2 else x.view(rows, w.cols)
     xtype, ldx = _matrix(flat, "x")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((*x.shape[:-1], w.rows), dtype=x.dtype, device=x.device)
-        elif tuple(out.shape) != (*x.shape[:-1], w.rows) or out.dtype != x.dtype:
-            raise ValueError(f"out must have shape {(*x.shape[:-1], w.rows)} and x's type")
+    if out is None:
+        out = x.new_empty((*shape[:-1], w.rows))
+        ldy = w.rows
+    else:
+        if tuple(out.shape) != (*shape[:-1], w.rows) or out.dtype != x.dtype:
+            raise ValueError(f"out must have shape {(*shape[:-1], w.rows)} and x's type")
         _, ldy = _matrix(out if out.dim() == 2 else out.view(rows, w.rows), "out")
-        need = capi.shampoo_mx4_linear_workspace_bytes(rows, w.rows, w.cols)
-        ws = _workspace(need, x.device)
-        capi.check(capi.shampoo_mx4_linear(
-            flat.data_ptr(), ldx, w.codes.data_ptr(), w.scales.data_ptr(), rows, w.rows, w.cols, out.data_ptr(), ldy,
-            xtype, ws.data_ptr(), need, torch.cuda.current_stream(x.device).cuda_stream), "shampoo_mx4_linear")
+    need = capi.shampoo_mx4_linear_workspace_bytes(rows, w.rows, w.cols)
+    ws, ws_ptr = _workspace(need, x)
+    capi.check(capi.shampoo_mx4_linear(flat.data_ptr(), ldx, w.codes_ptr, w.scales_ptr, rows, w.rows, w.cols,
+                                       out.data_ptr(), ldy, xtype, ws_ptr, need, _raw_stream(x.device.index)),
+               "shampoo_mx4_linear")
     return out
 
 
@@ -176,8 +200,8 @@ class _TrainLinear(torch.autograd.Function):
     def forward(ctx, x, w):
         need_x, need_w = ctx.needs_input_grad
         flat = _flat(x.detach())
-        xq, xt = _quantize(flat, True, need_w, None)
-        wq, wt = _quantize(w.detach(), True, need_x, None)
+        xq, xt = _quantize(flat, True, need_w)
+        wq, wt = _quantize(w.detach(), True, need_x)
         ctx.xt, ctx.wt = xt, wt
         ctx.types = x.dtype, w.dtype
         ctx.shape = x.shape
@@ -186,7 +210,7 @@ class _TrainLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad
-        q, qt = _quantize(_flat(dy), need_x, need_w, None)
+        q, qt = _quantize(_flat(dy), need_x, need_w)
         dx = product(q, ctx.wt, dtype=ctx.types[0]).view(ctx.shape) if need_x else None
         dw = product(qt, ctx.xt, dtype=ctx.types[1]) if need_w else None
         return dx, dw
