@@ -330,6 +330,9 @@ struct Mx4ProductArgs {
   float alpha, beta;
   int bf16;
   uint32_t tiles_m, tiles_n;
+  // Columns are split over blockIdx.y, split_blocks blocks of 1024 to each; with
+  // more than one split C holds one [M][N] partial product after the other.
+  int split_blocks;
 };
 
 // acc += A B^T over 64 columns for a 32 x 32 block.  Lane l of a wave holds 32
@@ -455,10 +458,10 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   const int r32 = lane & 31, h = lane >> 5;
 
   const uint32_t pitch = (uint32_t)(P.padded / 2), spitch = (uint32_t)(P.padded / kMx4Group);
-  const uint8_t* const A = P.a + m0 * pitch;
-  const uint8_t* const B = P.b + n0 * pitch;
-  const uint8_t* const As = P.as + m0 * spitch;
-  const uint8_t* const Bs = P.bs + n0 * spitch;
+  const uint8_t* const A = P.a + m0 * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
+  const uint8_t* const B = P.b + n0 * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
+  const uint8_t* const As = P.as + m0 * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
+  const uint8_t* const Bs = P.bs + n0 * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
   const int ma = (int)min<int64_t>(BT, P.M - m0) - 1, nb = (int)min<int64_t>(BT, P.N - n0) - 1;  // last valid rows
 
   // Piece c of an operand's chunk: row c / 8, permuted 16-byte column c % 8.
@@ -470,8 +473,9 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
     offA[it] = (uint32_t)min(row, ma) * pitch + 16 * ((c & 7) ^ mx4_swz_a(row));
     offB[it] = (uint32_t)min(row, nb) * pitch + 16 * ((c & 7) ^ mx4_swz_b(row));
   }
-  const int steps = (int)(P.padded / 128);  // 128-column halves of chunks
-  const int full = steps / 2;               // whole chunks
+  // This split's 128-column halves of chunks, and its whole chunks.
+  const int steps = min((int)(P.padded / 128) - (int)blockIdx.y * P.split_blocks * 8, P.split_blocks * 8);
+  const int full = steps / 2;
   auto issue_a = [&](int buf, int chunk) __attribute__((always_inline)) {
     const uint8_t* const a = A + (int64_t)chunk * kMx4RowBytes;
 #pragma unroll
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   // Quarter q of scale block blk: 32 T rows of A (q = 0, 1) or B.  Dword p of a
   // row goes to place p ^ 2 ((row / 8) % 4), so that the rows of a read, 8
   // dwords apart, spread over the banks.
-  const int last = (int)(spitch / 4) - 1;
+  const int last = steps - 1;
   auto issue_scales = [&](int blk, int q) __attribute__((always_inline)) {
     const uint8_t* const from = q < 2 ? As : Bs;
     const int limit = q < 2 ? ma : nb;
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
 #pragma unroll
         for (int r = 0; r < 32; r += kRows) {
           const int row = r + lane / kLanes;
-          mx4_store4<BF16, BETA, true>(P, m0 + wm + 32 * i + row, n,
+          mx4_store4<BF16, BETA, true>(P, blockIdx.y * P.M + m0 + wm + 32 * i + row, n,
                                        *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
         }
       } else {
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
           const int row = r + lane / kLanes;
           const int64_t m = m0 + wm + 32 * i + row;
           if (m < P.M && n < P.N)
-            mx4_store4<BF16, BETA, false>(P, m, n, *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
+            mx4_store4<BF16, BETA, false>(P, blockIdx.y * P.M + m, n, *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
         }
       }
     }
@@ -670,14 +674,18 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 16 MT): the weight-streaming form, bound by the bytes of B (or by
-// latency).  A workgroup takes 16 rows of B; its 8 waves split the columns and
-// add their partial sums through LDS in a fixed order.  Lane l holds, at each
-// 128-column step, columns 32 (l / 16) onwards of B's row l % 16 and of A's row
-// l % 16; A may be MX4 or still fp32 or bf16, then each wave quantises its part
-// of it beside B's loads, which saves a launch and A's way through memory.
+// Few rows (M <= 16): the weight-streaming form, bound by the bytes of B (or by
+// latency).  A workgroup takes 16 NT rows of B; its 4 waves split the columns
+// and add their partial sums through LDS in a fixed order.  Lane l holds, at
+// each 128-column step, columns 32 (l / 16) onwards of B's row l % 16 and of A's
+// row l % 16.  A wave works in batches of BATCH steps, whose scales are one load
+// of 4 BATCH bytes a row: read byte by byte they cost as many cache lines as
+// the codes.  A may still be fp32 or bf16 (at most kMx4FewElems elements): then
+// the workgroup quantises it into LDS while its first rows of B are on their
+// way, which saves a launch and A's way through memory.
 // ---------------------------------------------------------------------------
 enum { MX4_A_MX4 = 0, MX4_A_F32 = 1, MX4_A_BF16 = 2 };
+constexpr int kMx4FewElems = 16384;
 
 struct Mx4FewArgs {
   Mx4ProductArgs p;
@@ -690,99 +698,123 @@ __device__ __forceinline__ floatx4 mfma_mx4_16(const intx4& a, const intx4& b, c
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
 }
 
-// 32 elements of a row (those from `left` on as zero) as codes and scale byte.
-template <bool BF16>
-__device__ __forceinline__ intx4 mx4_quantize32(const void* x, int64_t at, int64_t left, int* scale_byte) {
-  constexpr int V = Mx4Piece<BF16>::kElems, kPieces = 32 / V;
-  Mx4Piece<BF16> p[kPieces];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) p[i].load(x, at + i * V, left - i * V);
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) top = max(top, p[i].top());
-  const uint32_t s = mx4_scale(top);
-  const float scale = mx4_scale_float(s);
-  intx4 c;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    uint32_t w;
-    if constexpr (BF16) {
-      w = p[d].encode(scale);
-    } else {
-      w = (p[2 * d].encode(scale) & 0xffffu) | (p[2 * d + 1].encode(scale) << 16);
-    }
-    c[d] = s == 255 ? 0 : (int)w;
-  }
-  *scale_byte = (int)s;
-  return c;
-}
-
-template <int AM, int MT>
-__global__ void __launch_bounds__(512) mx4_few_rows_kernel(const Mx4FewArgs Q) {
+template <int AM, int NT, int BATCH>
+__global__ void __launch_bounds__(256) mx4_few_rows_kernel(const Mx4FewArgs Q) {
+  typedef uint32_t Scales __attribute__((ext_vector_type(BATCH)));
   const Mx4ProductArgs& P = Q.p;
-  constexpr int kWaves = 8;
-  __shared__ float part[kWaves][MT][16][17];
+  constexpr int W = 4;
+  __shared__ float part[W][16][16 * NT + 1];
+  __shared__ __attribute__((aligned(16))) uint8_t qa[AM == MX4_A_MX4 ? 16 : kMx4FewElems / 2 + kMx4FewElems / kMx4Group];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t brow = min(n0 + r16, P.N - 1) * P.padded;
-  const int steps = (int)(P.padded / 128);
-  const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
-  floatx4 acc[MT];
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+  // The wave's steps: whole batches but for the matrix's last steps.
+  const int steps = (int)(P.padded / 128), batches = (steps + BATCH - 1) / BATCH;
+  const int s0 = batches * wave / W * BATCH, s1 = min(batches * (wave + 1) / W * BATCH, steps);
+  int64_t brow[NT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  // BATCH steps, B's loads first
-  auto batch = [&](int s, auto BATCH) __attribute__((always_inline)) {
-    constexpr int kBatch = decltype(BATCH)::value;
-    intx4 b[kBatch];
-    int sb[kBatch];
+  for (int j = 0; j < NT; ++j) brow[j] = min(n0 + 16 * j + r16, P.N - 1) * P.padded;
+  const int64_t arow = min<int64_t>(r16, P.M - 1) * P.padded;
+  floatx4 acc[NT];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t at = brow + (int64_t)(s + u) * 128 + 32 * g;
-      b[u] = ldg(reinterpret_cast<const intx4*>(P.b + at / 2));
-      sb[u] = ldg(P.bs + at / kMx4Group);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+  for (int j = 0; j < NT; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  intx4 b[BATCH][NT], a[BATCH];
+  Scales sb[NT], sa;
+  auto load_whole = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < BATCH; ++u) {
       const int64_t k = (int64_t)(s + u) * 128 + 32 * g;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int64_t m = 16 * t + r16;
-        intx4 a;
-        int sa;
-        if constexpr (AM == MX4_A_MX4) {
-          const int64_t at = min(m, P.M - 1) * P.padded + k;
-          a = ldg(reinterpret_cast<const intx4*>(P.a + at / 2));
-          sa = ldg(P.as + at / kMx4Group);
-        } else {
-          a = mx4_quantize32<AM == MX4_A_BF16>(Q.x, m * Q.ldx + k, m < P.M ? Q.K - k : 0, &sa);
-        }
-        acc[t] = mfma_mx4_16(b[u], a, acc[t], sb[u], sa);
-      }
+      for (int j = 0; j < NT; ++j) b[u][j] = ldg(reinterpret_cast<const intx4*>(P.b + (brow[j] + k) / 2));
+      if constexpr (AM == MX4_A_MX4) a[u] = ldg(reinterpret_cast<const intx4*>(P.a + (arow + k) / 2));
     }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sb[j] = ldg_any<Scales, 4>(P.bs + (brow[j] + s * 128) / kMx4Group);
+    if constexpr (AM == MX4_A_MX4) sa = ldg_any<Scales, 4>(P.as + (arow + s * 128) / kMx4Group);
   };
-  int s = s0;
-  for (; s + 4 <= s1; s += 4) batch(s, std::integral_constant<int, 4>{});
-  if (s + 2 <= s1) {
-    batch(s, std::integral_constant<int, 2>{});
-    s += 2;
+  auto multiply = [&](int s, int u, const intx4& av, uint32_t sav, const intx4 (&bv)[NT], const uint32_t (&sbv)[NT])
+      __attribute__((always_inline)) {
+    intx4 x = av;
+    uint32_t sx = sav >> (8 * g);
+    if constexpr (AM != MX4_A_MX4) {
+      const int at = min(r16, (int)P.M - 1) * (int)P.padded + (s + u) * 128 + 32 * g;
+      x = *reinterpret_cast<const intx4*>(qa + at / 2);
+      sx = qa[kMx4FewElems / 2 + at / kMx4Group];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = mfma_mx4_16(bv[j], x, acc[j], (int)(sbv[j] >> (8 * g)), (int)sx);
+  };
+
+  const bool first = s0 + BATCH <= s1;
+  if (first) load_whole(s0);
+  if constexpr (AM != MX4_A_MX4) {
+    // 8 elements a lane, 4 lanes a group
+    constexpr bool kBf16 = AM == MX4_A_BF16;
+    constexpr int kPieces = 8 / Mx4Piece<kBf16>::kElems;
+    const int per_row = (int)(P.padded / 8), pieces = (int)P.M * per_row;
+    for (int q = threadIdx.x; q < pieces; q += 256) {
+      const int row = q / per_row, k = (q - row * per_row) * 8;
+      Mx4Piece<kBf16> x[kPieces];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = k + i * Mx4Piece<kBf16>::kElems;
+        x[i].load(Q.x, row * Q.ldx + c, Q.K - c);
+        top = max(top, x[i].top());
+      }
+      const uint32_t s = mx4_scale(group_max<4>(top));
+      const float scale = mx4_scale_float(s);
+      uint32_t c = x[0].encode(scale);
+      if constexpr (kPieces == 2) c = (c & 0xffffu) | (x[1].encode(scale) << 16);
+      *reinterpret_cast<uint32_t*>(qa + 4 * q) = s == 255 ? 0u : c;
+      if ((q & 3) == 0) qa[kMx4FewElems / 2 + q / 4] = (uint8_t)s;
+    }
+    __syncthreads();
   }
-  if (s < s1) batch(s, std::integral_constant<int, 1>{});
-  // Lane l has columns n0 + 4 g ... of C's row l % 16.
+  int s = s0;
+  if (first) {
+    for (;;) {
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+      for (int u = 0; u < BATCH; ++u) {
+        uint32_t t[NT];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][t][r16][4 * g + e] = acc[t][e];
+        for (int j = 0; j < NT; ++j) t[j] = sb[j][u];
+        multiply(s, u, a[u], sa[u], b[u], t);
+      }
+      s += BATCH;
+      if (s + BATCH > s1) break;
+      load_whole(s);
+    }
+  }
+  for (; s < s1; ++s) {  // fewer than BATCH steps at the end of the matrix
+    const int64_t k = (int64_t)s * 128;
+    intx4 bv[NT], av = {0, 0, 0, 0};
+    uint32_t t[NT], ta = 0;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      bv[j] = ldg(reinterpret_cast<const intx4*>(P.b + (brow[j] + k + 32 * g) / 2));
+      t[j] = ldg(reinterpret_cast<const uint32_t*>(P.bs + (brow[j] + k) / kMx4Group));
+    }
+    if constexpr (AM == MX4_A_MX4) {
+      av = ldg(reinterpret_cast<const intx4*>(P.a + (arow + k + 32 * g) / 2));
+      ta = ldg(reinterpret_cast<const uint32_t*>(P.as + (arow + k) / kMx4Group));
+    }
+    multiply(s, 0, av, ta, bv, t);
+  }
+  // Lane l has columns n0 + 16 j + 4 g ... of C's row l % 16.
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][r16][16 * j + 4 * g + e] = acc[j][e];
   __syncthreads();
-#pragma unroll
-  for (int q = threadIdx.x; q < MT * 256; q += 512) {
-    const int t = q / 256, row = (q / 16) % 16, col = q % 16;
-    const int64_t m = 16 * t + row, n = n0 + col;
+  for (int q = threadIdx.x; q < NT * 256; q += 256) {
+    const int col = q % (16 * NT);
+    const int64_t m = q / (16 * NT), n = n0 + col;
+    if (m >= P.M || n >= P.N) continue;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w][t][row][col];
-    if (m >= P.M || n >= P.N) continue;
+    for (int w = 0; w < W; ++w) v += part[w][m][col];
     v *= P.alpha;
     const int64_t at = m * P.ldc + n;
     if (P.bf16) {
@@ -794,6 +826,34 @@ __global__ void __launch_bounds__(512) mx4_few_rows_kernel(const Mx4FewArgs Q) {
       if (P.beta != 0.f) v += P.beta * ldg(c);
       stg(c, v);
     }
+  }
+}
+
+// C = alpha sum + beta C over the partial products of a split, in their order.
+struct Mx4SumArgs {
+  Mx4ProductArgs p;
+  const float* parts;  // [splits][M][N]
+  int splits;
+};
+
+__global__ void __launch_bounds__(256) mx4_sum_kernel(const Mx4SumArgs Q) {
+  const Mx4ProductArgs& P = Q.p;
+  const uint32_t total = (uint32_t)(P.M * P.N), id = blockIdx.x * 256 + threadIdx.x;  // a split is of small C only
+  if (id >= total) return;
+  float v = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < Q.splits; ++s) v += ldg(Q.parts + (int64_t)s * total + id);
+  v *= P.alpha;
+  const uint32_t m = id / (uint32_t)P.N;
+  const int64_t at = m * P.ldc + (id - m * (uint32_t)P.N);
+  if (P.bf16) {
+    uint16_t* const c = static_cast<uint16_t*>(P.c) + at;
+    if (P.beta != 0.f) v += P.beta * __builtin_bit_cast(float, (uint32_t)ldg(c) << 16);
+    stg(c, f32_to_bf16_bits(v));
+  } else {
+    float* const c = static_cast<float*>(P.c) + at;
+    if (P.beta != 0.f) v += P.beta * ldg(c);
+    stg(c, v);
   }
 }
 

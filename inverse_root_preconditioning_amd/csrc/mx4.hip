@@ -1,6 +1,7 @@
 // C entry points of the MX4 quantisation and products (gfx950): arguments are
 // checked on the host, kernels enqueued on the caller's stream; nothing is
 // allocated and nothing synchronises.
+#include <algorithm>
 #include <cmath>
 
 #include "kernels_mx4.h"
@@ -78,12 +79,12 @@ int quantize(Mx4QuantArgs a, bool bf16, hipStream_t stream) {
 }
 
 template <int T, int W>
-int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
+int product_tiles(Mx4ProductArgs a, int splits, hipStream_t stream) {
   const int64_t tm = (a.M + 64 * T - 1) / (64 * T), tn = (a.N + 64 * T - 1) / (64 * T);
   if (tm * tn > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
   a.tiles_m = (uint32_t)tm;
   a.tiles_n = (uint32_t)tn;
-  const dim3 grid((uint32_t)(tm * tn)), block(64 * W);
+  const dim3 grid((uint32_t)(tm * tn), (uint32_t)splits), block(64 * W);
   const bool beta = a.beta != 0.f;
   if (a.bf16 && beta) {
     hipLaunchKernelGGL((mx4_product_kernel<T, W, true, true>), grid, block, 0, stream, a);
@@ -97,34 +98,71 @@ int product_tiles(Mx4ProductArgs a, hipStream_t stream) {
   return check_launch();
 }
 
-constexpr int64_t kFewRows = 32;       // most rows of A that the weight-streaming form takes
-constexpr int64_t kFewRowsToQuantise = 16;  // and that it quantises by itself
+constexpr int64_t kFewRows = 16;  // most rows of A that the weight-streaming form takes
 
+// Whether that form also quantises A.
+bool few_quantise(int64_t M, int64_t K) { return M <= kFewRows && M * mx4_padded(K) <= kMx4FewElems; }
+
+template <int AM, int NT, int BATCH>
+int few_rows_launch(const Mx4FewArgs& a, hipStream_t stream) {
+  const int64_t blocks = (a.p.N + 16 * NT - 1) / (16 * NT);
+  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
+  hipLaunchKernelGGL((mx4_few_rows_kernel<AM, NT, BATCH>), dim3((uint32_t)blocks), dim3(256), 0, stream, a);
+  return check_launch();
+}
+
+// 32 rows of B a workgroup where that still leaves one for every compute unit
+// and A has more than a row or two to read for each of them; batches of 4
+// steps unless that would leave waves without any.
 template <int AM>
 int few_rows(const Mx4FewArgs& a, hipStream_t stream) {
-  const int64_t blocks = (a.p.N + 15) / 16;
-  if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
-  const dim3 grid((uint32_t)blocks), block(512);
-  if (a.p.M <= 16) {
-    hipLaunchKernelGGL((mx4_few_rows_kernel<AM, 1>), grid, block, 0, stream, a);
-  } else {
-    if constexpr (AM == MX4_A_MX4) hipLaunchKernelGGL((mx4_few_rows_kernel<AM, 2>), grid, block, 0, stream, a);
-  }
-  return check_launch();
+  const bool wide = a.p.M > 2 && a.p.N >= 32 * 256;
+  if (a.p.padded >= 4 * 4 * 128) return wide ? few_rows_launch<AM, 2, 4>(a, stream) : few_rows_launch<AM, 1, 4>(a, stream);
+  if (a.p.padded >= 4 * 2 * 128) return wide ? few_rows_launch<AM, 2, 2>(a, stream) : few_rows_launch<AM, 1, 2>(a, stream);
+  return wide ? few_rows_launch<AM, 2, 1>(a, stream) : few_rows_launch<AM, 1, 1>(a, stream);
+}
+
+int64_t tiles_of(int64_t M, int64_t N, int64_t edge) { return ((M + edge - 1) / edge) * ((N + edge - 1) / edge); }
+
+// Splits of the columns for a product on 64 x 64 tiles, and the 1024-column
+// blocks of each: as many as fill the 256 compute units, where the columns
+// saved (1.3 us a block) pay for adding up the parts (2.5 us).
+int split_columns(int64_t M, int64_t N, int64_t K, int* blocks_each) {
+  const int64_t blocks = (K + 1023) / 1024, tiles = tiles_of(M, N, 64);
+  *blocks_each = (int)blocks;
+  if (M <= kFewRows || blocks < 4 || tiles > 128) return 1;
+  const int64_t want = std::min<int64_t>(blocks, 256 / tiles);
+  *blocks_each = (int)((blocks + want - 1) / want);
+  return (int)((blocks + *blocks_each - 1) / *blocks_each);
 }
 
 // Tile edge: the largest of 256, 128 and 64 whose grid still occupies most of
 // the 256 compute units.
-int product(const Mx4ProductArgs& a, hipStream_t stream) {
+int product(Mx4ProductArgs a, int64_t K, void* ws, hipStream_t stream) {
   if (a.M <= kFewRows) {
     Mx4FewArgs f = {};
     f.p = a;
     return few_rows<MX4_A_MX4>(f, stream);
   }
-  auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
-  if (tiles(256) >= 192) return product_tiles<4, 8>(a, stream);
-  if (tiles(128) >= 192) return product_tiles<2, 4>(a, stream);
-  return product_tiles<1, 4>(a, stream);
+  const int splits = split_columns(a.M, a.N, K, &a.split_blocks);
+  if (splits > 1) {
+    Mx4SumArgs s;
+    s.p = a;
+    s.parts = static_cast<const float*>(ws);
+    s.splits = splits;
+    a.c = ws;
+    a.ldc = a.N;
+    a.alpha = 1.f;
+    a.beta = 0.f;
+    a.bf16 = 0;
+    const int rc = product_tiles<1, 4>(a, splits, stream);
+    if (rc != SHAMPOO_OK) return rc;
+    hipLaunchKernelGGL(mx4_sum_kernel, dim3((uint32_t)((a.M * a.N + 255) / 256)), dim3(256), 0, stream, s);
+    return check_launch();
+  }
+  if (tiles_of(a.M, a.N, 256) >= 192) return product_tiles<4, 8>(a, 1, stream);
+  if (tiles_of(a.M, a.N, 128) >= 192) return product_tiles<2, 4>(a, 1, stream);
+  return product_tiles<1, 4>(a, 1, stream);
 }
 
 }  // namespace
@@ -185,7 +223,12 @@ int shampoo_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
   return check_launch();
 }
 
-size_t shampoo_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
+size_t shampoo_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_sides(M, N, K) != SHAMPOO_OK || M == 0 || N == 0 || K > kMaxK) return 0;
+  int each;
+  const int splits = split_columns(M, N, K, &each);
+  return splits > 1 ? align_up((size_t)splits * M * N * sizeof(float)) : 0;
+}
 
 int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                         const uint8_t* b_scales, int64_t M, int64_t N, int64_t K, float alpha, float beta, void* c,
@@ -200,7 +243,8 @@ int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const u
     return SHAMPOO_EINVAL;
   const size_t need = shampoo_mx4_workspace_bytes(M, N, K);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
-  Mx4ProductArgs a;
+  if (need > 0 && !aligned16(ws)) return SHAMPOO_EINVAL;
+  Mx4ProductArgs a = {};
   a.a = a_codes;
   a.as = a_scales;
   a.b = b_codes;
@@ -213,12 +257,12 @@ int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const u
   a.alpha = alpha;
   a.beta = beta;
   a.bf16 = dtype == SHAMPOO_T_BF16;
-  return product(a, stream);
+  return product(a, K, ws, stream);
 }
 
 size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (check_sides(M, N, K) != SHAMPOO_OK) return 0;
-  if (M <= kFewRowsToQuantise) return 0;
+  if (few_quantise(M, K)) return 0;
   const size_t elems = (size_t)M * (size_t)mx4_padded(K);
   return align_up(elems / 2) + align_up(elems / kMx4Group) + shampoo_mx4_workspace_bytes(M, N, K);
 }
@@ -236,7 +280,7 @@ int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const
   const size_t need = shampoo_mx4_linear_workspace_bytes(M, N, K);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
   if (!aligned16(ws)) return SHAMPOO_EINVAL;
-  if (M <= kFewRowsToQuantise) {
+  if (few_quantise(M, K)) {
     Mx4FewArgs f = {};
     f.p.b = w_codes;
     f.p.bs = w_scales;

@@ -138,7 +138,8 @@ def _product_case(M, N, K, dtype, alpha, beta, key):
 
 PRODUCTS = [(1, 1, 1), (1, 17, 33), (16, 16, 128), (1, 1000, 2048), (7, 130, 300), (33, 65, 1000), (100, 100, 100),
             (128, 128, 512), (257, 255, 129), (300, 513, 1537), (512, 256, 4096), (1, 4096, 64), (2000, 3, 200),
-            (15, 2048, 8192), (40, 1024, 2048), (640, 768, 1024), (1030, 1027, 260)]
+            (15, 2048, 8192), (40, 1024, 2048), (640, 768, 1024), (1030, 1027, 260), (17, 64, 4096),
+            (100, 300, 5000), (64, 2048, 8192), (333, 129, 12345), (16, 8200, 1200), (3, 8192, 2049)]
 
 
 @pytest.mark.parametrize("dtype,alpha,beta", [("f32", 1.0, 0.0), ("bf16", 1.0, 0.0), ("f32", -0.5, 1.0),
