@@ -10,7 +10,10 @@ using namespace shp;
 namespace {
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
-constexpr int kNormBlocks = 2048;
+constexpr int kNormBlocks = 1024;
+// Up to here one workgroup does it all: beyond, one compute unit's reading
+// (16 KB a segment) takes longer than a second launch.
+constexpr int64_t kNormSmall = 64;
 
 int check_launch() { return hipGetLastError() == hipSuccess ? SHAMPOO_OK : SHAMPOO_EHIP; }
 
@@ -26,12 +29,29 @@ uint32_t step_key(uint64_t seed, int step) {
   return hash_finish(s + (uint32_t)step * kHashC1);
 }
 
+template <bool PARAM_BF16, bool GRAD_BF16, bool MX8>
+int launch_copy(const AdamwArgs& a, uint32_t grid, hipStream_t stream) {
+  if (a.copies != nullptr) {
+    if constexpr (!PARAM_BF16)
+      hipLaunchKernelGGL((adamw_kernel<false, GRAD_BF16, MX8, true>), dim3(grid), dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((adamw_kernel<PARAM_BF16, GRAD_BF16, MX8, false>), dim3(grid), dim3(256), 0, stream, a);
+  }
+  return check_launch();
+}
+
+template <bool PARAM_BF16, bool GRAD_BF16>
+int launch(const AdamwArgs& a, bool mx8, uint32_t grid, hipStream_t stream) {
+  return mx8 ? launch_copy<PARAM_BF16, GRAD_BF16, true>(a, grid, stream)
+             : launch_copy<PARAM_BF16, GRAD_BF16, false>(a, grid, stream);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments) {
-  if (nsegments <= 0) return 0;
+  if (nsegments <= kNormSmall) return 0;
   return (size_t)norm_blocks(nsegments) * sizeof(double);
 }
 
@@ -39,18 +59,30 @@ int shampoo_grad_norm(const shampoo_tensor* tensors, const shampoo_segment* segm
                       float max_norm, float* out, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (nsegments < 0 || !(max_norm > 0.f) || out == nullptr) return SHAMPOO_EINVAL;
   if (!valid_type(dtype)) return SHAMPOO_EUNSUPPORTED;
-  if (nsegments > 0) {
-    if (tensors == nullptr || segments == nullptr) return SHAMPOO_EINVAL;
-    if (ws == nullptr || ws_bytes < shampoo_grad_norm_workspace_bytes(nsegments)) return SHAMPOO_EWORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(ws) & 7) != 0) return SHAMPOO_EINVAL;
+  if (nsegments > 0 && (tensors == nullptr || segments == nullptr)) return SHAMPOO_EINVAL;
+  const bool bf16 = dtype == SHAMPOO_T_BF16;
+  if (nsegments <= kNormSmall) {
+    if (bf16) {
+      hipLaunchKernelGGL(grad_norm_small_kernel<true>, dim3(1), dim3(1024), 0, stream, tensors, segments,
+                         (int)nsegments, max_norm, out);
+    } else {
+      hipLaunchKernelGGL(grad_norm_small_kernel<false>, dim3(1), dim3(1024), 0, stream, tensors, segments,
+                         (int)nsegments, max_norm, out);
+    }
+    return check_launch();
   }
+  if (ws == nullptr || ws_bytes < shampoo_grad_norm_workspace_bytes(nsegments)) return SHAMPOO_EWORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 7) != 0) return SHAMPOO_EINVAL;
   const int blocks = norm_blocks(nsegments);
   double* partial = static_cast<double*>(ws);
-  if (blocks > 0) {
-    hipLaunchKernelGGL(grad_norm_partial_kernel, dim3(blocks), dim3(256), 0, stream, tensors, segments, nsegments,
-                       dtype == SHAMPOO_T_BF16, partial);
-    if (check_launch() != SHAMPOO_OK) return SHAMPOO_EHIP;
+  if (bf16) {
+    hipLaunchKernelGGL(grad_norm_partial_kernel<true>, dim3(blocks), dim3(256), 0, stream, tensors, segments,
+                       nsegments, partial);
+  } else {
+    hipLaunchKernelGGL(grad_norm_partial_kernel<false>, dim3(blocks), dim3(256), 0, stream, tensors, segments,
+                       nsegments, partial);
   }
+  if (check_launch() != SHAMPOO_OK) return SHAMPOO_EHIP;
   hipLaunchKernelGGL(grad_norm_final_kernel, dim3(1), dim3(256), 0, stream, partial, blocks, max_norm, out);
   return check_launch();
 }
@@ -95,11 +127,11 @@ int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, con
   a.rbc1 = (float)(1.0 / (1.0 - std::pow(beta1, step)));
   a.rsbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, step)));
   a.key = step_key(seed, step);
-  a.param_bf16 = param_dtype == SHAMPOO_T_BF16;
-  a.grad_bf16 = grad_dtype == SHAMPOO_T_BF16;
-  a.mx8 = mx8;
-  hipLaunchKernelGGL(adamw_kernel, dim3((uint32_t)nsegments), dim3(256), 0, stream, a);
-  return check_launch();
+  const bool gb = grad_dtype == SHAMPOO_T_BF16;
+  if (param_dtype == SHAMPOO_T_BF16) return gb ? launch<true, true>(a, mx8, (uint32_t)nsegments, stream)
+                                               : launch<true, false>(a, mx8, (uint32_t)nsegments, stream);
+  return gb ? launch<false, true>(a, mx8, (uint32_t)nsegments, stream)
+            : launch<false, false>(a, mx8, (uint32_t)nsegments, stream);
 }
 
 int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
@@ -109,15 +141,24 @@ int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_
   if ((m == nullptr) != (m_scale == nullptr) || (m == nullptr) != (m_out == nullptr)) return SHAMPOO_EINVAL;
   if ((v == nullptr) != (v_scale == nullptr) || (v == nullptr) != (v_out == nullptr)) return SHAMPOO_EINVAL;
   if (n == 0) return SHAMPOO_OK;
-  const int64_t blocks = (n + 255) / 256;
+  if (m == nullptr && v == nullptr) return SHAMPOO_EINVAL;
+  const int64_t blocks = (n + 2047) / 2048;
   if (blocks > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
-  const int bf16 = dtype == SHAMPOO_T_BF16;
-  if (m != nullptr)
-    hipLaunchKernelGGL(mx8_decode_kernel<MomentM>, dim3((uint32_t)blocks), dim3(256), 0, stream, m, m_scale, n, m_out,
-                       bf16);
-  if (v != nullptr)
-    hipLaunchKernelGGL(mx8_decode_kernel<MomentV>, dim3((uint32_t)blocks), dim3(256), 0, stream, v, v_scale, n, v_out,
-                       bf16);
+  MomentsArgs a;
+  a.codes[0] = m;
+  a.codes[1] = v;
+  a.scales[0] = m_scale;
+  a.scales[1] = v_scale;
+  a.out[0] = m_out;
+  a.out[1] = v_out;
+  a.n = n;
+  a.first = m == nullptr ? 1 : 0;
+  const dim3 grid((uint32_t)blocks, m != nullptr && v != nullptr ? 2 : 1);
+  if (dtype == SHAMPOO_T_BF16) {
+    hipLaunchKernelGGL(mx8_decode_kernel<true>, grid, dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL(mx8_decode_kernel<false>, grid, dim3(256), 0, stream, a);
+  }
   return check_launch();
 }
 

@@ -67,16 +67,67 @@ __device__ __forceinline__ float mx8_decode(uint32_t code, int s) {
   return v * (s == 255 ? __builtin_nanf("") : pow2_field(s));  // s >= 1; 0 stands only beside codes of 0
 }
 
-__device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
-  if (!bf16) return ldg(static_cast<const float*>(p) + i);
-  return __builtin_bit_cast(float, (uint32_t)ldg(static_cast<const uint16_t*>(p) + i) << 16);
+// V consecutive elements of a tensor as floats (WHOLE: all of them; else those
+// below `left`, the others 0), at any element's address.
+template <bool BF16, int V, bool WHOLE>
+__device__ __forceinline__ void load_elems(const void* p, int64_t at, int left, float (&x)[V]) {
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      x[e] = 0.f;
+      if (e < left) {
+        if constexpr (BF16) {
+          x[e] = __builtin_bit_cast(float, (uint32_t)ldg(static_cast<const uint16_t*>(p) + at + e) << 16);
+        } else {
+          x[e] = ldg(static_cast<const float*>(p) + at + e);
+        }
+      }
+    }
+  } else if constexpr (BF16) {
+    typedef uint32_t Words __attribute__((ext_vector_type(V / 2)));
+    const Words w = ldg_once<Words, 2>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      x[e] = __builtin_bit_cast(float, (e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
+  } else {
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) {
+      const floatx4 w = ldg_once<floatx4, 4>(static_cast<const float*>(p) + at + 4 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * q + e] = w[e];
+    }
+  }
 }
 
-__device__ __forceinline__ float group_max_abs_bits(float x, uint32_t& bits) {
-  bits = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+template <int V, bool WHOLE>
+__device__ __forceinline__ void store_f32(void* p, int64_t at, int left, const float (&x)[V]) {
+  float* const o = static_cast<float*>(p) + at;
+  if constexpr (WHOLE) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, off, kWave));
-  return x;
+    for (int q = 0; q < V / 4; ++q)
+      stg_once<floatx4, 4>(o + 4 * q, floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < left) stg(o + e, x[e]);
+  }
+}
+
+// Bits of V bf16 values, two a word.
+template <int V, bool WHOLE>
+__device__ __forceinline__ void store_bf16(void* p, int64_t at, int left, const uint32_t (&w)[V / 2]) {
+  typedef uint32_t Words __attribute__((ext_vector_type(V / 2)));
+  uint16_t* const o = static_cast<uint16_t*>(p) + at;
+  if constexpr (WHOLE) {
+    Words x;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) x[e] = w[e];
+    stg_once<Words, 2>(o, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < left) stg(o + e, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
+  }
 }
 
 struct AdamwArgs {
@@ -90,13 +141,21 @@ struct AdamwArgs {
   double omb1, omb2;                             // 1 - beta
   float lr, beta1, beta2, eps, rbc1, rsbc2;      // rbc1 = 1 / (1 - beta1^t), rsbc2 = 1 / sqrt(1 - beta2^t)
   uint32_t key;
-  int param_bf16, grad_bf16, mx8;
 };
 
+// One workgroup a segment, everything read and written once and past the
+// caches.  A lane takes 4 consecutive elements, or 8 where all but the 8-bit
+// moments are bf16 (16 bytes either way: 8 floats a lane would read half cache
+// lines).  The square root and the reciprocal are the hardware's (1 ulp): they
+// reach the parameter only, far below its rounding.  HBM-bound.
+template <bool PARAM_BF16, bool GRAD_BF16, bool MX8, bool COPY>
 __global__ void __launch_bounds__(256) adamw_kernel(const AdamwArgs P) {
 // Which operations are fused is written out: the codes that the moments round
 // to must not depend on the compiler's choice.
 #pragma clang fp contract(off)
+    constexpr int V = MX8 && PARAM_BF16 && GRAD_BF16 ? 8 : 4, kRounds = kSegment / (256 * V);
+  constexpr int kLanes = kGroup / V;
+  typedef uint32_t Codes __attribute__((ext_vector_type(V / 4)));
   const shampoo_segment seg = P.segments[blockIdx.x];
   if ((uint64_t)seg.tensor >= (uint64_t)P.ntensors || seg.index < 0) return;
   float c = 1.f;
@@ -105,81 +164,158 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamwArgs P) {
     if (!(fabsf(c) <= FLT_MAX)) return;
   }
   const shampoo_tensor tp = P.params[seg.tensor], tg = P.grads[seg.tensor];
-  const int64_t first = (int64_t)seg.index * kSegment;
-  const int64_t left = min(tp.n, tg.n) - first;
-  const int len = (int)min((int64_t)kSegment, left);
+  void* const copy = COPY ? P.copies[seg.tensor].ptr : nullptr;
+  const int64_t first = (int64_t)seg.index * kSegment, pos0 = tp.offset + first;
+  const int len = (int)min((int64_t)kSegment, min(tp.n, tg.n) - first);
   const float eta = P.lr * P.hyper[2 * seg.tensor], keep = 1.f - eta * P.hyper[2 * seg.tensor + 1];
+  // The scale c goes into the constants (in double) where that cannot overflow:
+  // g c g k2 keeps v finite for a huge g with a small c, and takes four roundings at most.
   const float step = eta * P.rbc1, k1 = (float)(P.omb1 * c), k2 = (float)(P.omb2 * c);
-  for (int i0 = 0; i0 < len; i0 += 256) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < len;
-    const int64_t at = first + i, pos = tp.offset + at, grp = pos / kGroup;
-    float g = 0.f, m = 0.f, v = 0.f;
-    if (in) {
-      g = load_elem(tg.ptr, at, P.grad_bf16);
-      if (P.mx8) {
-        m = mx8_decode<MomentM>(ldg(static_cast<const uint8_t*>(P.m) + pos), ldg(P.m_scale + grp));
-        v = mx8_decode<MomentV>(ldg(static_cast<const uint8_t*>(P.v) + pos), ldg(P.v_scale + grp));
+
+  auto rounds = [&](auto WHOLE) __attribute__((always_inline)) {
+    constexpr bool kWhole = decltype(WHOLE)::value;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int i = (r * 256 + (int)threadIdx.x) * V, left = len - i;
+      const int64_t at = first + i, pos = pos0 + i, grp = pos / kGroup;
+      float p[V], g[V], m[V], v[V];
+      load_elems<PARAM_BF16, V, kWhole>(tp.ptr, at, left, p);
+      load_elems<GRAD_BF16, V, kWhole>(tg.ptr, at, left, g);
+      if constexpr (MX8) {
+        // The state buffers are padded to whole groups, so that whole vectors
+        // are there wherever a tensor has elements.
+        Codes mc = 0, vc = 0;
+        int ms = 1, vs = 1;
+        if (kWhole || left > 0) {
+          mc = ldg_once<Codes, V>(static_cast<const uint8_t*>(P.m) + pos);
+          vc = ldg_once<Codes, V>(static_cast<const uint8_t*>(P.v) + pos);
+          ms = ldg(P.m_scale + grp);
+          vs = ldg(P.v_scale + grp);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          m[e] = mx8_decode<MomentM>((mc[e / 4] >> (8 * (e % 4))) & 255u, ms);
+          v[e] = mx8_decode<MomentV>((vc[e / 4] >> (8 * (e % 4))) & 255u, vs);
+          if (!kWhole && e >= left) m[e] = v[e] = 0.f;
+        }
       } else {
-        m = ldg(static_cast<const float*>(P.m) + pos);
-        v = ldg(static_cast<const float*>(P.v) + pos);
+        load_elems<false, V, kWhole>(P.m, pos, left, m);
+        load_elems<false, V, kWhole>(P.v, pos, left, v);
       }
-      // The scale c goes into the constants (in double) where that cannot overflow:
-      // g c g k2 keeps v finite for a huge g with a small c, and takes four roundings at most.
-      m = __builtin_fmaf(g, k1, P.beta1 * m);
-      v = __builtin_fmaf(g * c, g * k2, P.beta2 * v);
-    }
-    const uint32_t h =
-        hash_finish((uint32_t)pos * kHashC1 + (uint32_t)((uint64_t)pos >> 32) * kHashC4 + P.key);
-    if (P.mx8) {
-      uint32_t mb, vb;
-      group_max_abs_bits(m, mb);
-      group_max_abs_bits(v, vb);
-      const int ms = mx8_scale<MomentM>(mb), vs = mx8_scale<MomentV>(vb);
-      if (in) {
-        stg(static_cast<uint8_t*>(P.m) + pos, (uint8_t)mx8_encode<MomentM>(m, ms, h & 0xffffu));
-        stg(static_cast<uint8_t*>(P.v) + pos, (uint8_t)mx8_encode<MomentV>(v, vs, h >> 16));
-        if ((i % kGroup) == 0) {
-          stg(P.m_scale + grp, (uint8_t)ms);
-          stg(P.v_scale + grp, (uint8_t)vs);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        m[e] = __builtin_fmaf(g[e], k1, P.beta1 * m[e]);
+        v[e] = __builtin_fmaf(g[e] * c, g[e] * k2, P.beta2 * v[e]);
+      }
+      uint32_t h[V];
+      if constexpr (MX8 || PARAM_BF16) {
+        // V consecutive positions share their upper 32 bits
+        const uint32_t x = (uint32_t)pos * kHashC1 + (uint32_t)((uint64_t)pos >> 32) * kHashC4 + P.key;
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = hash_finish(x + (uint32_t)e * kHashC1);
+      }
+      if constexpr (MX8) {
+        uint32_t mt = 0, vt = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          mt = max(mt, __builtin_bit_cast(uint32_t, m[e]) & 0x7fffffffu);
+          vt = max(vt, __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu);
+        }
+        const int ms = mx8_scale<MomentM>(group_max<kLanes>(mt)), vs = mx8_scale<MomentV>(group_max<kLanes>(vt));
+        Codes mc = 0, vc = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t a = mx8_encode<MomentM>(m[e], ms, h[e] & 0xffffu), b = mx8_encode<MomentV>(v[e], vs, h[e] >> 16);
+          if (kWhole || e < left) {  // the padding stays 0
+            mc[e / 4] |= a << (8 * (e % 4));
+            vc[e / 4] |= b << (8 * (e % 4));
+          }
+        }
+        if (kWhole || left > 0) {
+          stg_once<Codes, V>(static_cast<uint8_t*>(P.m) + pos, mc);
+          stg_once<Codes, V>(static_cast<uint8_t*>(P.v) + pos, vc);
+          if (threadIdx.x % kLanes == 0) {
+            stg(P.m_scale + grp, (uint8_t)ms);
+            stg(P.v_scale + grp, (uint8_t)vs);
+          }
+        }
+      } else {
+        store_f32<V, kWhole>(P.m, pos, left, m);
+        store_f32<V, kWhole>(P.v, pos, left, v);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_amdgcn_sqrtf(v[e]), P.rsbc2, P.eps));
+        p[e] = __builtin_fmaf(-step, d, p[e] * keep);
+      }
+      if constexpr (PARAM_BF16) {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t b = (__builtin_bit_cast(uint32_t, p[e]) + ((h[e] * kHashC2) >> 16)) >> 16;
+          const uint32_t q = p[e] != p[e] ? 0x7fc0u : b;
+          w[e / 2] = (e & 1) ? w[e / 2] | (q << 16) : q;
+        }
+        store_bf16<V, kWhole>(tp.ptr, at, left, w);
+      } else {
+        store_f32<V, kWhole>(tp.ptr, at, left, p);
+        if constexpr (COPY) {
+          uint32_t w[V / 2];
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+          store_bf16<V, kWhole>(copy, at, left, w);
         }
       }
-    } else if (in) {
-      stg(static_cast<float*>(P.m) + pos, m);
-      stg(static_cast<float*>(P.v) + pos, v);
     }
-    if (!in) continue;
-    const float d = m / (sqrtf(v) * P.rsbc2 + P.eps);
-    const float p = load_elem(tp.ptr, at, P.param_bf16) * keep - step * d;
-    if (P.param_bf16) {
-      const uint32_t b = (__builtin_bit_cast(uint32_t, p) + ((h * kHashC2) >> 16)) >> 16;
-      stg(static_cast<uint16_t*>(tp.ptr) + at, (uint16_t)(p != p ? 0x7fc0u : b));
-    } else {
-      stg(static_cast<float*>(tp.ptr) + at, p);
-      if (P.copies != nullptr) stg(static_cast<uint16_t*>(P.copies[seg.tensor].ptr) + at, f32_to_bf16_bits(p));
-    }
+  };
+  if (len == kSegment) {
+    rounds(std::true_type{});
+  } else {
+    rounds(std::false_type{});
   }
 }
 
-template <class F>
-__global__ void __launch_bounds__(256) mx8_decode_kernel(const uint8_t* codes, const uint8_t* scales, int64_t n,
-                                                         void* out, int bf16) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const float v = mx8_decode<F>(ldg(codes + i), ldg(scales + i / kGroup));
-  if (bf16) {
-    stg(static_cast<uint16_t*>(out) + i, f32_to_bf16_bits(v));
+struct MomentsArgs {
+  const uint8_t *codes[2], *scales[2];  // m, v
+  void* out[2];
+  int64_t n;
+  int first;  // 0: blockIdx.y = 0 is m; 1: only v
+};
+
+// 8 codes a lane.
+template <bool BF16>
+__global__ void __launch_bounds__(256) mx8_decode_kernel(const MomentsArgs P) {
+  const bool is_v = P.first + (int)blockIdx.y != 0;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= P.n) return;
+  const uint8_t* const codes = is_v ? P.codes[1] : P.codes[0];
+  const uint8_t* const scales = is_v ? P.scales[1] : P.scales[0];
+  void* const out = is_v ? P.out[1] : P.out[0];
+  const u32x2 c = ldg_once<u32x2, 1>(codes + i);
+  const int s = ldg(scales + i / kGroup);
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t code = (c[e / 4] >> (8 * (e % 4))) & 255u;
+    x[e] = is_v ? mx8_decode<MomentV>(code, s) : mx8_decode<MomentM>(code, s);
+  }
+  if constexpr (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+    store_bf16<8, true>(out, i, 8, w);
   } else {
-    stg(static_cast<float*>(out) + i, v);
+    store_f32<8, true>(out, i, 8, x);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Norm.  Pass 1: each workgroup sums the squares of a contiguous run of
+// Norm.  Pass 1: each workgroup (1024 of them) sums the squares of a contiguous run of
 // segments in double (a product of two floats is exact there, and no fp32
 // gradient overflows it); pass 2: one workgroup adds the partial sums.  Both
 // in a fixed order.
 // ---------------------------------------------------------------------------
+template <int kThreads>
 __device__ __forceinline__ double block_sum_f64(double v, double* red) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
@@ -187,29 +323,59 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red) {
   __syncthreads();
   double t = 0.;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t += red[i];
+  for (int i = 0; i < kThreads / kWave; ++i) t += red[i];
   __syncthreads();
   return t;
 }
 
+// out: the norm, and the factor that brings it down to max_norm.
+__device__ __forceinline__ void store_norm(double sum, float max_norm, float* out) {
+  const double norm = sqrt(sum);
+  const float f = (float)norm;
+  float coef = norm > max_norm ? (float)(max_norm / norm) : 1.f;
+  if (!(f <= FLT_MAX)) coef = __builtin_nanf("");
+  stg(out, f);
+  stg(out + 1, coef);
+}
+
+template <bool BF16>
 __global__ void __launch_bounds__(256) grad_norm_partial_kernel(const shampoo_tensor* tensors,
                                                                 const shampoo_segment* segments, int64_t nseg,
-                                                                int bf16, double* partial) {
+                                                                double* partial) {
   __shared__ double red[4];
-  double sum = 0.;
-  const int64_t s1 = nseg * (blockIdx.x + 1) / gridDim.x;
-  for (int64_t s = nseg * blockIdx.x / gridDim.x; s < s1; ++s) {
-    const shampoo_segment seg = segments[s];
-    const shampoo_tensor t = tensors[seg.tensor];
+  constexpr int V = BF16 ? 8 : 4, kRounds = kSegment / (256 * V);
+  const int64_t s0 = nseg * blockIdx.x / gridDim.x, s1 = nseg * (blockIdx.x + 1) / gridDim.x;
+  double sum[2] = {0., 0.};
+  shampoo_segment seg = segments[s0];  // every block has one: gridDim.x <= nseg
+  shampoo_tensor t = tensors[seg.tensor];
+  for (int64_t s = s0; s < s1; ++s) {
     const int64_t first = (int64_t)seg.index * kSegment;
     const int len = (int)min((int64_t)kSegment, t.n - first);
-    for (int i = threadIdx.x; i < len; i += 256) {
-      const double g = load_elem(t.ptr, first + i, bf16);
-      sum += g * g;
+    const void* const p = t.ptr;
+    float x[kRounds][V];
+    if (len == kSegment) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
+        load_elems<BF16, V, true>(p, first + (r * 256 + (int)threadIdx.x) * V, V, x[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int i = (r * 256 + (int)threadIdx.x) * V;
+        load_elems<BF16, V, false>(p, first + i, len - i, x[r]);
+      }
     }
+    seg = segments[min(s + 1, nseg - 1)];  // the next descriptor, under this segment's loads
+    t = tensors[seg.tensor];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const double g = x[r][e];
+        sum[e & 1] = __builtin_fma(g, g, sum[e & 1]);
+      }
   }
-  sum = block_sum_f64(sum, red);
-  if (threadIdx.x == 0) stg(partial + blockIdx.x, sum);
+  const double total = block_sum_f64<256>(sum[0] + sum[1], red);
+  if (threadIdx.x == 0) stg(partial + blockIdx.x, total);
 }
 
 __global__ void __launch_bounds__(256) grad_norm_final_kernel(const double* partial, int count, float max_norm,
@@ -217,14 +383,38 @@ __global__ void __launch_bounds__(256) grad_norm_final_kernel(const double* part
   __shared__ double red[4];
   double sum = 0.;
   for (int i = threadIdx.x; i < count; i += 256) sum += ldg(partial + i);
-  sum = block_sum_f64(sum, red);
-  if (threadIdx.x != 0) return;
-  const double norm = sqrt(sum);
-  const float f = (float)norm;
-  float coef = norm > max_norm ? (float)(max_norm / norm) : 1.f;
-  if (!(f <= FLT_MAX)) coef = __builtin_nanf("");
-  stg(out, f);
-  stg(out + 1, coef);
+  sum = block_sum_f64<256>(sum, red);
+  if (threadIdx.x == 0) store_norm(sum, max_norm, out);
+}
+
+// A few segments: both passes in one workgroup, a wave a segment.
+template <bool BF16>
+__global__ void __launch_bounds__(1024) grad_norm_small_kernel(const shampoo_tensor* tensors,
+                                                               const shampoo_segment* segments, int nseg,
+                                                               float max_norm, float* out) {
+  __shared__ double red[16];
+  constexpr int V = BF16 ? 8 : 4;
+  const int lane = threadIdx.x % kWave;
+  double sum = 0.;
+  for (int s = threadIdx.x / kWave; s < nseg; s += 16) {
+    const shampoo_segment seg = segments[s];
+    const shampoo_tensor t = tensors[seg.tensor];
+    const int64_t first = (int64_t)seg.index * kSegment;
+    const int len = (int)min((int64_t)kSegment, t.n - first);
+#pragma unroll 4
+    for (int i = lane * V; i < len; i += kWave * V) {
+      float x[V];
+      if (i + V <= len) {
+        load_elems<BF16, V, true>(t.ptr, first + i, V, x);
+      } else {
+        load_elems<BF16, V, false>(t.ptr, first + i, len - i, x);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
+    }
+  }
+  sum = block_sum_f64<1024>(sum, red);
+  if (threadIdx.x == 0) store_norm(sum, max_norm, out);
 }
 
 }  // namespace shp

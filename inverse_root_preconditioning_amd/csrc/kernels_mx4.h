@@ -25,17 +25,6 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t top_bits) {
 // nearest even and saturate at 6.
 __device__ __forceinline__ float mx4_scale_float(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
 
-// Largest of v over groups of 4 (8) consecutive lanes, in every lane.
-template <int LANES>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  static_assert(LANES == 4 || LANES == 8, "lanes of a group");
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));  // quad_perm 1 0 3 2
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));  // quad_perm 2 3 0 1
-  if constexpr (LANES == 8)
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror
-  return v;
-}
-
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
