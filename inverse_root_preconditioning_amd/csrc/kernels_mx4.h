@@ -336,7 +336,7 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 }
 
 // ---------------------------------------------------------------------------
-// C = alpha A B^T + beta C on tiles of 64 T x 64 T: W / 2 x 2 waves, each 4 T / W x T
+// C = alpha A B^T + beta C on tiles of 64 T x 64 T: 4 waves (2 x 2), each T x T
 // blocks of the 32 x 32 x 64 scaled MFMA.  Chunks of 256 columns (128 bytes a row)
 // go straight into one of two LDS buffers (global_load_lds_dwordx4) while the
 // other is multiplied.
@@ -379,60 +379,70 @@ __device__ __forceinline__ void to_lds4(const uint8_t* from, uint8_t* to) {
 }
 
 // 4 elements of a row of C at column n (all of them, or those below N).
-template <bool BF16, bool BETA, bool WHOLE>
-__device__ __forceinline__ void mx4_store4(const Mx4ProductArgs& P, int64_t m, int64_t n, const floatx4& v) {
-  const int64_t at = m * P.ldc + n;
-  uint16_t* const ch = static_cast<uint16_t*>(P.c) + at;
-  float* const cf = static_cast<float*>(P.c) + at;
-  if (!WHOLE && n + 4 > P.N) {
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ floatx4 mx4_load4(const Mx4ProductArgs& P, int64_t m, int64_t n) {
+  const uint16_t* const ch = static_cast<const uint16_t*>(P.c) + m * P.ldc + n;
+  const float* const cf = static_cast<const float*>(P.c) + m * P.ldc + n;
+  floatx4 o = {0.f, 0.f, 0.f, 0.f};
+  if (WHOLE || n + 4 <= P.N) {
+    if constexpr (BF16) {
+      const u32x2 w = ldg_any<u32x2, 2>(ch);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = __builtin_bit_cast(float, (e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
+    } else {
+      o = ldg_any<floatx4, 4>(cf);
+    }
+  } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (n + e < P.N) {
-        float o = P.alpha * v[e];
         if constexpr (BF16) {
-          if constexpr (BETA) o += P.beta * __builtin_bit_cast(float, (uint32_t)ldg(ch + e) << 16);
-          stg(ch + e, f32_to_bf16_bits(o));
+          o[e] = __builtin_bit_cast(float, (uint32_t)ldg(ch + e) << 16);
         } else {
-          if constexpr (BETA) o += P.beta * ldg(cf + e);
-          stg(cf + e, o);
+          o[e] = ldg(cf + e);
         }
       }
     }
-    return;
   }
-  floatx4 o;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = P.alpha * v[e];
-  if constexpr (BF16) {
-    if constexpr (BETA) {
-      const u32x2 old = ldg_any<u32x2, 2>(ch);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] += P.beta * __builtin_bit_cast(float, (e & 1) ? (old[e / 2] & 0xffff0000u) : (old[e / 2] << 16));
+  return o;
+}
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void mx4_store4(const Mx4ProductArgs& P, int64_t m, int64_t n, const floatx4& v) {
+  uint16_t* const ch = static_cast<uint16_t*>(P.c) + m * P.ldc + n;
+  float* const cf = static_cast<float*>(P.c) + m * P.ldc + n;
+  if (WHOLE || n + 4 <= P.N) {
+    if constexpr (BF16) {
+      stg_any<u32x2, 2>(ch, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+    } else {
+      stg_any<floatx4, 4>(cf, v);
     }
-    stg_any<u32x2, 2>(ch, u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])});
   } else {
-    if constexpr (BETA) {
-      const floatx4 old = ldg_any<floatx4, 4>(cf);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += P.beta * old[e];
+    for (int e = 0; e < 4; ++e) {
+      if (n + e < P.N) {
+        if constexpr (BF16) {
+          stg(ch + e, f32_to_bf16_bits(v[e]));
+        } else {
+          stg(cf + e, v[e]);
+        }
+      }
     }
-    stg_any<floatx4, 4>(cf, o);
   }
 }
 
-template <int T, int W, bool BF16, bool BETA>
-__global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4ProductArgs P) {
-  constexpr int BT = 64 * T, NT = 64 * W;                      // tile edge, threads
-  constexpr int TM = 4 * T / W, TN = T;                        // blocks of a wave: W / 2 x 2 waves
+template <int T, bool BF16, bool BETA>
+__global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArgs P) {
+  constexpr int BT = 64 * T, NT = 256;                         // tile edge, threads
   constexpr int kData = BT * kMx4RowBytes, kStage = 2 * kData;
   constexpr int kScale = BT * 4 * kMx4ScaleDwords;             // one operand's scale block
   constexpr int LD = kData / (NT * 16);                       // 16-byte loads a thread, operand and chunk
   constexpr int LS = kScale / 2 / (NT * 4);                    // 4-byte scale loads likewise
-  constexpr int kSlice = 32 * TN + 4;                          // floats: pitch of a wave's output slice
+  constexpr int kSlice = 32 * T + 4;                          // floats: pitch of a wave's output slice
   constexpr int kLds = 2 * kStage + 4 * kScale;
   static_assert(LD * NT * 16 == kData && LS * NT * 8 == kScale, "chunking");
-  static_assert(W * 32 * kSlice * 4 <= kLds && kLds <= 160 * 1024, "fits the LDS");
+  static_assert(4 * 32 * kSlice * 4 <= kLds && kLds <= 160 * 1024, "fits the LDS");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
 
   // Tiles in groups of 8 tile rows, column by column within a group: the 32
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   const int64_t m0 = (int64_t)(8 * group + in_group % rows_here) * BT, n0 = (int64_t)(in_group / rows_here) * BT;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wave >> 1) * 32 * TM, wn = (wave & 1) * 32 * TN;
+  const int wm = (wave >> 1) * 32 * T, wn = (wave & 1) * 32 * T;
   const int r32 = lane & 31, h = lane >> 5;
 
   const uint32_t pitch = (uint32_t)(P.padded / 2), spitch = (uint32_t)(P.padded / kMx4Group);
@@ -482,7 +492,7 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   auto issue_scales = [&](int blk, int q) __attribute__((always_inline)) {
     const uint8_t* const from = q < 2 ? As : Bs;
     const int limit = q < 2 ? ma : nb;
-    const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * (wave & 3))), last);
+    const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * wave)), last);
     uint8_t* const to = lds + 2 * kStage + (blk & 1) * 2 * kScale;
 #pragma unroll
     for (int it = 0; it < LS; ++it) {
@@ -503,11 +513,11 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
     }
   };
 
-  floatx16 acc[TM][TN];
+  floatx16 acc[T][T];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < T; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < T; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
@@ -519,14 +529,14 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   const int scaleB = 2 * kStage + kScale + (wn + rb) * 4 * kMx4ScaleDwords;
   constexpr int kBlock = 32 * kMx4RowBytes, kBlockScales = 32 * 4 * kMx4ScaleDwords;
 
-  intx4 fa[2][TM], fb[2][TN];
-  int sa[TM], sb[TN];
+  intx4 fa[2][T], fb[2][T];
+  int sa[T], sb[T];
   auto read = [&](int buf, int slot, int q) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < T; ++i)
       fa[slot][i] = *reinterpret_cast<const intx4*>(lds + buf + rowA + i * kBlock + 16 * (q ^ swzA));
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < T; ++j)
       fb[slot][j] = *reinterpret_cast<const intx4*>(lds + buf + rowB + j * kBlock + 16 * (q ^ swzB));
   };
   // This lane's scales at dword p of scale block parity blk.
@@ -534,9 +544,9 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
     const int base = (blk & 1) * 2 * kScale;
     const int pa = 4 * (p ^ (2 * ((r32 >> 3) & 3))), pb = 4 * (p ^ (2 * ((rb >> 3) & 3)));
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const int*>(lds + base + scaleA + i * kBlockScales + pa);
+    for (int i = 0; i < T; ++i) sa[i] = *reinterpret_cast<const int*>(lds + base + scaleA + i * kBlockScales + pa);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
+    for (int j = 0; j < T; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
   };
   constexpr int kWaitAll = 0 | (7 << 4);  // vmcnt(0) lgkmcnt(0)
   auto meet = [&]() __attribute__((always_inline)) {
@@ -561,16 +571,16 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   if (steps & 1) {  // lane half h takes groups 2 h and 2 h + 1
     read_scales(1, min((((full / 4) | 1) * kMx4ScaleDwords), last) == last ? 0 : 2 * (full % 4));
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = sa[i] >> (16 * h);
+    for (int i = 0; i < T; ++i) sa[i] = sa[i] >> (16 * h);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) sb[j] = sb[j] >> (16 * h);
+    for (int j = 0; j < T; ++j) sb[j] = sb[j] >> (16 * h);
     static_for<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = decltype(S)::value;
       read(kStage, s, 2 * h + s);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_mx4<s>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i]);
+        for (int j = 0; j < T; ++j) acc[i][j] = mfma_mx4<s>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i]);
     });
     meet();
   }
@@ -582,14 +592,14 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
     read(0, 0, 4 * h);
     for (int c = 0; c < full; ++c) {
       const int other = kStage - cur;
-      int ta[TM], tb[TN];
+      int ta[T], tb[T];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) ta[i] = sa[i];
+      for (int i = 0; i < T; ++i) ta[i] = sa[i];
 #pragma unroll
-      for (int j = 0; j < TN; ++j) tb[j] = sb[j];
+      for (int j = 0; j < T; ++j) tb[j] = sb[j];
       static_for<4>([&](auto S) __attribute__((always_inline)) {
         constexpr int s = decltype(S)::value;
-        constexpr int kReads = TM + TN, kMfma = TM * TN;
+        constexpr int kReads = 2 * T, kMfma = T * T;
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (s == 0) issue_b(other, min(c + 1, full - 1));
         if constexpr (s == 1) issue_scales(c / 4 + 1, c % 4);
@@ -602,9 +612,9 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
           read(other, 0, 4 * h);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < T; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
+          for (int j = 0; j < T; ++j)
             acc[i][j] = mfma_mx4<s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], tb[j], ta[i]);
         // one MFMA, one LDS read, and so on; then the loads
         static_for<(kReads < kMfma ? kReads : kMfma)>([&](auto) __attribute__((always_inline)) {
@@ -626,32 +636,36 @@ __global__ void __launch_bounds__(64 * W, 1) mx4_product_kernel(const Mx4Product
   float* const slice = reinterpret_cast<float*>(lds) + wave * 32 * kSlice;
   auto output = [&](auto WHOLE) __attribute__((always_inline)) {
     constexpr bool kWhole = decltype(WHOLE)::value;
+    constexpr int kLanes = 8 * T, kRows = 64 / kLanes, kIter = 32 / kRows;  // kLanes lanes hold a row, 4 elements each
+    const int col = 4 * (lane % kLanes), row0 = lane / kLanes;
+    const int64_t n = n0 + wn + col;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int i = 0; i < T; ++i) {
+      const int64_t mi = m0 + wm + 32 * i + row0, split = (int64_t)blockIdx.y * P.M;
+      // all of C's loads first: none can pass a store
+      floatx4 old[BETA ? kIter : 1];
+      if constexpr (BETA) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+        for (int r = 0; r < kIter; ++r)
+          if (kWhole || (mi + r * kRows < P.M && n < P.N)) old[r] = mx4_load4<BF16, kWhole>(P, mi + r * kRows, n);
+      }
+#pragma unroll
+      for (int j = 0; j < T; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<floatx4*>(slice + r32 * kSlice + 32 * j + 16 * h + 4 * q) =
               floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-      constexpr int kLanes = 8 * TN, kRows = 64 / kLanes;  // lanes that hold a row, 4 elements each
-      const int col = 4 * (lane % kLanes);
-      const int64_t n = n0 + wn + col;
-      if constexpr (kWhole) {
+      floatx4 v[kIter];
 #pragma unroll
-        for (int r = 0; r < 32; r += kRows) {
-          const int row = r + lane / kLanes;
-          mx4_store4<BF16, BETA, true>(P, blockIdx.y * P.M + m0 + wm + 32 * i + row, n,
-                                       *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
+      for (int r = 0; r < kIter; ++r) v[r] = *reinterpret_cast<const floatx4*>(slice + (r * kRows + row0) * kSlice + col);
+#pragma unroll
+      for (int r = 0; r < kIter; ++r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[r][e] *= P.alpha;
+          if constexpr (BETA) v[r][e] += P.beta * old[r][e];
         }
-      } else {
-#pragma unroll 1
-        for (int r = 0; r < 32; r += kRows) {
-          const int row = r + lane / kLanes;
-          const int64_t m = m0 + wm + 32 * i + row;
-          if (m < P.M && n < P.N)
-            mx4_store4<BF16, BETA, false>(P, blockIdx.y * P.M + m, n, *reinterpret_cast<const floatx4*>(slice + row * kSlice + col));
-        }
+        if (kWhole || (mi + r * kRows < P.M && n < P.N)) mx4_store4<BF16, kWhole>(P, split + mi + r * kRows, n, v[r]);
       }
     }
   };

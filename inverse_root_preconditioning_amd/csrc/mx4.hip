@@ -78,22 +78,22 @@ int quantize(Mx4QuantArgs a, bool bf16, hipStream_t stream) {
   return check_launch();
 }
 
-template <int T, int W>
+template <int T>
 int product_tiles(Mx4ProductArgs a, int splits, hipStream_t stream) {
   const int64_t tm = (a.M + 64 * T - 1) / (64 * T), tn = (a.N + 64 * T - 1) / (64 * T);
   if (tm * tn > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
   a.tiles_m = (uint32_t)tm;
   a.tiles_n = (uint32_t)tn;
-  const dim3 grid((uint32_t)(tm * tn), (uint32_t)splits), block(64 * W);
+  const dim3 grid((uint32_t)(tm * tn), (uint32_t)splits), block(256);
   const bool beta = a.beta != 0.f;
   if (a.bf16 && beta) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, W, true, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, true, true>), grid, block, 0, stream, a);
   } else if (a.bf16) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, W, true, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, true, false>), grid, block, 0, stream, a);
   } else if (beta) {
-    hipLaunchKernelGGL((mx4_product_kernel<T, W, false, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, false, true>), grid, block, 0, stream, a);
   } else {
-    hipLaunchKernelGGL((mx4_product_kernel<T, W, false, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx4_product_kernel<T, false, false>), grid, block, 0, stream, a);
   }
   return check_launch();
 }
@@ -155,14 +155,14 @@ int product(Mx4ProductArgs a, int64_t K, void* ws, hipStream_t stream) {
     a.alpha = 1.f;
     a.beta = 0.f;
     a.bf16 = 0;
-    const int rc = product_tiles<1, 4>(a, splits, stream);
+    const int rc = product_tiles<1>(a, splits, stream);
     if (rc != SHAMPOO_OK) return rc;
     hipLaunchKernelGGL(mx4_sum_kernel, dim3((uint32_t)((a.M * a.N + 255) / 256)), dim3(256), 0, stream, s);
     return check_launch();
   }
-  if (tiles_of(a.M, a.N, 256) >= 192) return product_tiles<4, 8>(a, 1, stream);
-  if (tiles_of(a.M, a.N, 128) >= 192) return product_tiles<2, 4>(a, 1, stream);
-  return product_tiles<1, 4>(a, 1, stream);
+  if (tiles_of(a.M, a.N, 256) >= 192) return product_tiles<4>(a, 1, stream);
+  if (tiles_of(a.M, a.N, 128) >= 192) return product_tiles<2>(a, 1, stream);
+  return product_tiles<1>(a, 1, stream);
 }
 
 }  // namespace
