@@ -21,7 +21,7 @@ LIB = os.path.join(LIBDIR, "libshampoo_mi355x.so")
 ARCH = os.environ.get("SHAMPOO_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["shampoo.hip", "adamw.hip", "mx4.hip"]
-HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h", "kernels_adamw.h", "kernels_mx4.h"]
+HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h", "vector_io.h", "kernels_adamw.h", "kernels_mx4.h"]
 
 
 def hipcc():

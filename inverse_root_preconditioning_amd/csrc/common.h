@@ -44,31 +44,6 @@ __device__ __forceinline__ void stg(T* p, const T& v) {
   *(__attribute__((address_space(1))) T*)p = v;
 }
 
-// The same for a vector at an address aligned to ALIGN bytes only (global
-// memory takes vector accesses at any element's address).
-template <class V, int ALIGN>
-__device__ __forceinline__ V ldg_any(const void* p) {
-  typedef V U __attribute__((aligned(ALIGN)));
-  return *(const __attribute__((address_space(1))) U*)p;
-}
-template <class V, int ALIGN>
-__device__ __forceinline__ void stg_any(void* p, const V& v) {
-  typedef V U __attribute__((aligned(ALIGN)));
-  *(__attribute__((address_space(1))) U*)p = v;
-}
-
-// The same for data that is read or written once: not kept in the caches.
-template <class V, int ALIGN>
-__device__ __forceinline__ V ldg_once(const void* p) {
-  typedef V U __attribute__((aligned(ALIGN)));
-  return __builtin_nontemporal_load((const __attribute__((address_space(1))) U*)p);
-}
-template <class V, int ALIGN>
-__device__ __forceinline__ void stg_once(void* p, const V& v) {
-  typedef V U __attribute__((aligned(ALIGN)));
-  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) U*)p);
-}
-
 // f(std::integral_constant<int, i>) for i = 0..N-1, expanded at compile time
 // (indices stay constants even where a loop would be too large to unroll).
 template <class F, int... I>
@@ -89,17 +64,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  return v;
-}
-
-// Largest of v over groups of 4 (8) consecutive lanes, in every lane.
-template <int LANES>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  static_assert(LANES == 4 || LANES == 8, "lanes of a group");
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));  // quad_perm 1 0 3 2
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));  // quad_perm 2 3 0 1
-  if constexpr (LANES == 8)
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror
   return v;
 }
 

@@ -2,7 +2,7 @@
 // walk a list of 4096-element segments, one workgroup a segment.
 #pragma once
 
-#include "common.h"
+#include "vector_io.h"
 
 namespace shp {
 

@@ -2,7 +2,7 @@
 // product C = alpha A B^T + beta C on the scaled MFMA of gfx950.
 #pragma once
 
-#include "common.h"
+#include "vector_io.h"
 
 namespace shp {
 

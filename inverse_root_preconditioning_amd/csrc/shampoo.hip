@@ -1023,7 +1023,8 @@ const char* shampoo_strerror(int code) {
   switch (code) {
     case SHAMPOO_OK: return "success";
     case SHAMPOO_EINVAL: return "invalid argument (null pointer, negative count or parameter out of range)";
-    case SHAMPOO_EUNSUPPORTED: return "unsupported configuration (B must be a multiple of 64 in [64, 16384])";
+    case SHAMPOO_EUNSUPPORTED: return "unsupported configuration (a type or size that is not implemented; B must be a multiple of 64 in "
+             "[64, 16384])";
     case SHAMPOO_EWORKSPACE: return "workspace missing or smaller than shampoo_workspace_bytes";
     case SHAMPOO_EHIP: return "HIP runtime error while launching a kernel";
     case SHAMPOO_ESCRATCH:
