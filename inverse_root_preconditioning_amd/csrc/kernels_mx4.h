@@ -353,7 +353,7 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 //    then in registers.  It frees the chunk's buffer: A's half of the chunk
 //    after next is loaded into it under this step's MFMAs, B's under the next's.
 //  - 16-byte pieces of a row are permuted by the row (mx4_swz_a, mx4_swz_b), so
-//    that the 8 rows a fragment read takes per clock lie in different banks.
+//    that the rows a fragment read takes per clock lie in different banks.
 //  - B is the MFMA's first operand and its rows are assigned to MFMA rows so
 //    that a lane ends with 16 consecutive columns of one row of C.  Each wave
 //    turns its 32-row slices through LDS into stores of whole rows.
@@ -364,9 +364,10 @@ constexpr int kMx4ScaleDwords = 8;          // of a row and block: 4 chunks
 
 __device__ __forceinline__ int mx4_swz_a(int row) { return (row ^ ((row >> 3) & 3)) & 7; }
 // Row of B that MFMA row r (0 ... 31) of a block takes, and its permutation:
-// 8 consecutive r cover rows 0-3 and 16-19 of the block (plus a multiple of 4).
+// 16 consecutive r cover rows 0-7 and 16-23 of the block (or 8 further on), whose
+// even and odd rows lie in different halves of the banks.
 __device__ __forceinline__ int mx4_row_b(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
-__device__ __forceinline__ int mx4_swz_b(int row) { return (row & 3) | ((row >> 2) & 4); }
+__device__ __forceinline__ int mx4_swz_b(int row) { return ((row >> 1) & 3) | ((row >> 2) & 4); }
 
 // 16 (4) bytes a lane from memory to consecutive places in LDS.
 __device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
