@@ -10,8 +10,6 @@ All the arithmetic runs in the HIP library (see capi and include/shampoo.h).
 """
 from __future__ import annotations
 
-import functools
-
 import numpy as np
 import torch
 
@@ -20,20 +18,7 @@ from . import capi
 _TYPES = {torch.float32: capi.T_F32, torch.bfloat16: capi.T_BF16}
 _STATES = {"f32": capi.STATE_F32, "mx8": capi.STATE_MX8}
 
-
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without the Python objects
-
-
-def _on_stream(fn):
-    """Lets fn(...) be called with stream=...: its work and its allocations then
-    belong to that stream (else to the current one)."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return call
 
 
 def _dense(t):
@@ -103,20 +88,23 @@ class TensorTable:
         self._norm_ws = capi.shampoo_grad_norm_workspace_bytes(self.nsegments)
 
 
-@_on_stream
-def grad_norm(table, max_norm=float("inf"), out=None):
+def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
     """float32 [2] on the device: the Euclidean norm of all the table's tensors
     as one vector, and min(1, max_norm / norm) (NaN if the norm is not finite,
     which makes AdamW.step change nothing)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return grad_norm(table, max_norm, out)
     if out is None:
-        out = table.tensor.new_empty(2, dtype=torch.float32)
+        out = table.tensor.new_empty((2,), dtype=torch.float32)
     elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2):
         raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements")
     need = table._norm_ws
     ws = table.tensor.new_empty(need, dtype=torch.uint8) if need else None
-    capi.check(capi.shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
-                                      out.data_ptr(), ws.data_ptr() if need else 0, need, _raw_stream(table.index)),
-               "shampoo_grad_norm")
+    rc = capi.load().shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
+                                       out.data_ptr(), ws.data_ptr() if need else 0, need, _raw_stream(table.index))
+    if rc:
+        capi.check(rc, "shampoo_grad_norm")
     return out
 
 
@@ -171,50 +159,58 @@ class AdamW:
         self.v = torch.zeros(p.total, dtype=dtype, device=dev)
         self.m_scale = torch.zeros(p.total // capi.GROUP, dtype=torch.uint8, device=dev) if low else None
         self.v_scale = torch.zeros(p.total // capi.GROUP, dtype=torch.uint8, device=dev) if low else None
+        # the buffers stay where they are: load_state_dict copies into them
+        self._state = _STATES[state]
+        self._state_ptrs = tuple(0 if t is None else t.data_ptr() for t in (self.m, self.v, self.m_scale, self.v_scale))
+        self._hyper_ptr = self.hyper.data_ptr()
+        self._copies_ptr = 0 if self.copies is None else self.copies.ptr
 
     def _same(self, table, name):
-        if table is self._checked:
-            return                     # neither its layouts nor its device change
         if table.layouts != self.params.layouts:
             raise ValueError(f"{name} differ from the parameters in number, size or layout")
         if table.device != self.params.device:
             raise ValueError(f"{name} are on another device than the parameters")
-        self._checked = table
 
-    @_on_stream
-    def step(self, grads, lr=None, grad_scale=None):
+    def step(self, grads, lr=None, grad_scale=None, stream=None):
         """One step with the gradients of a TensorTable (or a list of tensors).
         grad_scale: float32 tensor of one element on the device that multiplies
         the gradients; if it is not finite, nothing changes but `t`."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(grads, lr, grad_scale)
         if not isinstance(grads, TensorTable):
             grads = TensorTable(grads)
         p = self.params
-        self._same(grads, "gradients")
+        if grads is not self._checked:
+            self._same(grads, "gradients")
+            self._checked = grads        # neither its layouts nor its device change
         scale_ptr = 0
         if grad_scale is not None:
             if not (grad_scale.is_cuda and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1):
                 raise ValueError("grad_scale must be a float32 CUDA tensor of one element")
             scale_ptr = grad_scale.data_ptr()
-        low = self.m_scale is not None
-        capi.check(capi.shampoo_adamw(
-            p.ptr, grads.ptr, self.copies.ptr if self.copies is not None else 0, self.hyper.data_ptr(), p.n,
-            p.segments_ptr, p.nsegments, p.type, grads.type, _STATES[self.state], self.m.data_ptr(), self.v.data_ptr(),
-            self.m_scale.data_ptr() if low else 0, self.v_scale.data_ptr() if low else 0,
-            self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.t + 1, self.seed, scale_ptr,
-            _raw_stream(p.index)), "shampoo_adamw")
+        b1, b2 = self.betas
+        rc = capi.load().shampoo_adamw(
+            p.ptr, grads.ptr, self._copies_ptr, self._hyper_ptr, p.n, p.segments_ptr, p.nsegments, p.type, grads.type,
+            self._state, *self._state_ptrs, self.lr if lr is None else lr, b1, b2, self.eps, self.t + 1, self.seed,
+            scale_ptr, _raw_stream(p.index))
+        if rc:
+            capi.check(rc, "shampoo_adamw")
         self.t += 1
 
-    @_on_stream
-    def moments(self, dtype=torch.float32):
+    def moments(self, dtype=torch.float32, stream=None):
         """The values of (m, v) as flat tensors in the state's layout."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.moments(dtype)
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
         if self.m_scale is None:
             return self.m.to(dtype), self.v.to(dtype)
         m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
-        capi.check(capi.shampoo_adamw_moments(
-            self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), m.numel(),
-            m.data_ptr(), v.data_ptr(), _TYPES[dtype], _raw_stream(self.params.index)), "shampoo_adamw_moments")
+        mc, vc, ms, vs = self._state_ptrs
+        capi.check(capi.shampoo_adamw_moments(mc, ms, vc, vs, m.numel(), m.data_ptr(), v.data_ptr(), _TYPES[dtype],
+                                              _raw_stream(self.params.index)), "shampoo_adamw_moments")
         return m, v
 
     def state_dict(self):

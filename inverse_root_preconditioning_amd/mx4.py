@@ -14,11 +14,14 @@ import math
 import torch
 
 from . import capi
-from .adamw import _TYPES, _on_stream, _raw_stream
+from .adamw import _TYPES, _raw_stream
 
 
 def _padded(k):
-    return -(-k // capi.MX4_PAD) * capi.MX4_PAD
+    return (k + 127) & -128          # capi.MX4_PAD
+
+
+_check = capi.check
 
 
 def _matrix(t, name):
@@ -68,7 +71,7 @@ class MX4Matrix:
         """Uninitialised storage on the device of the tensor `like`: one buffer, scales after codes."""
         m = cls.__new__(cls)
         n = rows * _padded(cols) // 2             # a multiple of 64
-        m._buf = like.new_empty(n + n // 16, dtype=torch.uint8)
+        m._buf = like.new_empty((n + n // 16,), dtype=torch.uint8)
         m._codes = m._scales = None
         m.codes_ptr = m._buf.data_ptr()
         m.scales_ptr = m.codes_ptr + n
@@ -100,35 +103,52 @@ def _quantize(x, along_rows, along_cols):
         return q, qt
     dtype, ld = _matrix(x, "x")
     rows, cols = x.shape
-    q = MX4Matrix.empty(rows, cols, x) if along_rows else None
-    qt = MX4Matrix.empty(cols, rows, x) if along_cols else None
-    capi.check(capi.shampoo_mx4_quantize(
-        x.data_ptr(), dtype, rows, cols, ld, q.codes_ptr if q else 0, q.scales_ptr if q else 0,
-        qt.codes_ptr if qt else 0, qt.scales_ptr if qt else 0, _raw_stream(x.device.index)), "shampoo_mx4_quantize")
+    q = qt = None
+    codes = scales = codes_t = scales_t = 0
+    if along_rows:
+        q = MX4Matrix.empty(rows, cols, x)
+        codes, scales = q.codes_ptr, q.scales_ptr
+    if along_cols:
+        qt = MX4Matrix.empty(cols, rows, x)
+        codes_t, scales_t = qt.codes_ptr, qt.scales_ptr
+    rc = capi.load().shampoo_mx4_quantize(x.data_ptr(), dtype, rows, cols, ld, codes, scales, codes_t, scales_t,
+                                          _raw_stream(x.device.index))
+    if rc:
+        _check(rc, "shampoo_mx4_quantize")
     return q, qt
 
 
-@_on_stream
-def quantize(x):
+def quantize(x, stream=None):
     """x [rows, cols] (or a transposed view of such a matrix) as MX4, 32
     consecutive columns sharing a scale."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize(x)
     return _quantize(x, True, False)[0]
 
 
-@_on_stream
-def quantize_both(x):
+def quantize_both(x, stream=None):
     """(quantize(x), quantize(x.t())) from one reading of x."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_both(x)
     return _quantize(x, True, True)
 
 
-@_on_stream
-def dequantize(q, dtype=torch.float32):
+def dequantize(q, dtype=torch.float32, stream=None):
     """The values of q."""
-    if dtype not in _TYPES:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dequantize(q, dtype)
+    code = _TYPES.get(dtype)
+    if code is None:
         raise ValueError("dtype must be float32 or bfloat16")
-    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
-    capi.check(capi.shampoo_mx4_dequantize(q.codes_ptr, q.scales_ptr, q.rows, q.cols, out.data_ptr(), _TYPES[dtype],
-                                           q.cols, _raw_stream(q.device.index)), "shampoo_mx4_dequantize")
+    rows, cols, device = q.rows, q.cols, q.device
+    out = torch.empty((rows, cols), dtype=dtype, device=device)
+    rc = capi.load().shampoo_mx4_dequantize(q.codes_ptr, q.scales_ptr, rows, cols, out.data_ptr(), code, cols,
+                                            _raw_stream(device.index))
+    if rc:
+        _check(rc, "shampoo_mx4_dequantize")
     return out
 
 
@@ -140,54 +160,66 @@ def _workspace(need, like):
     return ws, ws.data_ptr()
 
 
-@_on_stream
-def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0):
+def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=None):
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
-    if a.cols != b.cols:
-        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    if a.device != b.device or (out is not None and out.device != a.device):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return product(a, b, out, dtype, alpha, beta)
+    M, N, K, device = a.rows, b.rows, a.cols, a.device
+    if K != b.cols:
+        raise ValueError(f"a has {K} columns, b {b.cols}")
+    if device != b.device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out")
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
+        out = torch.empty((M, N), dtype=dtype, device=device)
     ctype, ld = _matrix(out, "out")
-    if tuple(out.shape) != (a.rows, b.rows):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(a.rows, b.rows)}")
-    need = capi.shampoo_mx4_workspace_bytes(a.rows, b.rows, a.cols)
+    if out.shape != (M, N):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, N)}")
+    lib = capi.load()
+    need = lib.shampoo_mx4_workspace_bytes(M, N, K)
     ws, ws_ptr = _workspace(need, out)
-    capi.check(capi.shampoo_mx4_product(a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, a.rows, b.rows, a.cols,
-                                        alpha, beta, out.data_ptr(), ctype, ld, ws_ptr, need,
-                                        _raw_stream(a.device.index)), "shampoo_mx4_product")
+    rc = lib.shampoo_mx4_product(a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, M, N, K, alpha, beta,
+                                 out.data_ptr(), ctype, ld, ws_ptr, need, _raw_stream(device.index))
+    if rc:
+        _check(rc, "shampoo_mx4_product")
     return out
 
 
-@_on_stream
-def linear(x, w, out=None):
+def linear(x, w, out=None, stream=None):
     """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type."""
-    shape = x.shape
-    if shape[-1] != w.cols:
-        raise ValueError(f"x has {shape[-1]} columns, w {w.cols}")
-    if x.device != w.device or (out is not None and out.device != w.device):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear(x, w, out)
+    shape, N, K, device = x.shape, w.rows, w.cols, w.device
+    if shape[-1] != K:
+        raise ValueError(f"x has {shape[-1]} columns, w {K}")
+    if x.device != device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
-    rows = math.prod(shape[:-1])
-    flat = x if len(shape) == 2 else x.view(rows, w.cols)
-    xtype, ldx = _matrix(flat, "x")
-    if out is None:
-        out = x.new_empty((*shape[:-1], w.rows))
-        ldy = w.rows
+    if len(shape) == 2:
+        flat, rows, to = x, shape[0], (shape[0], N)
     else:
-        if tuple(out.shape) != (*shape[:-1], w.rows) or out.dtype != x.dtype:
-            raise ValueError(f"out must have shape {(*shape[:-1], w.rows)} and x's type")
-        _, ldy = _matrix(out if out.dim() == 2 else out.view(rows, w.rows), "out")
-    need = capi.shampoo_mx4_linear_workspace_bytes(rows, w.rows, w.cols)
+        rows, to = math.prod(shape[:-1]), (*shape[:-1], N)
+        flat = x.view(rows, K)
+    xtype, ldx = _matrix(flat, "x")
+    ldy = N
+    if out is None:
+        out = x.new_empty(to)
+    else:
+        if out.shape != to or out.dtype != x.dtype:
+            raise ValueError(f"out must have shape {to} and x's type")
+        _, ldy = _matrix(out if len(to) == 2 else out.view(rows, N), "out")
+    lib = capi.load()
+    need = lib.shampoo_mx4_linear_workspace_bytes(rows, N, K)
     ws, ws_ptr = _workspace(need, x)
-    capi.check(capi.shampoo_mx4_linear(flat.data_ptr(), ldx, w.codes_ptr, w.scales_ptr, rows, w.rows, w.cols,
-                                       out.data_ptr(), ldy, xtype, ws_ptr, need, _raw_stream(x.device.index)),
-               "shampoo_mx4_linear")
+    rc = lib.shampoo_mx4_linear(flat.data_ptr(), ldx, w.codes_ptr, w.scales_ptr, rows, N, K, out.data_ptr(), ldy,
+                                xtype, ws_ptr, need, _raw_stream(device.index))
+    if rc:
+        _check(rc, "shampoo_mx4_linear")
     return out
 
 
