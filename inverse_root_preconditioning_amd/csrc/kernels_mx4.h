@@ -73,6 +73,21 @@ struct Mx4Piece<true> {
       }
     }
   }
+  // The piece at (row, col) of a matrix whose edge it may cross, without a branch
+  // on the lane: 8 elements that are there, shifted down, the rest zero.
+  __device__ __forceinline__ void load_edge(const Mx4QuantArgs& P, int64_t row, int64_t col) {
+    if (P.cols < 8) {
+      load(P.x, row * P.ld + col, row < P.rows ? P.cols - col : 0);
+      return;
+    }
+    const int64_t from = min(col, P.cols - 8);
+    const uint32_t d = row < P.rows ? (uint32_t)min<int64_t>(col - from, 8) : 8u;
+    w = ldg_any<u32x4, 2>(static_cast<const uint16_t*>(P.x) + min(row, P.rows - 1) * P.ld + from);
+    if (d & 1) w = u32x4{(w[0] >> 16) | (w[1] << 16), (w[1] >> 16) | (w[2] << 16), (w[2] >> 16) | (w[3] << 16), w[3] >> 16};
+    if (d & 2) w = u32x4{w[1], w[2], w[3], 0};
+    if (d & 4) w = u32x4{w[2], w[3], 0, 0};
+    if (d & 8) w = u32x4{0, 0, 0, 0};
+  }
   // Bits, as fp32, of the largest magnitude.
   __device__ __forceinline__ uint32_t top() const {
     const uint32_t m = max_halves(max_halves(abs_halves(w[0]), abs_halves(w[1])),
@@ -99,6 +114,18 @@ struct Mx4Piece<false> {
       for (int e = 0; e < 4; ++e) w[e] = e < left ? ldg(p + e) : 0.f;
     }
   }
+  __device__ __forceinline__ void load_edge(const Mx4QuantArgs& P, int64_t row, int64_t col) {
+    if (P.cols < 4) {
+      load(P.x, row * P.ld + col, row < P.rows ? P.cols - col : 0);
+      return;
+    }
+    const int64_t from = min(col, P.cols - 4);
+    const uint32_t d = row < P.rows ? (uint32_t)min<int64_t>(col - from, 4) : 4u;
+    w = ldg_any<floatx4, 4>(static_cast<const float*>(P.x) + min(row, P.rows - 1) * P.ld + from);
+    if (d & 1) w = floatx4{w[1], w[2], w[3], 0.f};
+    if (d & 2) w = floatx4{w[2], w[3], 0.f, 0.f};
+    if (d & 4) w = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
   __device__ __forceinline__ uint32_t top() const {
     return max(max(abs_bits(w[0]), abs_bits(w[1])), max(abs_bits(w[2]), abs_bits(w[3])));
   }
@@ -122,10 +149,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantAr
   for (int i = 0; i < kPasses; ++i) {
     const int64_t r = row0 + i * per_pass;
 #pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
-      const int64_t c = col + q * Mx4Piece<BF16>::kElems;
-      x[i][q].load(P.x, r * P.ld + c, r < P.rows ? P.cols - c : 0);
-    }
+    for (int q = 0; q < kPieces; ++q) x[i][q].load_edge(P, r, col + q * Mx4Piece<BF16>::kElems);
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
@@ -148,100 +172,112 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantAr
 // 64 pieces in registers, so that a group along a column lies within a lane
 // and one along a row within 4 (bf16) or 8 lanes.  The 4 waves of a workgroup
 // are stacked, and the 16 bytes that a lane has for a column of the transpose
-// meet its neighbours' in LDS, so that 64 bytes are stored at a time.  Rows up
+// meet their neighbours in LDS, so that 64 bytes are stored at a time.  Rows up
 // to padded_rows are zero groups.
 template <bool BF16, bool ROWS>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4QuantArgs P) {
-  constexpr int V = Mx4Piece<BF16>::kElems, kLanes = kMx4Group / V;
+  constexpr int V = Mx4Piece<BF16>::kElems, kLanes = kMx4Group / V, kCols = kWave * V;
+  constexpr int kPitch = 64;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kCols * (kPitch + 4)];
   const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
-  constexpr int kCols = kWave * V;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kCols * (64 + 4)];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int64_t row0 = (int64_t)rb * 128 + wave * 32, col = ((int64_t)cb * kWave + lane) * V;
-  Mx4Piece<BF16> x[32];
-  if (row0 + 32 <= P.rows && ((int64_t)cb + 1) * kWave * V <= P.cols) {
-#pragma unroll
-    for (int r = 0; r < 32; ++r) x[r].load(P.x, (row0 + r) * P.ld + col, V);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 32; ++r) x[r].load(P.x, (row0 + r) * P.ld + col, row0 + r < P.rows ? P.cols - col : 0);
-  }
-  if constexpr (ROWS) {
-    const int part = lane % kLanes;
-    uint8_t* codes = P.codes + row0 * (P.padded_cols / 2) + col * 4 / 8;
-    uint8_t* scales = P.scales + row0 * (P.padded_cols / kMx4Group) + col / kMx4Group;
-    uint32_t mine = 0;
+  const int64_t base = (int64_t)rb * 128, row0 = base + wave * 32;
+  const int64_t col0 = (int64_t)cb * kCols, col = col0 + lane * V;
+
+  auto quantize = [&](auto WHOLE) __attribute__((always_inline)) {
+    constexpr bool kWhole = decltype(WHOLE)::value;
+    Mx4Piece<BF16> x[32];
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
-      const uint32_t s = mx4_scale(group_max<kLanes>(x[r].top()));
-      uint32_t c = x[r].encode(mx4_scale_float(s));
-      if (s == 255) c = 0;
-      const bool in = row0 + r < P.rows && col < P.padded_cols;
-      if (in) {
-        if constexpr (BF16) {
-          stg(reinterpret_cast<uint32_t*>(codes + r * (P.padded_cols / 2)), c);
-        } else {
-          stg(reinterpret_cast<uint16_t*>(codes + r * (P.padded_cols / 2)), (uint16_t)c);
-        }
-      }
-      // each lane of a group keeps the scale of one of kLanes rows, then all store
-      if (part == r % kLanes) mine = s;
-      if (r % kLanes == kLanes - 1) {
-        const int q = r - (kLanes - 1) + part;
-        if (row0 + q < P.rows && col < P.padded_cols) stg(scales + q * (P.padded_cols / kMx4Group), (uint8_t)mine);
+      if constexpr (kWhole) {
+        x[r].load(P.x, (row0 + r) * P.ld + col, V);
+      } else {
+        x[r].load_edge(P, row0 + r, col);
       }
     }
-  }
-  const int64_t pitch = P.padded_rows / 2, spitch = P.padded_rows / kMx4Group;
-  static_for<V>([&](auto I) __attribute__((always_inline)) {
-    constexpr int i = decltype(I)::value;
-    uint32_t top = 0;
-    u32x4 out;
-    if constexpr (BF16) {
-      uint32_t m = 0;
+    if constexpr (ROWS) {
+      const int part = lane % kLanes;
+      const int64_t pitch = P.padded_cols / 2, spitch = P.padded_cols / kMx4Group;
+      uint8_t* const codes = P.codes + row0 * pitch + col / 2;
+      uint8_t* const scales = P.scales + row0 * spitch + col / kMx4Group;
+      uint32_t mine = 0;
 #pragma unroll
-      for (int r = 0; r < 32; ++r) m = max_halves(m, abs_halves(x[r].w[i / 2]));
-      top = (i & 1) ? m & 0xffff0000u : m << 16;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 32; ++r) top = max(top, abs_bits(x[r].w[i]));
-    }
-    const uint32_t s = mx4_scale(top);
-    const float scale = mx4_scale_float(s);
-    static_for<4>([&](auto D) __attribute__((always_inline)) {
-      constexpr int d = decltype(D)::value;
-      uint32_t c = 0;
-      static_for<4>([&](auto B) __attribute__((always_inline)) {
-        constexpr int b = decltype(B)::value, r = 8 * d + 2 * b;
-        if constexpr (BF16) {
-          // rows r and r + 1 of this column: both low or both high halves
-          const uint32_t pair = __builtin_amdgcn_perm(x[r + 1].w[i / 2], x[r].w[i / 2],
-                                                      (i & 1) ? 0x07060302u : 0x05040100u);
-          c = mx4_codes_bf16<b>(c, pair, scale);
-        } else {
-          c = mx4_codes_f32<b>(c, x[r].w[i], x[r + 1].w[i], scale);
+      for (int r = 0; r < 32; ++r) {
+        if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // keeps the rows' temporaries out of each other's way
+        const uint32_t s = mx4_scale(group_max<kLanes>(x[r].top()));
+        uint32_t c = x[r].encode(mx4_scale_float(s));
+        if (s == 255) c = 0;
+        if (kWhole || (row0 + r < P.rows && col < P.padded_cols)) {
+          if constexpr (BF16) {
+            stg(reinterpret_cast<uint32_t*>(codes + r * pitch), c);
+          } else {
+            stg(reinterpret_cast<uint16_t*>(codes + r * pitch), (uint16_t)c);
+          }
         }
+        // each lane of a group keeps the scale of one of kLanes rows, then all store
+        if (part == r % kLanes) mine = s;
+        if (r % kLanes == kLanes - 1) {
+          const int q = r - (kLanes - 1) + part;
+          if (kWhole || (row0 + q < P.rows && col < P.padded_cols)) stg(scales + q * spitch, (uint8_t)mine);
+        }
+      }
+    }
+    static_for<V>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = decltype(I)::value;
+      uint32_t top = 0;
+      u32x4 out;
+      if constexpr (BF16) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) m = max_halves(m, abs_halves(x[r].w[i / 2]));
+        top = (i & 1) ? m & 0xffff0000u : m << 16;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) top = max(top, abs_bits(x[r].w[i]));
+      }
+      const uint32_t s = mx4_scale(top);
+      const float scale = mx4_scale_float(s);
+      static_for<4>([&](auto D) __attribute__((always_inline)) {
+        constexpr int d = decltype(D)::value;
+        uint32_t c = 0;
+        static_for<4>([&](auto B) __attribute__((always_inline)) {
+          constexpr int b = decltype(B)::value, r = 8 * d + 2 * b;
+          if constexpr (BF16) {
+            // rows r and r + 1 of this column: both low or both high halves
+            const uint32_t pair = __builtin_amdgcn_perm(x[r + 1].w[i / 2], x[r].w[i / 2],
+                                                        (i & 1) ? 0x07060302u : 0x05040100u);
+            c = mx4_codes_bf16<b>(c, pair, scale);
+          } else {
+            c = mx4_codes_f32<b>(c, x[r].w[i], x[r + 1].w[i], scale);
+          }
+        });
+        out[d] = s == 255 ? 0u : c;
       });
-      out[d] = s == 255 ? 0u : c;
+      // at place (wave + lane) % 4 of the column's four: lanes are V columns apart
+      const int c = lane * V + i;
+      *reinterpret_cast<u32x4*>(lds + c * kPitch + 16 * ((wave + lane) & 3)) = out;
+      lds[kCols * kPitch + c * 4 + wave] = (uint8_t)s;
     });
-    // place (wave + lane) % 4 of the column's four: lanes are V columns apart
-    *reinterpret_cast<u32x4*>(lds + (lane * V + i) * 64 + 16 * ((wave + lane) & 3)) = out;
-    lds[kCols * 64 + (lane * V + i) * 4 + wave] = (uint8_t)s;
-  });
-  __syncthreads();
-  const int64_t base = (int64_t)rb * 128, col0 = (int64_t)cb * kCols;
-#pragma unroll
-  for (int q = threadIdx.x; q < kCols * 4; q += 256) {
-    const int c = q / 4, w = q % 4;
-    if (col0 + c < P.cols)
-      stg(reinterpret_cast<u32x4*>(P.codes_t + (col0 + c) * pitch + base / 2 + 16 * w),
-          *reinterpret_cast<const u32x4*>(lds + c * 64 + 16 * ((w + c / V) & 3)));
+  };
+  if (base + 128 <= P.rows && col0 + kCols <= P.cols) {
+    quantize(std::true_type{});
+  } else {
+    quantize(std::false_type{});
   }
-#pragma unroll
-  for (int c = threadIdx.x; c < kCols; c += 256)
+  __syncthreads();
+  const int64_t pitch = P.padded_rows / 2, spitch = P.padded_rows / kMx4Group;
+#pragma unroll 4
+  for (int q = threadIdx.x; q < kCols * 4; q += 256) {
+    const int c = q / 4, u = q % 4;
+    if (col0 + c < P.cols)
+      stg(reinterpret_cast<u32x4*>(P.codes_t + (col0 + c) * pitch + base / 2 + 16 * u),
+          *reinterpret_cast<const u32x4*>(lds + c * kPitch + 16 * ((u + c / V) & 3)));
+  }
+  for (int c = threadIdx.x; c < kCols; c += 256) {
     if (col0 + c < P.cols)
       stg(reinterpret_cast<uint32_t*>(P.scales_t + (col0 + c) * spitch + base / kMx4Group),
-          *reinterpret_cast<const uint32_t*>(lds + kCols * 64 + c * 4));
+          *reinterpret_cast<const uint32_t*>(lds + kCols * kPitch + c * 4));
+  }
 }
 
 struct Mx4DequantArgs {
