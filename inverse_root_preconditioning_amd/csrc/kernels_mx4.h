@@ -31,7 +31,6 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
                                                                 __builtin_bit_cast(u16x2, b)));
 }
 __device__ __forceinline__ uint32_t abs_halves(uint32_t a) { return a & 0x7fff7fffu; }
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
 
 // Byte SEL of `old` replaced by the codes of two values.
 template <int SEL>
@@ -50,88 +49,84 @@ struct Mx4QuantArgs {
   uint8_t *codes, *scales;           // of x
   uint8_t *codes_t, *scales_t;       // of its transpose
   uint32_t col_blocks;
-  int lanes_log2;                    // rows kernel: lanes on a row (8 elements each)
+  int lanes_log2;                    // rows kernel: lanes on a row
 };
 
-// 8 consecutive bf16 (16 bytes) or 4 consecutive floats of a row, those from
-// `left` on as zero.
-template <bool BF16>
-struct Mx4Piece;
-template <>
-struct Mx4Piece<true> {
-  static constexpr int kElems = 8;
-  u32x4 w;
-  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left) {
-    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
-    if (left >= 8) {
-      w = ldg_any<u32x4, 2>(p);
+// V consecutive elements of a row: bf16, two a word, or fp32 bits.
+template <bool BF16, int V>
+struct Mx4Piece {
+  static constexpr int kElems = V, kWords = BF16 ? V / 2 : V;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  Words w;
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    if constexpr (BF16) {
+      w = ldg_any<Words, 2>(static_cast<const uint16_t*>(x) + at);
     } else {
+      w = ldg_any<Words, 4>(static_cast<const float*>(x) + at);
+    }
+  }
+  // The piece at (row, col) of a matrix whose edge it may cross (or pass), zero
+  // outside.  No branch on the lane: V elements that are there, shifted down.
+  __device__ __forceinline__ void load_edge(const void* x, int64_t rows, int64_t cols, int64_t ld, int64_t row,
+                                            int64_t col) {
+    if (cols >= V) {
+      const int64_t from = min(col, cols - V);
+      const uint32_t d = row < rows ? (uint32_t)min<int64_t>(col - from, V) : (uint32_t)V;
+      load(x, min(row, rows - 1) * ld + from);
+      if constexpr (BF16) {
+        if (d & 1) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = 2 * e < left ? ldg(p + 2 * e) : 0u, hi = 2 * e + 1 < left ? ldg(p + 2 * e + 1) : 0u;
-        w[e] = lo | (hi << 16);
+          for (int i = 0; i < kWords; ++i) w[i] = (w[i] >> 16) | (i + 1 < kWords ? w[i + 1] << 16 : 0u);
+        }
+      }
+#pragma unroll
+      for (int b = 1; b < kWords; b *= 2) {
+        if (d & (BF16 ? 2 * b : b)) {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) w[i] = i + b < kWords ? w[i + b] : 0u;
+        }
+      }
+      if (d == V) w = (Words)0u;
+    } else {
+      w = (Words)0u;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (row < rows && col + e < cols) {
+          if constexpr (BF16) {
+            w[e / 2] |= (uint32_t)ldg(static_cast<const uint16_t*>(x) + row * ld + col + e) << (16 * (e & 1));
+          } else {
+            w[e] = ldg(static_cast<const uint32_t*>(x) + row * ld + col + e);
+          }
+        }
       }
     }
   }
-  // The piece at (row, col) of a matrix whose edge it may cross, without a branch
-  // on the lane: 8 elements that are there, shifted down, the rest zero.
-  __device__ __forceinline__ void load_edge(const Mx4QuantArgs& P, int64_t row, int64_t col) {
-    if (P.cols < 8) {
-      load(P.x, row * P.ld + col, row < P.rows ? P.cols - col : 0);
-      return;
-    }
-    const int64_t from = min(col, P.cols - 8);
-    const uint32_t d = row < P.rows ? (uint32_t)min<int64_t>(col - from, 8) : 8u;
-    w = ldg_any<u32x4, 2>(static_cast<const uint16_t*>(P.x) + min(row, P.rows - 1) * P.ld + from);
-    if (d & 1) w = u32x4{(w[0] >> 16) | (w[1] << 16), (w[1] >> 16) | (w[2] << 16), (w[2] >> 16) | (w[3] << 16), w[3] >> 16};
-    if (d & 2) w = u32x4{w[1], w[2], w[3], 0};
-    if (d & 4) w = u32x4{w[2], w[3], 0, 0};
-    if (d & 8) w = u32x4{0, 0, 0, 0};
-  }
   // Bits, as fp32, of the largest magnitude.
   __device__ __forceinline__ uint32_t top() const {
-    const uint32_t m = max_halves(max_halves(abs_halves(w[0]), abs_halves(w[1])),
-                                  max_halves(abs_halves(w[2]), abs_halves(w[3])));
-    return max(m & 0xffff0000u, m << 16);
-  }
-  __device__ __forceinline__ uint32_t encode(float scale) const {
-    uint32_t c = mx4_codes_bf16<0>(0u, w[0], scale);
-    c = mx4_codes_bf16<1>(c, w[1], scale);
-    c = mx4_codes_bf16<2>(c, w[2], scale);
-    return mx4_codes_bf16<3>(c, w[3], scale);
-  }
-};
-template <>
-struct Mx4Piece<false> {
-  static constexpr int kElems = 4;
-  floatx4 w;
-  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left) {
-    const float* p = static_cast<const float*>(x) + at;
-    if (left >= 4) {
-      w = ldg_any<floatx4, 4>(p);
+    uint32_t m = 0;
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max_halves(m, abs_halves(w[i]));
+      return max(m & 0xffff0000u, m << 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = e < left ? ldg(p + e) : 0.f;
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
     }
   }
-  __device__ __forceinline__ void load_edge(const Mx4QuantArgs& P, int64_t row, int64_t col) {
-    if (P.cols < 4) {
-      load(P.x, row * P.ld + col, row < P.rows ? P.cols - col : 0);
-      return;
-    }
-    const int64_t from = min(col, P.cols - 4);
-    const uint32_t d = row < P.rows ? (uint32_t)min<int64_t>(col - from, 4) : 4u;
-    w = ldg_any<floatx4, 4>(static_cast<const float*>(P.x) + min(row, P.rows - 1) * P.ld + from);
-    if (d & 1) w = floatx4{w[1], w[2], w[3], 0.f};
-    if (d & 2) w = floatx4{w[2], w[3], 0.f, 0.f};
-    if (d & 4) w = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
-  __device__ __forceinline__ uint32_t top() const {
-    return max(max(abs_bits(w[0]), abs_bits(w[1])), max(abs_bits(w[2]), abs_bits(w[3])));
-  }
-  __device__ __forceinline__ uint32_t encode(float scale) const {  // two bytes
-    const uint32_t c = mx4_codes_f32<0>(0u, w[0], w[1], scale);
-    return mx4_codes_f32<1>(c, w[2], w[3], scale);
+  // V / 2 bytes of codes.
+  __device__ __forceinline__ uint32_t encode(float scale) const {
+    uint32_t c = 0;
+    static_for<V / 2>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = decltype(I)::value;
+      if constexpr (BF16) {
+        c = mx4_codes_bf16<i>(c, w[i], scale);
+      } else {
+        c = mx4_codes_f32<i>(c, __builtin_bit_cast(float, (uint32_t)w[2 * i]),
+                             __builtin_bit_cast(float, (uint32_t)w[2 * i + 1]), scale);
+      }
+    });
+    return c;
   }
 };
 
@@ -139,27 +134,24 @@ struct Mx4Piece<false> {
 // columns of 4 x 256 / lanes rows.  Memory-bound.
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantArgs P) {
-  constexpr int kPasses = 4, kPieces = 8 / Mx4Piece<BF16>::kElems;
+  constexpr int kPasses = 4;
   const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
   const int lanes = 1 << P.lanes_log2, per_pass = 256 >> P.lanes_log2;
   const int64_t col = ((int64_t)cb * lanes + (threadIdx.x & (lanes - 1))) * 8;
   const int64_t row0 = (int64_t)rb * kPasses * per_pass + (threadIdx.x >> P.lanes_log2);
-  Mx4Piece<BF16> x[kPasses][kPieces];
+  Mx4Piece<BF16, 8> x[kPasses];
+  if (((int64_t)rb + 1) * kPasses * per_pass <= P.rows && ((int64_t)cb + 1) * lanes * 8 <= P.cols) {
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = row0 + i * per_pass;
+    for (int i = 0; i < kPasses; ++i) x[i].load(P.x, (row0 + i * per_pass) * P.ld + col);
+  } else {
 #pragma unroll
-    for (int q = 0; q < kPieces; ++q) x[i][q].load_edge(P, r, col + q * Mx4Piece<BF16>::kElems);
+    for (int i = 0; i < kPasses; ++i) x[i].load_edge(P.x, P.rows, P.cols, P.ld, row0 + i * per_pass, col);
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int64_t r = row0 + i * per_pass;
-    uint32_t top = x[i][0].top();
-    if constexpr (kPieces == 2) top = max(top, x[i][1].top());
-    const uint32_t s = mx4_scale(group_max<4>(top));
-    const float scale = mx4_scale_float(s);
-    uint32_t c = x[i][0].encode(scale);
-    if constexpr (kPieces == 2) c = (c & 0xffffu) | (x[i][1].encode(scale) << 16);
+    const uint32_t s = mx4_scale(group_max<4>(x[i].top()));
+    uint32_t c = x[i].encode(mx4_scale_float(s));
     if (s == 255) c = 0;
     if (r < P.rows && col < P.padded_cols) {
       stg(reinterpret_cast<uint32_t*>(P.codes + r * (P.padded_cols / 2) + col / 2), c);
@@ -169,14 +161,14 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantAr
 }
 
 // Columns, and rows as well with ROWS, from one reading: a wave holds 32 rows of
-// 64 pieces in registers, so that a group along a column lies within a lane
-// and one along a row within 4 (bf16) or 8 lanes.  The 4 waves of a workgroup
+// 64 pieces of V elements in registers, so that a group along a column lies
+// within a lane and one along a row within 32 / V lanes.  The 4 waves of a workgroup
 // are stacked, and the 16 bytes that a lane has for a column of the transpose
 // meet their neighbours in LDS, so that 64 bytes are stored at a time.  Rows up
 // to padded_rows are zero groups.
-template <bool BF16, bool ROWS>
+template <bool BF16, int V, bool ROWS>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4QuantArgs P) {
-  constexpr int V = Mx4Piece<BF16>::kElems, kLanes = kMx4Group / V, kCols = kWave * V;
+  constexpr int kLanes = kMx4Group / V, kCols = kWave * V;
   constexpr int kPitch = 64;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kCols * (kPitch + 4)];
   const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
@@ -186,13 +178,13 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4Quan
 
   auto quantize = [&](auto WHOLE) __attribute__((always_inline)) {
     constexpr bool kWhole = decltype(WHOLE)::value;
-    Mx4Piece<BF16> x[32];
+    Mx4Piece<BF16, V> x[32];
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
       if constexpr (kWhole) {
-        x[r].load(P.x, (row0 + r) * P.ld + col, V);
+        x[r].load(P.x, (row0 + r) * P.ld + col);
       } else {
-        x[r].load_edge(P, row0 + r, col);
+        x[r].load_edge(P.x, P.rows, P.cols, P.ld, row0 + r, col);
       }
     }
     if constexpr (ROWS) {
@@ -208,10 +200,12 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4Quan
         uint32_t c = x[r].encode(mx4_scale_float(s));
         if (s == 255) c = 0;
         if (kWhole || (row0 + r < P.rows && col < P.padded_cols)) {
-          if constexpr (BF16) {
+          if constexpr (V == 8) {
             stg(reinterpret_cast<uint32_t*>(codes + r * pitch), c);
-          } else {
+          } else if constexpr (V == 4) {
             stg(reinterpret_cast<uint16_t*>(codes + r * pitch), (uint16_t)c);
+          } else {
+            stg(codes + r * pitch, (uint8_t)c);
           }
         }
         // each lane of a group keeps the scale of one of kLanes rows, then all store
@@ -233,7 +227,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4Quan
         top = (i & 1) ? m & 0xffff0000u : m << 16;
       } else {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) top = max(top, abs_bits(x[r].w[i]));
+        for (int r = 0; r < 32; ++r) top = max(top, x[r].w[i] & 0x7fffffffu);
       }
       const uint32_t s = mx4_scale(top);
       const float scale = mx4_scale_float(s);
@@ -248,7 +242,8 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_cols_kernel(const Mx4Quan
                                                         (i & 1) ? 0x07060302u : 0x05040100u);
             c = mx4_codes_bf16<b>(c, pair, scale);
           } else {
-            c = mx4_codes_f32<b>(c, x[r].w[i], x[r + 1].w[i], scale);
+            c = mx4_codes_f32<b>(c, __builtin_bit_cast(float, (uint32_t)x[r].w[i]),
+                                 __builtin_bit_cast(float, (uint32_t)x[r + 1].w[i]), scale);
           }
         });
         out[d] = s == 255 ? 0u : c;
@@ -288,20 +283,25 @@ struct Mx4DequantArgs {
   int lanes_log2;
 };
 
-// 8 codes a lane, the rows kernel's shape.
+// 16 bytes of output a lane (8 bf16, 4 floats), the rows kernel's shape.
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs P) {
-  constexpr int kPasses = 4;
+  constexpr int kPasses = 4, E = BF16 ? 8 : 4;
   const uint32_t rb = blockIdx.x / P.col_blocks, cb = blockIdx.x - rb * P.col_blocks;
   const int lanes = 1 << P.lanes_log2, per_pass = 256 >> P.lanes_log2;
-  const int64_t col = ((int64_t)cb * lanes + (threadIdx.x & (lanes - 1))) * 8;
+  const int64_t col = ((int64_t)cb * lanes + (threadIdx.x & (lanes - 1))) * E;
   const int64_t row0 = (int64_t)rb * kPasses * per_pass + (threadIdx.x >> P.lanes_log2);
   if (col >= P.cols) return;
   uint32_t c[kPasses], s[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int64_t r = min(row0 + i * per_pass, P.rows - 1);
-    c[i] = ldg(reinterpret_cast<const uint32_t*>(P.codes + r * (P.padded / 2) + col / 2));
+    const uint8_t* const from = P.codes + r * (P.padded / 2) + col / 2;
+    if constexpr (BF16) {
+      c[i] = ldg(reinterpret_cast<const uint32_t*>(from));
+    } else {
+      c[i] = ldg(reinterpret_cast<const uint16_t*>(from));
+    }
     s[i] = ldg(P.scales + r * (P.padded / kMx4Group) + col / kMx4Group);
   }
 #pragma unroll
@@ -313,35 +313,34 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArg
     const int64_t at = r * P.ld + col;
     if constexpr (BF16) {
       u32x4 w;
-      w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 0));
-      w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 1));
-      w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 2));
-      w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, 3));
+      static_for<4>([&](auto B) __attribute__((always_inline)) {
+        constexpr int b = decltype(B)::value;
+        w[b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], scale, b));
+      });
       if (bad) w = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
       uint16_t* const o = static_cast<uint16_t*>(P.out) + at;
-      if (col + 8 <= P.cols) {
+      if (col + E <= P.cols) {
         stg_any<u32x4, 2>(o, w);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < E; ++e)
           if (col + e < P.cols) stg(o + e, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
       }
     } else {
-      floatx4 v[2];
-      static_for<4>([&](auto B) __attribute__((always_inline)) {
+      floatx4 v;
+      static_for<2>([&](auto B) __attribute__((always_inline)) {
         constexpr int b = decltype(B)::value;
         const f32x2_t t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], scale, b);
-        v[b / 2][2 * (b & 1)] = bad ? __builtin_nanf("") : t[0];
-        v[b / 2][2 * (b & 1) + 1] = bad ? __builtin_nanf("") : t[1];
+        v[2 * b] = bad ? __builtin_nanf("") : t[0];
+        v[2 * b + 1] = bad ? __builtin_nanf("") : t[1];
       });
       float* const o = static_cast<float*>(P.out) + at;
-      if (col + 8 <= P.cols) {
-        stg_any<floatx4, 4>(o, v[0]);
-        stg_any<floatx4, 4>(o + 4, v[1]);
+      if (col + E <= P.cols) {
+        stg_any<floatx4, 4>(o, v);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (col + e < P.cols) stg(o + e, v[e / 4][e & 3]);
+        for (int e = 0; e < E; ++e)
+          if (col + e < P.cols) stg(o + e, v[e]);
       }
     }
   }
@@ -790,23 +789,12 @@ __global__ void __launch_bounds__(256) mx4_few_rows_kernel(const Mx4FewArgs Q) {
   if (first) load_whole(s0);
   if constexpr (AM != MX4_A_MX4) {
     // 8 elements a lane, 4 lanes a group
-    constexpr bool kBf16 = AM == MX4_A_BF16;
-    constexpr int kPieces = 8 / Mx4Piece<kBf16>::kElems;
     const int per_row = (int)(P.padded / 8), pieces = (int)P.M * per_row;
     for (int q = threadIdx.x; q < pieces; q += 256) {
       const int row = q / per_row, k = (q - row * per_row) * 8;
-      Mx4Piece<kBf16> x[kPieces];
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int c = k + i * Mx4Piece<kBf16>::kElems;
-        x[i].load(Q.x, row * Q.ldx + c, Q.K - c);
-        top = max(top, x[i].top());
-      }
-      const uint32_t s = mx4_scale(group_max<4>(top));
-      const float scale = mx4_scale_float(s);
-      uint32_t c = x[0].encode(scale);
-      if constexpr (kPieces == 2) c = (c & 0xffffu) | (x[1].encode(scale) << 16);
+      Mx4Piece<AM == MX4_A_BF16, 8> x;
+      x.load_edge(Q.x, P.M, Q.K, Q.ldx, row, k);
+      const uint32_t s = mx4_scale(group_max<4>(x.top())), c = x.encode(mx4_scale_float(s));
       *reinterpret_cast<uint32_t*>(qa + 4 * q) = s == 255 ? 0u : c;
       if ((q & 3) == 0) qa[kMx4FewElems / 2 + q / 4] = (uint8_t)s;
     }

@@ -31,14 +31,16 @@ __device__ __forceinline__ void stg_once(void* p, const V& v) {
   __builtin_nontemporal_store(v, (__attribute__((address_space(1))) U*)p);
 }
 
-// Largest of v over groups of 4 (8) consecutive lanes, in every lane.
+// Largest of v over groups of 4, 8 or 16 consecutive lanes, in every lane.
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  static_assert(LANES == 4 || LANES == 8, "lanes of a group");
+  static_assert(LANES == 4 || LANES == 8 || LANES == 16, "lanes of a group");
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));  // quad_perm 1 0 3 2
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));  // quad_perm 2 3 0 1
-  if constexpr (LANES == 8)
+  if constexpr (LANES >= 8)
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror
+  if constexpr (LANES == 16)
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true));  // row_mirror
   return v;
 }
 
