@@ -131,7 +131,8 @@ struct Mx4Piece {
 };
 
 // Rows only: 8 elements a lane, 4 lanes a group; a workgroup takes `lanes` x 8
-// columns of 4 x 256 / lanes rows.  Memory-bound.
+// columns of 4 x 256 / lanes rows.  Memory-bound: 16384 x 8192 bf16 in 60 us
+// (5.6 TB/s).
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantArgs P) {
   constexpr int kPasses = 4;
@@ -284,6 +285,8 @@ struct Mx4DequantArgs {
 };
 
 // 16 bytes of output a lane (8 bf16, 4 floats), the rows kernel's shape.
+// Memory-bound: 16384 x 8192 to bf16 in 62 us (5.5 TB/s), to fp32 in 106 us
+// (5.8; 153 us with 8 floats a lane, half cache lines a store).
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs P) {
   constexpr int kPasses = 4, E = BF16 ? 8 : 4;
@@ -392,6 +395,14 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 //  - B is the MFMA's first operand and its rows are assigned to MFMA rows so
 //    that a lane ends with 16 consecutive columns of one row of C.  Each wave
 //    turns its 32-row slices through LDS into stores of whole rows.
+//
+// Measured, 16384 x 2048 x 8192 to bf16: 134 us, 4.1 PFLOP/s, matrix cores busy
+// half of the cycles.  It is bound by power: the same MFMAs fed from registers
+// reach 9.0 PFLOP/s on zeros but 5.9 on random operands (the clock falls from
+// 2.4 to 1.4 GHz), and 8 waves a tile, which take 5% fewer cycles, take the
+// same time.  8192 x 8192 x 2048: 88 us (3.1), a quarter of it each tile's first
+// loads and its output, which nothing overlaps.  1024 x 1024 x 4096 on 64 x 64
+// tiles: 8.3 us, 1.3 us for 1024 columns.
 // ---------------------------------------------------------------------------
 constexpr int kMx4Chunk = 256;              // columns
 constexpr int kMx4RowBytes = kMx4Chunk / 2;
@@ -721,7 +732,9 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
 // of 4 BATCH bytes a row: read byte by byte they cost as many cache lines as
 // the codes.  A may still be fp32 or bf16 (at most kMx4FewElems elements): then
 // the workgroup quantises it into LDS while its first rows of B are on their
-// way, which saves a launch and A's way through memory.
+// way, which saves a launch and A's way through memory.  Measured, one bf16 row
+// by 8192 x 2048: 3.6 us (a launch alone takes 2), by 8192 x 8192: 8.4 us
+// (4.2 TB/s); 16 rows by 8192 x 8192, B read for two tiles at a time: 10.3 us.
 // ---------------------------------------------------------------------------
 enum { MX4_A_MX4 = 0, MX4_A_F32 = 1, MX4_A_BF16 = 2 };
 constexpr int kMx4FewElems = 16384;
@@ -857,7 +870,8 @@ __global__ void __launch_bounds__(256) mx4_few_rows_kernel(const Mx4FewArgs Q) {
   }
 }
 
-// C = alpha sum + beta C over the partial products of a split, in their order.
+// C = alpha sum + beta C over the partial products of a split, in their order:
+// 2.5 us with its launch; 64 x 2048 x 8192 takes 6.7 us in 8 splits, 13.5 in one.
 struct Mx4SumArgs {
   Mx4ProductArgs p;
   const float* parts;  // [splits][M][N]

@@ -12,6 +12,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import capi
 from .adamw import _TYPES, _raw_stream
@@ -240,6 +241,7 @@ class _TrainLinear(torch.autograd.Function):
         return product(xq, wq, dtype=x.dtype).view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad
         q, qt = _quantize(_flat(dy), need_x, need_w)
