@@ -357,7 +357,7 @@ typedef struct shampoo_segment {
 } shampoo_segment;
 
 #define SHAMPOO_GROUP 32       /* elements that share a scale byte */
-#define SHAMPOO_SEGMENT 4096
+#define SHAMPOO_SEGMENT 2048
 
 /*
  * shampoo_grad_norm -- Euclidean norm of many tensors taken as one vector.

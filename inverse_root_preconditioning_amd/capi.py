@@ -55,7 +55,7 @@ T_BF16 = 1
 STATE_F32 = 0
 STATE_MX8 = 1
 GROUP = 32                # elements that share a scale byte
-SEGMENT = 4096
+SEGMENT = 2048
 MX4_PAD = 128             # columns of an MX4 matrix are padded to a multiple of this
 
 ABI_VERSION = 3

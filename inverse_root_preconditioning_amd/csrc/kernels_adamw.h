@@ -1,5 +1,5 @@
 // AdamW over many tensors and the norm of many tensors: HBM-bound kernels that
-// walk a list of 4096-element segments, one workgroup a segment.
+// walk a list of 2048-element segments.
 #pragma once
 
 #include "vector_io.h"
@@ -143,15 +143,17 @@ struct AdamwArgs {
   uint32_t key;
 };
 
-// One workgroup a segment, everything read and written once and past the
-// caches.  A lane takes 4 consecutive elements, or 8 where all but the 8-bit
-// moments are bf16 (16 bytes either way: 8 floats a lane would read half cache
-// lines).  The square root and the reciprocal are the hardware's (1 ulp): they
-// reach the parameter only, far below its rounding.
+// One workgroup a segment (of 2048: 4096 are 1 to 5% slower on large sets and 14%
+// on 2700 of them, whose last workgroups then leave the GPU half empty),
+// everything read and written once and past the caches.  A lane takes 4
+// consecutive elements, or 8 where all but the 8-bit moments are bf16 (16 bytes
+// either way: 8 floats a lane would read half cache lines).  The square root
+// and the reciprocal are the hardware's (1 ulp): they reach the parameter only,
+// far below its rounding.
 //
 // HBM-bound.  302e6 parameters: fp32 throughout 1.48 ms (5.7 TB/s, the rate of a
-// large copy; 1.58 ms through the caches), bf16 with 8-bit moments 0.55 ms
-// (5.5 TB/s; 5% more with 4 elements a lane).
+// large copy; 1.58 ms through the caches), bf16 with 8-bit moments 0.52 ms
+// (5.9 TB/s; 5% more with 4 elements a lane).
 template <bool PARAM_BF16, bool GRAD_BF16, bool MX8, bool COPY>
 __global__ void __launch_bounds__(256) adamw_kernel(const AdamwArgs P) {
 // Which operations are fused is written out: the codes that the moments round
@@ -348,36 +350,57 @@ __global__ void __launch_bounds__(256) grad_norm_partial_kernel(const shampoo_te
                                                                 const shampoo_segment* segments, int64_t nseg,
                                                                 double* partial) {
   __shared__ double red[4];
-  constexpr int V = BF16 ? 8 : 4, kRounds = kSegment / (256 * V);
+  // kSegs segments at a time: 16 bytes a lane twice, whatever the type
+  constexpr int V = BF16 ? 8 : 4, kRounds = kSegment / (256 * V), kSegs = 2 / kRounds;
+  static_assert(kSegs * kRounds == 2, "two loads a lane");
   const int64_t s0 = nseg * blockIdx.x / gridDim.x, s1 = nseg * (blockIdx.x + 1) / gridDim.x;
   double sum[2] = {0., 0.};
-  shampoo_segment seg = segments[s0];  // every block has one: gridDim.x <= nseg
-  shampoo_tensor t = tensors[seg.tensor];
-  for (int64_t s = s0; s < s1; ++s) {
-    const int64_t first = (int64_t)seg.index * kSegment;
-    const int len = (int)min((int64_t)kSegment, t.n - first);
-    const void* const p = t.ptr;
-    float x[kRounds][V];
-    if (len == kSegment) {
+  shampoo_segment seg[kSegs];
+  shampoo_tensor t[kSegs];
+  auto describe = [&](int64_t s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kSegs; ++k) {
+      seg[k] = segments[min(s + k, nseg - 1)];
+      t[k] = tensors[seg[k].tensor];
+    }
+  };
+  describe(s0);
+  for (int64_t s = s0; s < s1; s += kSegs) {
+    float x[kSegs][kRounds][V];
+    int64_t first[kSegs];
+    int len[kSegs];
+    bool whole = true;
+#pragma unroll
+    for (int k = 0; k < kSegs; ++k) {
+      first[k] = (int64_t)seg[k].index * kSegment;
+      len[k] = s + k < s1 ? (int)min((int64_t)kSegment, t[k].n - first[k]) : 0;
+      whole = whole && len[k] == kSegment;
+    }
+    // one branch for all: each would wait for its loads where it ends
+    auto load = [&](auto WHOLE) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < kSegs; ++k)
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          const int i = (r * 256 + (int)threadIdx.x) * V;
+          load_elems<BF16, V, decltype(WHOLE)::value>(t[k].ptr, first[k] + i, len[k] - i, x[k][r]);
+        }
+    };
+    if (whole) {
+      load(std::true_type{});
+    } else {
+      load(std::false_type{});
+    }
+    describe(s + kSegs);  // the next descriptors, under these loads
+#pragma unroll
+    for (int k = 0; k < kSegs; ++k)
 #pragma unroll
       for (int r = 0; r < kRounds; ++r)
-        load_elems<BF16, V, true>(p, first + (r * 256 + (int)threadIdx.x) * V, V, x[r]);
-    } else {
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int i = (r * 256 + (int)threadIdx.x) * V;
-        load_elems<BF16, V, false>(p, first + i, len - i, x[r]);
-      }
-    }
-    seg = segments[min(s + 1, nseg - 1)];  // the next descriptor, under this segment's loads
-    t = tensors[seg.tensor];
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const double g = x[r][e];
-        sum[e & 1] = __builtin_fma(g, g, sum[e & 1]);
-      }
+        for (int e = 0; e < V; ++e) {
+          const double g = x[k][r][e];
+          sum[e & 1] = __builtin_fma(g, g, sum[e & 1]);
+        }
   }
   const double total = block_sum_f64<256>(sum[0] + sum[1], red);
   if (threadIdx.x == 0) stg(partial + blockIdx.x, total);
