@@ -395,14 +395,19 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 //  - B is the MFMA's first operand and its rows are assigned to MFMA rows so
 //    that a lane ends with 16 consecutive columns of one row of C.  Each wave
 //    turns its 32-row slices through LDS into stores of whole rows.
+//  - A workgroup of the 256-tile stays on its compute unit and takes every 256th
+//    tile where the columns are whole scale blocks of 1024: the loads ahead of a
+//    tile's last chunks are the next tile's, and its stores end under the next
+//    tile's MFMAs (8192 x 8192 x 2048 92 -> 83 us, 8190 x 8190 x 2048 103 -> 88,
+//    16384 x 2048 x 8192 129.5 -> 126).
 //
-// Measured, 16384 x 2048 x 8192 to bf16: 134 us, 4.1 PFLOP/s, matrix cores busy
+// Measured, 16384 x 2048 x 8192 to bf16: 126 us, 4.4 PFLOP/s, matrix cores busy
 // half of the cycles.  It is bound by power: the same MFMAs fed from registers
 // reach 9.0 PFLOP/s on zeros but 5.9 on random operands (the clock falls from
 // 2.4 to 1.4 GHz), and 8 waves a tile, which take 5% fewer cycles, take the
-// same time.  8192 x 8192 x 2048: 88 us (3.1), a quarter of it each tile's first
-// loads and its output, which nothing overlaps.  1024 x 1024 x 4096 on 64 x 64
-// tiles: 8.3 us, 1.3 us for 1024 columns.
+// same time.  8192 x 8192 x 2048: 83 us (3.3), whose 128 MiB of output take 25
+// by themselves.  1024 x 1024 x 4096 on 64 x 64 tiles: 8.3 us, 1.3 us for 1024
+// columns.
 // ---------------------------------------------------------------------------
 constexpr int kMx4Chunk = 256;              // columns
 constexpr int kMx4RowBytes = kMx4Chunk / 2;
@@ -479,6 +484,11 @@ __device__ __forceinline__ void mx4_store4(const Mx4ProductArgs& P, int64_t m, i
   }
 }
 
+// Whether a workgroup goes on from tile to tile.  With beta the old values of C
+// and the next tile's fragments together pass 512 registers (ten times slower);
+// of smaller tiles several workgroups share a compute unit, and overlap anyway.
+constexpr bool mx4_streams(int T, bool beta) { return T == 4 && !beta; }
+
 template <int T, bool BF16, bool BETA>
 __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArgs P) {
   constexpr int BT = 64 * T, NT = 256;                         // tile edge, threads
@@ -486,39 +496,65 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
   constexpr int kScale = BT * 4 * kMx4ScaleDwords;             // one operand's scale block
   constexpr int LD = kData / (NT * 16);                       // 16-byte loads a thread, operand and chunk
   constexpr int LS = kScale / 2 / (NT * 4);                    // 4-byte scale loads likewise
-  constexpr int kSlice = 32 * T + 4;                          // floats: pitch of a wave's output slice
+  constexpr int kSlice = T > 1 ? 64 : 32;                     // columns of a wave's output slice
   constexpr int kLds = 2 * kStage + 4 * kScale;
   static_assert(LD * NT * 16 == kData && LS * NT * 8 == kScale, "chunking");
-  static_assert(4 * 32 * kSlice * 4 <= kLds && kLds <= 160 * 1024, "fits the LDS");
+  constexpr bool kStream = mx4_streams(T, BETA);              // a workgroup may take several tiles
+  static_assert(4 * 32 * kSlice * 4 <= (kStream ? kData : kLds) && kLds <= 160 * 1024, "fits the LDS");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
 
   // Tiles in groups of 8 tile rows, column by column within a group: the 32
   // tiles that an XCD runs at a time share 8 panels of A and 4 of B.
-  const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const uint32_t group = id / (8 * P.tiles_n), in_group = id - group * (8 * P.tiles_n);
-  const uint32_t rows_here = min(8u, P.tiles_m - 8 * group);
-  const int64_t m0 = (int64_t)(8 * group + in_group % rows_here) * BT, n0 = (int64_t)(in_group / rows_here) * BT;
+  const uint32_t tiles = P.tiles_m * P.tiles_n;
+  int64_t m0, n0;      // the tile that is multiplied
+  int64_t lm, ln;      // the tile that is loaded next
+  auto place = [&](uint32_t tile, int64_t& m, int64_t& n) __attribute__((always_inline)) {
+    const uint32_t id = xcd_remap(tile, tiles);
+    const uint32_t group = id / (8 * P.tiles_n), in_group = id - group * (8 * P.tiles_n);
+    const uint32_t rows_here = min(8u, P.tiles_m - 8 * group);
+    m = (int64_t)(8 * group + in_group % rows_here) * BT;
+    n = (int64_t)(in_group / rows_here) * BT;
+  };
+  uint32_t tile = blockIdx.x;
+  place(tile, m0, n0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * 32 * T, wn = (wave & 1) * 32 * T;
   const int r32 = lane & 31, h = lane >> 5;
 
   const uint32_t pitch = (uint32_t)(P.padded / 2), spitch = (uint32_t)(P.padded / kMx4Group);
-  const uint8_t* const A = P.a + m0 * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
-  const uint8_t* const B = P.b + n0 * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
-  const uint8_t* const As = P.as + m0 * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
-  const uint8_t* const Bs = P.bs + n0 * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
-  const int ma = (int)min<int64_t>(BT, P.M - m0) - 1, nb = (int)min<int64_t>(BT, P.N - n0) - 1;  // last valid rows
-
+  const uint8_t *A, *B, *As, *Bs;
+  int ma, nb;  // last valid rows, for the scales
   // Piece c of an operand's chunk: row c / 8, permuted 16-byte column c % 8.
   // Rows past the last one repeat it; they end in rows of C that are not stored.
   uint32_t offA[LD], offB[LD];
+  auto aim_a = [&](int64_t m) __attribute__((always_inline)) {
+    A = P.a + m * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
+    const int limit = (int)min<int64_t>(BT, P.M - m) - 1;
 #pragma unroll
-  for (int it = 0; it < LD; ++it) {
-    const int c = it * NT + tid, row = c >> 3;
-    offA[it] = (uint32_t)min(row, ma) * pitch + 16 * ((c & 7) ^ mx4_swz_a(row));
-    offB[it] = (uint32_t)min(row, nb) * pitch + 16 * ((c & 7) ^ mx4_swz_b(row));
-  }
+    for (int it = 0; it < LD; ++it) {
+      const int c = it * NT + tid, row = c >> 3;
+      offA[it] = (uint32_t)min(row, limit) * pitch + 16 * ((c & 7) ^ mx4_swz_a(row));
+    }
+  };
+  auto aim_b = [&](int64_t n) __attribute__((always_inline)) {
+    B = P.b + n * pitch + (int64_t)blockIdx.y * P.split_blocks * 512;
+    const int limit = (int)min<int64_t>(BT, P.N - n) - 1;
+#pragma unroll
+    for (int it = 0; it < LD; ++it) {
+      const int c = it * NT + tid, row = c >> 3;
+      offB[it] = (uint32_t)min(row, limit) * pitch + 16 * ((c & 7) ^ mx4_swz_b(row));
+    }
+  };
+  auto aim_scales = [&](int64_t m, int64_t n) __attribute__((always_inline)) {
+    As = P.as + m * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
+    Bs = P.bs + n * spitch + (int64_t)blockIdx.y * P.split_blocks * 32;
+    ma = (int)min<int64_t>(BT, P.M - m) - 1;
+    nb = (int)min<int64_t>(BT, P.N - n) - 1;
+  };
+  aim_a(m0);
+  aim_b(n0);
+  aim_scales(m0, n0);
   // This split's 128-column halves of chunks, and its whole chunks.
   const int steps = min((int)(P.padded / 128) - (int)blockIdx.y * P.split_blocks * 8, P.split_blocks * 8);
   const int full = steps / 2;
@@ -532,15 +568,15 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
 #pragma unroll
     for (int it = 0; it < LD; ++it) to_lds16(b + offB[it], lds + buf + kData + (it * NT + wave * 64) * 16);
   };
-  // Quarter q of scale block blk: 32 T rows of A (q = 0, 1) or B.  Dword p of a
-  // row goes to place p ^ 2 ((row / 8) % 4), so that the rows of a read, 8
+  // Quarter q of scale block blk, to the place of blocks of its parity: 32 T rows
+  // of A (q = 0, 1) or B.  Dword p of a row goes to place p ^ 2 ((row / 8) % 4), so that the rows of a read, 8
   // dwords apart, spread over the banks.
   const int last = steps - 1;
-  auto issue_scales = [&](int blk, int q) __attribute__((always_inline)) {
+  auto issue_scales = [&](int blk, int parity, int q) __attribute__((always_inline)) {
     const uint8_t* const from = q < 2 ? As : Bs;
     const int limit = q < 2 ? ma : nb;
     const uint32_t col = 4 * min(blk * kMx4ScaleDwords + ((tid & 7) ^ (2 * wave)), last);
-    uint8_t* const to = lds + 2 * kStage + (blk & 1) * 2 * kScale;
+    uint8_t* const to = lds + 2 * kStage + (parity & 1) * 2 * kScale;
 #pragma unroll
     for (int it = 0; it < LS; ++it) {
       const uint32_t row = (uint32_t)min(((q & 1) * LS + it) * (NT / 8) + (tid >> 3), limit);
@@ -595,7 +631,8 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
 #pragma unroll
     for (int j = 0; j < T; ++j) sb[j] = *reinterpret_cast<const int*>(lds + base + scaleB + j * kBlockScales + pb);
   };
-  constexpr int kWaitAll = 0 | (7 << 4);  // vmcnt(0) lgkmcnt(0)
+  constexpr int kWaitAll = 0 | (7 << 4);            // vmcnt(0) lgkmcnt(0)
+  constexpr int kWaitLds = 0xc00f | (7 << 4);       // lgkmcnt(0)
   auto meet = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(kWaitAll);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -607,12 +644,12 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     issue_a(0, 0);
     issue_b(0, 0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) issue_scales(0, q);
+    for (int q = 0; q < 4; ++q) issue_scales(0, 0, q);
   }
   if (steps & 1) {
     issue_half(kStage);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) issue_scales((full / 4) | 1, q);  // odd: block 1's place; clamped to the last dword
+    for (int q = 0; q < 4; ++q) issue_scales((full / 4) | 1, 1, q);  // clamped to the last dword
   }
   meet();
   if (steps & 1) {  // lane half h takes groups 2 h and 2 h + 1
@@ -631,14 +668,30 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     });
     meet();
   }
+  int cur = 0, block = 0;  // buffer of the next chunk; scale blocks before this tile's
   if (full > 0) {
-    // Loads past the last chunk repeat it into the buffer that nothing reads any more.
     issue_a(kStage, min(1, full - 1));
-    int cur = 0;
     read_scales(0, h);
     read(0, 0, 4 * h);
+  }
+  for (;;) {
+    // The chunks of this workgroup's tiles are one stream: the loads that run
+    // ahead of a tile's last chunks are the next tile's first ones (its own first
+    // ones again after the last tile, into buffers that nothing reads any more).
+    const uint32_t next = tile + gridDim.x;
+    const bool more = kStream && next < tiles;
+    lm = m0;
+    ln = n0;
+    if (more) place(next, lm, ln);
     for (int c = 0; c < full; ++c) {
+      if constexpr (kStream) {
+        if (c + 4 == full) aim_scales(lm, ln);
+        if (c + 2 == full) aim_a(lm);
+        if (c + 1 == full) aim_b(ln);
+      }
       const int other = kStage - cur;
+      const int ahead1 = c + 1 < full ? c + 1 : 0, ahead2 = min(c + 2 < full ? c + 2 : c + 2 - full, full - 1);
+      const int ahead_scales = 4 * (c / 4 + 1) < full ? c / 4 + 1 : 0;
       int ta[T], tb[T];
 #pragma unroll
       for (int i = 0; i < T; ++i) ta[i] = sa[i];
@@ -648,14 +701,14 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
         constexpr int s = decltype(S)::value;
         constexpr int kReads = 2 * T, kMfma = T * T;
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (s == 0) issue_b(other, min(c + 1, full - 1));
-        if constexpr (s == 1) issue_scales(c / 4 + 1, c % 4);
+        if constexpr (s == 0) issue_b(other, ahead1);
+        if constexpr (s == 1) issue_scales(ahead_scales, block + c / 4 + 1, c % 4);
         if constexpr (s < 3) {
           read(cur, (s + 1) & 1, 4 * h + s + 1);
         } else {
           meet();
-          issue_a(cur, min(c + 2, full - 1));
-          read_scales((c + 1) / 4, 2 * ((c + 1) % 4) + h);
+          issue_a(cur, ahead2);
+          read_scales(block + (c + 1) / 4, 2 * ((c + 1) % 4) + h);
           read(other, 0, 4 * h);
         }
 #pragma unroll
@@ -676,50 +729,78 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
       });
       cur = other;
     }
-  }
 
-  // Output: 32 rows of C at a time through this wave's slice of LDS.
-  meet();
-  float* const slice = reinterpret_cast<float*>(lds) + wave * 32 * kSlice;
-  auto output = [&](auto WHOLE) __attribute__((always_inline)) {
-    constexpr bool kWhole = decltype(WHOLE)::value;
-    constexpr int kLanes = 8 * T, kRows = 64 / kLanes, kIter = 32 / kRows;  // kLanes lanes hold a row, 4 elements each
-    const int col = 4 * (lane % kLanes), row0 = lane / kLanes;
-    const int64_t n = n0 + wn + col;
+    // Output: 32 rows of kSlice columns of C at a time through this wave's slice
+    // of LDS, 16-byte pieces permuted by the row.  A stream's slices lie in B's
+    // half of the last chunk's buffer: the next tile's loads reach it only after
+    // the barrier below.
+    if constexpr (!kStream) meet();
+    uint8_t* const slice = lds + (kStream ? kStage - cur + kData : 0) + wave * 32 * kSlice * 4;
+    auto output = [&](auto WHOLE) __attribute__((always_inline)) {
+      constexpr bool kWhole = decltype(WHOLE)::value;
+      constexpr int kLanes = kSlice / 4, kRows = 64 / kLanes, kIter = 32 / kRows;  // kLanes lanes hold a row, 4 elements each
+      const int piece = lane % kLanes, row0 = lane / kLanes;
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      const int64_t mi = m0 + wm + 32 * i + row0, split = (int64_t)blockIdx.y * P.M;
-      // all of C's loads first: none can pass a store
-      floatx4 old[BETA ? kIter : 1];
-      if constexpr (BETA) {
+      for (int i = 0; i < T; ++i) {
 #pragma unroll
-        for (int r = 0; r < kIter; ++r)
-          if (kWhole || (mi + r * kRows < P.M && n < P.N)) old[r] = mx4_load4<BF16, kWhole>(P, mi + r * kRows, n);
+        for (int part = 0; part < 32 * T / kSlice; ++part) {
+          const int64_t n = n0 + wn + part * kSlice + 4 * piece;
+          const int64_t mi = m0 + wm + 32 * i + row0, split = (int64_t)blockIdx.y * P.M;
+          // all of C's loads first: none can pass a store
+          floatx4 old[BETA ? kIter : 1];
+          if constexpr (BETA) {
+#pragma unroll
+            for (int r = 0; r < kIter; ++r)
+              if (kWhole || (mi + r * kRows < P.M && n < P.N)) old[r] = mx4_load4<BF16, kWhole>(P, mi + r * kRows, n);
+          }
+#pragma unroll
+          for (int jj = 0; jj < kSlice / 32; ++jj) {
+            const int j = part * (kSlice / 32) + jj;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<floatx4*>(slice + r32 * kSlice * 4 + 16 * ((8 * jj + 4 * h + q) ^ (r32 & (kLanes - 1)))) =
+                  floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          }
+          floatx4 v[kIter];
+#pragma unroll
+          for (int r = 0; r < kIter; ++r) {
+            const int row = r * kRows + row0;
+            v[r] = *reinterpret_cast<const floatx4*>(slice + row * kSlice * 4 + 16 * (piece ^ (row & (kLanes - 1))));
+          }
+#pragma unroll
+          for (int r = 0; r < kIter; ++r) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[r][e] *= P.alpha;
+              if constexpr (BETA) v[r][e] += P.beta * old[r][e];
+            }
+            if (kWhole || (mi + r * kRows < P.M && n < P.N)) mx4_store4<BF16, kWhole>(P, split + mi + r * kRows, n, v[r]);
+          }
+        }
       }
+    };
+    if (m0 + BT <= P.M && n0 + BT <= P.N) {
+      output(std::true_type{});
+    } else {
+      output(std::false_type{});
+    }
+    if (!more) return;
+
+#pragma unroll
+    for (int i = 0; i < T; ++i)
 #pragma unroll
       for (int j = 0; j < T; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<floatx4*>(slice + r32 * kSlice + 32 * j + 16 * h + 4 * q) =
-              floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-      floatx4 v[kIter];
-#pragma unroll
-      for (int r = 0; r < kIter; ++r) v[r] = *reinterpret_cast<const floatx4*>(slice + (r * kRows + row0) * kSlice + col);
-#pragma unroll
-      for (int r = 0; r < kIter; ++r) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[r][e] *= P.alpha;
-          if constexpr (BETA) v[r][e] += P.beta * old[r][e];
-        }
-        if (kWhole || (mi + r * kRows < P.M && n < P.N)) mx4_store4<BF16, kWhole>(P, split + mi + r * kRows, n, v[r]);
-      }
-    }
-  };
-  if (m0 + BT <= P.M && n0 + BT <= P.N) {
-    output(std::true_type{});
-  } else {
-    output(std::false_type{});
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    tile = next;
+    m0 = lm;
+    n0 = ln;
+    block += full / 4;
+    // every wave has read its slice; the stores are left under way
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 }
 

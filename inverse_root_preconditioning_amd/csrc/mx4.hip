@@ -91,8 +91,10 @@ int product_tiles(Mx4ProductArgs a, int splits, hipStream_t stream) {
   if (tm * tn > kMaxGrid) return SHAMPOO_EUNSUPPORTED;
   a.tiles_m = (uint32_t)tm;
   a.tiles_n = (uint32_t)tn;
-  const dim3 grid((uint32_t)(tm * tn), (uint32_t)splits), block(256);
   const bool beta = a.beta != 0.f;
+  // one workgroup a compute unit, going from tile to tile, where it can
+  const bool stream_tiles = mx4_streams(T, beta) && a.padded % 1024 == 0;
+  const dim3 grid((uint32_t)(stream_tiles ? std::min<int64_t>(tm * tn, 256) : tm * tn), (uint32_t)splits), block(256);
   if (a.bf16 && beta) {
     hipLaunchKernelGGL((mx4_product_kernel<T, true, true>), grid, block, 0, stream, a);
   } else if (a.bf16) {

@@ -84,6 +84,34 @@ def test_product_with_an_output_beyond_32_bit_offsets():
         assert bool(np.all(np.abs(_f64(c[rows]) - want) <= tol))
 
 
+@pytest.mark.parametrize("M,N,K,dtype,beta", [
+    (4400, 4300, 1000, "f32", 0.0), (4400, 4301, 2048, "bf16", 0.0), (6001, 6000, 1024, "bf16", 0.0),
+    (4096, 4352, 5000, "f32", 0.0), (70001, 255, 1024, "f32", 0.0), (4400, 4300, 1000, "f32", 0.5), (4400, 4300, 1100, "bf16", 0.0)])
+def test_product_of_more_tiles_than_compute_units(M, N, K, dtype, beta):
+    """Workgroups that go from tile to tile, whole ones and those at the edges,
+    once to three times, into rows that lie further apart than they are long."""
+    print(f"tiles case: {M} {N} {K} {dtype} {beta}", flush=True)
+    r = np.random.Generator(np.random.PCG64([M, N, K]))
+    a = MX.quantize(torch.from_numpy(r.standard_normal((M, K), dtype=np.float32)).cuda())
+    b = MX.quantize(torch.from_numpy(r.standard_normal((N, K), dtype=np.float32)).cuda())
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    whole = torch.full((M, N + 24), 0.75, device="cuda", dtype=td)
+    out = whole[:, 8:N + 8]
+    MX.product(a, b, out=out, alpha=-0.5, beta=beta)
+    av, bv = MX.dequantize(a).double(), MX.dequantize(b).double().T.contiguous()
+    want = -0.5 * (av @ bv) + beta * 0.75
+    tol = (K + 8) * 2.0 ** -24 * (0.5 * (av.abs() @ bv.abs()) + beta * 0.75)
+    if dtype == "bf16":
+        tol += 2.0 ** -8 * want.abs()
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert bool((whole[:, :8] == 0.75).all()) and bool((whole[:, N + 8:] == 0.75).all())
+    first = whole.clone()
+    if beta == 0.0:
+        for _ in range(3):                          # the same bits again
+            MX.product(a, b, out=out, alpha=-0.5)
+            assert torch.equal(whole, first)
+
+
 @pytest.mark.parametrize("M,N", [(20, 5), (300, 300)])
 def test_product_over_no_columns(M, N):
     z = lambda r: MX.quantize(torch.zeros(r, 0, device="cuda"))  # noqa: E731
