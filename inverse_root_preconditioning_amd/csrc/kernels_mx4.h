@@ -690,8 +690,9 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
         if (c + 1 == full) aim_b(ln);
       }
       const int other = kStage - cur;
-      const int ahead1 = c + 1 < full ? c + 1 : 0, ahead2 = min(c + 2 < full ? c + 2 : c + 2 - full, full - 1);
-      const int ahead_scales = 4 * (c / 4 + 1) < full ? c / 4 + 1 : 0;
+      const int ahead1 = kStream && c + 1 == full ? 0 : min(c + 1, full - 1);
+      const int ahead2 = min(kStream && c + 2 >= full ? c + 2 - full : c + 2, full - 1);
+      const int ahead_scales = kStream && 4 * (c / 4 + 1) >= full ? 0 : c / 4 + 1;
       int ta[T], tb[T];
 #pragma unroll
       for (int i = 0; i < T; ++i) ta[i] = sa[i];
