@@ -736,6 +736,8 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
     // half of the last chunk's buffer: the next tile's loads reach it only after
     // the barrier below.
     if constexpr (!kStream) meet();
+    // no loads into LDS may be left when the workgroup ends
+    if (kStream && !more) __builtin_amdgcn_s_waitcnt(kWaitAll);
     uint8_t* const slice = lds + (kStream ? kStage - cur + kData : 0) + wave * 32 * kSlice * 4;
     auto output = [&](auto WHOLE) __attribute__((always_inline)) {
       constexpr bool kWhole = decltype(WHOLE)::value;
