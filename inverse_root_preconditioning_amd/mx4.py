@@ -161,6 +161,12 @@ def _workspace(need, like):
     return ws, ws.data_ptr()
 
 
+def _refuse_gradient(t, name, call):
+    """A product of raw memory has no graph: a gradient that it would cut is an error."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{call} forms no gradient of {name}: use train_linear, detach it, or call under no_grad")
+
+
 def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=None):
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
@@ -178,6 +184,8 @@ def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=No
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
         out = torch.empty((M, N), dtype=dtype, device=device)
+    else:
+        _refuse_gradient(out, "out", "product")
     ctype, ld = _matrix(out, "out")
     if out.shape != (M, N):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, N)}")
@@ -192,13 +200,16 @@ def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=No
 
 
 def linear(x, w, out=None, stream=None):
-    """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type."""
+    """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type.  It
+    forms no gradients, and refuses an x that would need one."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, w, out)
     shape, N, K, device = x.shape, w.rows, w.cols, w.device
     if shape[-1] != K:
         raise ValueError(f"x has {shape[-1]} columns, w {K}")
+    if x.requires_grad:
+        _refuse_gradient(x, "x", "linear")
     if x.device != device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
     if len(shape) == 2:
@@ -211,6 +222,7 @@ def linear(x, w, out=None, stream=None):
     if out is None:
         out = x.new_empty(to)
     else:
+        _refuse_gradient(out, "out", "linear")
         if out.shape != to or out.dtype != x.dtype:
             raise ValueError(f"out must have shape {to} and x's type")
         _, ldy = _matrix(out if len(to) == 2 else out.view(rows, N), "out")

@@ -1,0 +1,47 @@
+"""What autograd may expect of the MX4 layers: gradients that a call cannot form
+are refused, and what backward needs is kept the way autograd frees and moves it."""
+import pytest
+import torch
+
+from inverse_root_preconditioning_amd import capi
+from inverse_root_preconditioning_amd import mx4 as MX
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    capi.load()
+
+
+def _pair(rows=40, n=96, k=160):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    return torch.randn(rows, k, generator=gen, device="cuda"), torch.randn(n, k, generator=gen, device="cuda")
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_linear_refuses_an_input_that_requires_grad(rows):
+    x, w = _pair(rows)
+    q = MX.quantize(w)
+    want = MX.linear(x, q)
+    x.requires_grad_()
+    for bad in (x, x * 1.0, x.view(rows, 1, -1)):
+        with pytest.raises(ValueError, match="gradient"):
+            MX.linear(bad, q)
+    with torch.no_grad():
+        assert torch.equal(MX.linear(x, q), want)
+    assert torch.equal(MX.linear(x.detach(), q), want)
+
+
+def test_outputs_that_require_grad_are_refused():
+    x, w = _pair()
+    q, xq = MX.quantize(w), MX.quantize(x)
+    out = torch.zeros(40, 96, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        MX.linear(x, q, out=out)
+    with pytest.raises(ValueError, match="gradient"):
+        MX.product(xq, q, out=out)
+    with torch.no_grad():
+        assert torch.equal(MX.linear(x, q, out=out), MX.product(xq, q, dtype=torch.float32))
