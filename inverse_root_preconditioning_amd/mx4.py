@@ -12,6 +12,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import capi
@@ -167,6 +168,11 @@ def _refuse_gradient(t, name, call):
         raise ValueError(f"{call} forms no gradient of {name}: use train_linear, detach it, or call under no_grad")
 
 
+def _has_tangent(t):
+    # outside a dual level (the only case whose time counts) there are no tangents
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None
+
+
 def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=None):
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
@@ -210,6 +216,8 @@ def linear(x, w, out=None, stream=None):
         raise ValueError(f"x has {shape[-1]} columns, w {K}")
     if x.requires_grad:
         _refuse_gradient(x, "x", "linear")
+    if _has_tangent(x):
+        raise ValueError("linear forms no tangent of x")
     if x.device != device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
     if len(shape) == 2:
@@ -267,9 +275,9 @@ def train_linear(x, w):
     gradients through the quantisers as if they were the identity:
     dx = mx4(dy) mx4(w^T)^T and dw = mx4(dy^T) mx4(x^T)^T, every operand
     quantised along the dimension it is summed over.  What the backward pass
-    needs is kept in MX4 (0.53 bytes an element)."""
+    needs is kept in MX4 (0.53 bytes an element).  Forward-mode tangents are refused."""
     if x.shape[-1] != w.shape[-1] or w.dim() != 2:
         raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} do not multiply")
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or _has_tangent(x) or _has_tangent(w):
         return _TrainLinear.apply(x, w)
     return product(quantize(_flat(x)), quantize(w.detach()), dtype=x.dtype).view(*x.shape[:-1], w.shape[0])

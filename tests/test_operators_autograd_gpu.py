@@ -2,6 +2,7 @@
 are refused, and what backward needs is kept the way autograd frees and moves it."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from inverse_root_preconditioning_amd import capi
 from inverse_root_preconditioning_amd import mx4 as MX
@@ -45,3 +46,20 @@ def test_outputs_that_require_grad_are_refused():
         MX.product(xq, q, out=out)
     with torch.no_grad():
         assert torch.equal(MX.linear(x, q, out=out), MX.product(xq, q, dtype=torch.float32))
+
+
+def test_forward_mode_tangents_are_refused():
+    x, w = _pair()
+    q = MX.quantize(w)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        dual_w = forward_ad.make_dual(w, torch.ones_like(w))
+        with pytest.raises(ValueError, match="tangent"):
+            MX.linear(dual, q)
+        for args in ((dual, w), (x, dual_w)):
+            with pytest.raises(NotImplementedError, match="jvp"):
+                MX.train_linear(*args)
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="jvp"):
+                MX.train_linear(*args)
+        assert torch.equal(MX.train_linear(x, w), MX.train_linear(x, w))
+        MX.linear(x, q)
