@@ -71,13 +71,19 @@ class MX4Matrix:
     @classmethod
     def empty(cls, rows, cols, like):
         """Uninitialised storage on the device of the tensor `like`: one buffer, scales after codes."""
-        m = cls.__new__(cls)
         n = rows * _padded(cols) // 2             # a multiple of 64
-        m._buf = like.new_empty((n + n // 16,), dtype=torch.uint8)
+        return cls._over(like.new_empty((n + n // 16,), dtype=torch.uint8), rows, cols)
+
+    @classmethod
+    def _over(cls, buf, rows, cols):
+        """The matrix in a buffer of empty's layout."""
+        m = cls.__new__(cls)
+        n = rows * _padded(cols) // 2
+        m._buf = buf
         m._codes = m._scales = None
         m.codes_ptr = m._buf.data_ptr()
         m.scales_ptr = m.codes_ptr + n
-        m.rows, m.cols, m.device = rows, cols, like.device
+        m.rows, m.cols, m.device = rows, cols, buf.device
         return m
 
     @property
@@ -255,18 +261,24 @@ class _TrainLinear(torch.autograd.Function):
         flat = _flat(x.detach())
         xq, xt = _quantize(flat, True, need_w)
         wq, wt = _quantize(w.detach(), True, need_x)
-        ctx.xt, ctx.wt = xt, wt
+        # saved as tensors, so that backward frees them and hooks (offload, checkpoints) see them
+        ctx.save_for_backward(xt._buf if need_w else None, wt._buf if need_x else None)
         ctx.types = x.dtype, w.dtype
-        ctx.shape = x.shape
+        ctx.shape, ctx.w_shape, ctx.rows = x.shape, w.shape, flat.shape[0]
         return product(xq, wq, dtype=x.dtype).view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad
+        x_buf, w_buf = ctx.saved_tensors
+        N, K = ctx.w_shape
         q, qt = _quantize(_flat(dy), need_x, need_w)
-        dx = product(q, ctx.wt, dtype=ctx.types[0]).view(ctx.shape) if need_x else None
-        dw = product(qt, ctx.xt, dtype=ctx.types[1]) if need_w else None
+        dx = dw = None
+        if need_x:
+            dx = product(q, MX4Matrix._over(w_buf, K, N), dtype=ctx.types[0]).view(ctx.shape)
+        if need_w:
+            dw = product(qt, MX4Matrix._over(x_buf, K, ctx.rows), dtype=ctx.types[1])
         return dx, dw
 
 
