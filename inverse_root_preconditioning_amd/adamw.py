@@ -19,6 +19,14 @@ _TYPES = {torch.float32: capi.T_F32, torch.bfloat16: capi.T_BF16}
 _STATES = {"f32": capi.STATE_F32, "mx8": capi.STATE_MX8}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without the Python objects
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_stream(stream, device):
+    """Context of a call on `stream`; the tensors are on `device`."""
+    if stream.device_index != device.index:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _dense(t):
@@ -93,12 +101,16 @@ def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
     as one vector, and min(1, max_norm / norm) (NaN if the norm is not finite,
     which makes AdamW.step change nothing)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, table.device):
+            return grad_norm(table, max_norm, out)
+    if table.index != _current_device():
+        with torch.cuda.device(table.index):
             return grad_norm(table, max_norm, out)
     if out is None:
         out = table.tensor.new_empty((2,), dtype=torch.float32)
-    elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2):
-        raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements")
+    elif not (out.get_device() == table.index and out.dtype == torch.float32 and out.is_contiguous()
+              and out.numel() == 2):
+        raise ValueError("out must be a contiguous float32 CUDA tensor of 2 elements on the table's device")
     need = table._norm_ws
     ws = table.tensor.new_empty(need, dtype=torch.uint8) if need else None
     rc = capi.load().shampoo_grad_norm(table.ptr, table.segments_ptr, table.nsegments, table.type, max_norm,
@@ -175,19 +187,22 @@ class AdamW:
         """One step with the gradients of a TensorTable (or a list of tensors).
         grad_scale: float32 tensor of one element on the device that multiplies
         the gradients; if it is not finite, nothing changes but `t`."""
+        p = self.params
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on_stream(stream, p.device):
+                return self.step(grads, lr, grad_scale)
+        if p.index != _current_device():
+            with torch.cuda.device(p.index):
                 return self.step(grads, lr, grad_scale)
         if not isinstance(grads, TensorTable):
             grads = TensorTable(grads)
-        p = self.params
         if grads is not self._checked:
             self._same(grads, "gradients")
             self._checked = grads        # neither its layouts nor its device change
         scale_ptr = 0
         if grad_scale is not None:
-            if not (grad_scale.is_cuda and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1):
-                raise ValueError("grad_scale must be a float32 CUDA tensor of one element")
+            if not (grad_scale.get_device() == p.index and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1):
+                raise ValueError("grad_scale must be a float32 CUDA tensor of one element on the parameters' device")
             scale_ptr = grad_scale.data_ptr()
         b1, b2 = self.betas
         rc = capi.load().shampoo_adamw(
@@ -200,8 +215,12 @@ class AdamW:
 
     def moments(self, dtype=torch.float32, stream=None):
         """The values of (m, v) as flat tensors in the state's layout."""
+        p = self.params
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on_stream(stream, p.device):
+                return self.moments(dtype)
+        if p.index != _current_device():
+            with torch.cuda.device(p.index):
                 return self.moments(dtype)
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
@@ -210,7 +229,7 @@ class AdamW:
         m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
         mc, vc, ms, vs = self._state_ptrs
         capi.check(capi.shampoo_adamw_moments(mc, ms, vc, vs, m.numel(), m.data_ptr(), v.data_ptr(), _TYPES[dtype],
-                                              _raw_stream(self.params.index)), "shampoo_adamw_moments")
+                                              _raw_stream(p.index)), "shampoo_adamw_moments")
         return m, v
 
     def state_dict(self):

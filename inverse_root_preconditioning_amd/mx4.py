@@ -16,7 +16,7 @@ from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import capi
-from .adamw import _TYPES, _raw_stream
+from .adamw import _TYPES, _current_device, _on_stream, _raw_stream
 
 
 def _padded(k):
@@ -110,6 +110,10 @@ def _quantize(x, along_rows, along_cols):
         qt, q = _quantize(x.t(), along_cols, along_rows)
         return q, qt
     dtype, ld = _matrix(x, "x")
+    index = x.device.index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return _quantize(x, along_rows, along_cols)
     rows, cols = x.shape
     q = qt = None
     codes = scales = codes_t = scales_t = 0
@@ -120,7 +124,7 @@ def _quantize(x, along_rows, along_cols):
         qt = MX4Matrix.empty(cols, rows, x)
         codes_t, scales_t = qt.codes_ptr, qt.scales_ptr
     rc = capi.load().shampoo_mx4_quantize(x.data_ptr(), dtype, rows, cols, ld, codes, scales, codes_t, scales_t,
-                                          _raw_stream(x.device.index))
+                                          _raw_stream(index))
     if rc:
         _check(rc, "shampoo_mx4_quantize")
     return q, qt
@@ -130,7 +134,7 @@ def quantize(x, stream=None):
     """x [rows, cols] (or a transposed view of such a matrix) as MX4, 32
     consecutive columns sharing a scale."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, x.device):
             return quantize(x)
     return _quantize(x, True, False)[0]
 
@@ -138,7 +142,7 @@ def quantize(x, stream=None):
 def quantize_both(x, stream=None):
     """(quantize(x), quantize(x.t())) from one reading of x."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, x.device):
             return quantize_both(x)
     return _quantize(x, True, True)
 
@@ -146,12 +150,15 @@ def quantize_both(x, stream=None):
 def dequantize(q, dtype=torch.float32, stream=None):
     """The values of q."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, q.device):
             return dequantize(q, dtype)
     code = _TYPES.get(dtype)
     if code is None:
         raise ValueError("dtype must be float32 or bfloat16")
     rows, cols, device = q.rows, q.cols, q.device
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return dequantize(q, dtype)
     out = torch.empty((rows, cols), dtype=dtype, device=device)
     rc = capi.load().shampoo_mx4_dequantize(q.codes_ptr, q.scales_ptr, rows, cols, out.data_ptr(), code, cols,
                                             _raw_stream(device.index))
@@ -183,13 +190,16 @@ def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=No
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, a.device):
             return product(a, b, out, dtype, alpha, beta)
     M, N, K, device = a.rows, b.rows, a.cols, a.device
     if K != b.cols:
         raise ValueError(f"a has {K} columns, b {b.cols}")
     if device != b.device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return product(a, b, out, dtype, alpha, beta)
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out")
@@ -215,7 +225,7 @@ def linear(x, w, out=None, stream=None):
     """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type.  It
     forms no gradients, and refuses an x that would need one."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, w.device):
             return linear(x, w, out)
     shape, N, K, device = x.shape, w.rows, w.cols, w.device
     if shape[-1] != K:
@@ -226,6 +236,9 @@ def linear(x, w, out=None, stream=None):
         raise ValueError("linear forms no tangent of x")
     if x.device != device or (out is not None and out.device != device):
         raise ValueError("the operands are on one device")
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return linear(x, w, out)
     if len(shape) == 2:
         flat, rows, to = x, shape[0], (shape[0], N)
     else:
