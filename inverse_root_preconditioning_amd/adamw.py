@@ -22,11 +22,18 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_strea
 _current_device = torch._C._cuda_getDevice
 
 
-def _on_stream(stream, device):
-    """Context of a call on `stream`; the tensors are on `device`."""
+def _on_stream(stream, device, call, *operands):
+    """call() on `stream`; the operands (None: not given) are on `device`.  They
+    may be another stream's memory and be freed there before the call has run, so
+    the allocator is told of it."""
     if stream.device_index != device.index:
         raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        result = call()
+    for t in operands:
+        if t is not None:
+            t.record_stream(stream)
+    return result
 
 
 def _dense(t):
@@ -94,6 +101,14 @@ class TensorTable:
         self.ptr = self.tensor.data_ptr()
         self.segments_ptr = self.segments.data_ptr()
         self._norm_ws = capi.shampoo_grad_norm_workspace_bytes(self.nsegments)
+        self._streams = set()
+
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream, for the table and its tensors (a use is noted until they are freed)."""
+        if stream.cuda_stream not in self._streams:
+            for t in (self.tensor, self.segments, *self._keep):
+                t.record_stream(stream)
+            self._streams.add(stream.cuda_stream)
 
 
 def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
@@ -101,8 +116,7 @@ def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
     as one vector, and min(1, max_norm / norm) (NaN if the norm is not finite,
     which makes AdamW.step change nothing)."""
     if stream is not None:
-        with _on_stream(stream, table.device):
-            return grad_norm(table, max_norm, out)
+        return _on_stream(stream, table.device, lambda: grad_norm(table, max_norm, out), table, out)
     if table.index != _current_device():
         with torch.cuda.device(table.index):
             return grad_norm(table, max_norm, out)
@@ -183,14 +197,22 @@ class AdamW:
         if table.device != self.params.device:
             raise ValueError(f"{name} are on another device than the parameters")
 
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream, for the parameters, their copies and the state."""
+        self.params.record_stream(stream)
+        for t in (self.copies, self.hyper, self.m, self.v, self.m_scale, self.v_scale):
+            if t is not None:
+                t.record_stream(stream)
+
     def step(self, grads, lr=None, grad_scale=None, stream=None):
         """One step with the gradients of a TensorTable (or a list of tensors).
         grad_scale: float32 tensor of one element on the device that multiplies
         the gradients; if it is not finite, nothing changes but `t`."""
         p = self.params
         if stream is not None:
-            with _on_stream(stream, p.device):
-                return self.step(grads, lr, grad_scale)
+            grads = grads if isinstance(grads, TensorTable) else list(grads)
+            return _on_stream(stream, p.device, lambda: self.step(grads, lr, grad_scale), self, grad_scale,
+                              *((grads,) if isinstance(grads, TensorTable) else grads))
         if p.index != _current_device():
             with torch.cuda.device(p.index):
                 return self.step(grads, lr, grad_scale)
@@ -217,8 +239,7 @@ class AdamW:
         """The values of (m, v) as flat tensors in the state's layout."""
         p = self.params
         if stream is not None:
-            with _on_stream(stream, p.device):
-                return self.moments(dtype)
+            return _on_stream(stream, p.device, lambda: self.moments(dtype), self)
         if p.index != _current_device():
             with torch.cuda.device(p.index):
                 return self.moments(dtype)

@@ -104,6 +104,11 @@ class MX4Matrix:
     def shape(self):
         return (self.rows, self.cols)
 
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream."""
+        for t in (self._codes, self._scales) if self._buf is None else (self._buf,):
+            t.record_stream(stream)
+
 
 def _quantize(x, along_rows, along_cols):
     if x.dim() == 2 and x.stride(1) != 1 and x.stride(0) == 1 and x.shape[1] > 1:
@@ -134,24 +139,21 @@ def quantize(x, stream=None):
     """x [rows, cols] (or a transposed view of such a matrix) as MX4, 32
     consecutive columns sharing a scale."""
     if stream is not None:
-        with _on_stream(stream, x.device):
-            return quantize(x)
+        return _on_stream(stream, x.device, lambda: quantize(x), x)
     return _quantize(x, True, False)[0]
 
 
 def quantize_both(x, stream=None):
     """(quantize(x), quantize(x.t())) from one reading of x."""
     if stream is not None:
-        with _on_stream(stream, x.device):
-            return quantize_both(x)
+        return _on_stream(stream, x.device, lambda: quantize_both(x), x)
     return _quantize(x, True, True)
 
 
 def dequantize(q, dtype=torch.float32, stream=None):
     """The values of q."""
     if stream is not None:
-        with _on_stream(stream, q.device):
-            return dequantize(q, dtype)
+        return _on_stream(stream, q.device, lambda: dequantize(q, dtype), q)
     code = _TYPES.get(dtype)
     if code is None:
         raise ValueError("dtype must be float32 or bfloat16")
@@ -190,8 +192,7 @@ def product(a, b, out=None, dtype=torch.bfloat16, alpha=1.0, beta=0.0, stream=No
     """alpha a b^T + beta out, accumulated in fp32: a [M, K], b [N, K] -> [M, N].
     Written to `out` if given (of its type), else to a new matrix of `dtype`."""
     if stream is not None:
-        with _on_stream(stream, a.device):
-            return product(a, b, out, dtype, alpha, beta)
+        return _on_stream(stream, a.device, lambda: product(a, b, out, dtype, alpha, beta), a, b, out)
     M, N, K, device = a.rows, b.rows, a.cols, a.device
     if K != b.cols:
         raise ValueError(f"a has {K} columns, b {b.cols}")
@@ -225,8 +226,7 @@ def linear(x, w, out=None, stream=None):
     """mx4(x) w^T for x [..., K] and an MX4 weight w [N, K], in x's type.  It
     forms no gradients, and refuses an x that would need one."""
     if stream is not None:
-        with _on_stream(stream, w.device):
-            return linear(x, w, out)
+        return _on_stream(stream, w.device, lambda: linear(x, w, out), x, w, out)
     shape, N, K, device = x.shape, w.rows, w.cols, w.device
     if shape[-1] != K:
         raise ValueError(f"x has {shape[-1]} columns, w {K}")

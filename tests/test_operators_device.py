@@ -38,6 +38,9 @@ class Tensor:
     def data_ptr(self):
         return 0x10000
 
+    def record_stream(self, stream):
+        self.used_on = stream
+
     def new_empty(self, shape, dtype=None):
         return Tensor(shape if isinstance(shape, tuple) else (shape,), dtype or self.dtype, self.device.index)
 
@@ -80,7 +83,8 @@ def _table(index=1, layouts=(64,)):
     t = AW.TensorTable.__new__(AW.TensorTable)
     t.device, t.index, t.layouts = torch.device("cuda", index), index, layouts
     t.ptr = t.segments_ptr = 0x10000
-    t.nsegments, t.type, t.n, t._norm_ws, t.tensor = 1, capi.T_F32, 1, 64, Tensor((1, 3), torch.int64, index)
+    t.nsegments, t.type, t.n, t._norm_ws = 1, capi.T_F32, 1, 64
+    t.tensor, t.segments, t._keep, t._streams = Tensor((1, 3), torch.int64, index), Tensor((1, 2)), [Tensor((64,))], set()
     return t
 
 
@@ -88,6 +92,7 @@ def _adamw(index=1):
     o = AW.AdamW.__new__(AW.AdamW)
     o.params, o._checked, o.t, o.seed, o.lr, o.betas, o.eps = _table(index), None, 0, 0, 1e-3, (0.9, 0.95), 1e-8
     o._copies_ptr = o._hyper_ptr = 0
+    o.copies, o.hyper = None, Tensor((1, 2), index=index)
     o._state, o._state_ptrs = capi.STATE_MX8, (1, 2, 3, 4)
     o.m = o.v = o.m_scale = o.v_scale = Tensor((64,), torch.uint8, index)
     return o
@@ -118,12 +123,12 @@ def test_the_tensors_device_is_current_at_the_launch(name, machine):
 
 @pytest.mark.parametrize("name", CALLS)
 def test_a_stream_is_on_the_tensors_device(name, machine):
-    stream = types.SimpleNamespace(device_index=1)
+    stream = types.SimpleNamespace(device_index=1, cuda_stream=7)
     CALLS[name](stream=stream)
     assert machine.calls and all((dev, s) == (1, ("stream of", 1)) for _, dev, s in machine.calls)
     machine.calls.clear()
     with pytest.raises(ValueError, match="stream"):
-        CALLS[name](stream=types.SimpleNamespace(device_index=0))
+        CALLS[name](stream=types.SimpleNamespace(device_index=0, cuda_stream=7))
     assert not machine.calls
 
 
@@ -139,3 +144,20 @@ def test_small_operands_are_on_the_same_device(machine):
     _adamw().step(_table(), grad_scale=Tensor((1,)))
     AW.grad_norm(_table(), 1.0, out=Tensor((2,)))
     assert len(machine.calls) == 2
+
+
+def test_operands_of_another_stream_are_noted(machine):
+    """The allocator learns of every operand that a call on `stream` uses."""
+    s = types.SimpleNamespace(device_index=1, cuda_stream=7)
+    x, q, r, out = Tensor((8, 64)), _matrix(), _matrix(), Tensor((8, 8))
+    MX.quantize(x, stream=s)
+    MX.dequantize(q, stream=s)
+    MX.product(q, r, out=out, stream=s)
+    table, opt, scale, norm = _table(), _adamw(), Tensor((1,)), Tensor((2,))
+    AW.grad_norm(table, 1.0, out=norm, stream=s)
+    opt.step(table, grad_scale=scale, stream=s)
+    y, w = Tensor((8, 64)), _matrix()
+    MX.linear(y, w, stream=s)
+    used = [x, q._buf, r._buf, out, norm, scale, y, w._buf, table.tensor, table.segments, *table._keep, opt.hyper, opt.m,
+            opt.params.tensor]
+    assert all(t.used_on is s for t in used)
