@@ -78,7 +78,7 @@ class TensorTable:
         self.type = _TYPES[dtype]
         self.device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
         self.index = self.device.index
-        self.layouts = [_layout(t) for t in tensors]
+        self.layouts = tuple(_layout(t) for t in tensors)
         self._keep = tensors
         sizes = np.array([t.numel() for t in tensors], dtype=np.int64)
         padded = (sizes + capi.GROUP - 1) // capi.GROUP * capi.GROUP
@@ -218,9 +218,10 @@ class AdamW:
                 return self.step(grads, lr, grad_scale)
         if not isinstance(grads, TensorTable):
             grads = TensorTable(grads)
-        if grads is not self._checked:
+        # Layouts found equal are found again by their tuple; the table itself, and the gradients with it, is not kept.
+        if grads.layouts is not self._checked or grads.index != p.index:
             self._same(grads, "gradients")
-            self._checked = grads        # neither its layouts nor its device change
+            self._checked = grads.layouts
         scale_ptr = 0
         if grad_scale is not None:
             if not (grad_scale.get_device() == p.index and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1):
