@@ -1,6 +1,8 @@
 // C entry points of the AdamW step and the gradient norm (gfx950): arguments
 // are checked on the host, kernels enqueued on the caller's stream; nothing
 // is allocated and nothing synchronises.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "kernels_adamw.h"
@@ -123,10 +125,14 @@ int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, con
   a.omb1 = 1.0 - beta1;
   a.beta2 = (float)beta2;
   a.omb2 = 1.0 - beta2;
-  a.eps = (float)eps;
+  // A subnormal eps would count as 0 in the kernel's reciprocal.  FLT_MIN serves
+  // as well: it vanishes beside the least root of a v > 0, 2^-74.5.
+  a.eps = eps > 0. ? std::max((float)eps, FLT_MIN) : 0.f;
   a.rbc1 = (float)(1.0 / (1.0 - std::pow(beta1, step)));
   a.rsbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, step)));
   a.key = step_key(seed, step);
+  // the root of a subnormal is below 2^-63: beside such an eps it is less than half an ulp
+  a.tiny_roots = !(a.eps >= 0x1p-38f * a.rsbc2);
   const bool gb = grad_dtype == SHAMPOO_T_BF16;
   if (param_dtype == SHAMPOO_T_BF16) return gb ? launch<true, true>(a, mx8, (uint32_t)nsegments, stream)
                                                : launch<true, false>(a, mx8, (uint32_t)nsegments, stream);

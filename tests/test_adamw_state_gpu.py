@@ -9,6 +9,8 @@ from inverse_root_preconditioning_amd import capi
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
@@ -42,3 +44,32 @@ def test_tables_are_checked_after_another_was():
         opt.step([torch.ones_like(t) for t in reversed(p)])
     opt.step([torch.ones_like(t) for t in p])
     assert opt.t == 2
+
+
+@pytest.mark.parametrize("state", ["f32", "mx8"])
+@pytest.mark.parametrize("size", [1e-19, 1e-20, 1e-21])
+def test_second_moments_below_the_normal_range(size, state):
+    """eps = 0: the first step is lr in size whatever the gradient's.  v lies in
+    fp32's subnormals, 2^-149 apart, and is rounded to them: its relative error
+    is at most 2^-150 / v, half of it the update's."""
+    p = torch.ones(96, device="cuda")
+    opt = AW.AdamW([p], lr=0.125, betas=(0.9, 0.95), eps=0.0, weight_decay=0.0, state=state)
+    g = torch.full((96,), size, device="cuda")
+    g[::2] *= -1
+    opt.step([g])
+    v = 0.05 * float(g.abs()[0]) ** 2
+    tol = 0.125 * (2.0 ** -150 / v + 32 * U) + 2 * U
+    want = torch.where(g > 0, 0.875, 1.125).double()
+    off = (p.double() - want).abs().max().item()
+    assert off <= tol
+
+
+@pytest.mark.parametrize("eps", [1e-38, 1e-40, 1e-50])
+def test_an_eps_below_the_normal_range_divides_zero(eps):
+    """A gradient of 0 leaves m = v = 0, and 0 / eps is 0."""
+    p = torch.ones(96, device="cuda")
+    opt = AW.AdamW([p], lr=0.125, eps=eps, weight_decay=0.0)
+    g = torch.zeros(96, device="cuda")
+    g[5] = 1.0
+    opt.step([g])
+    assert p[5].item() == 0.875 and p.sum().item() == 95.875
