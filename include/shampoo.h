@@ -471,7 +471,8 @@ int shampoo_mx4_product(const uint8_t* a_codes, const uint8_t* a_scales, const u
  * shampoo_mx4_linear -- Y = mx4(X) W^T: X [M][K] is quantised along its rows
  * and multiplied by the MX4 weight W [N][K].
  *
- *   X          of dtype, row stride ldx;  Y [M][N] of dtype, row stride ldy
+ *   X          of dtype, row stride ldx;  Y [M][N] of dtype, row stride ldy,
+ *              apart from X (SHAMPOO_EINVAL; other columns of one matrix are)
  *   ws         shampoo_mx4_linear_workspace_bytes(M, N, K) bytes
  */
 int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const uint8_t* w_scales, int64_t M,

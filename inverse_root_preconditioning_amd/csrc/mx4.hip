@@ -32,6 +32,20 @@ bool valid_mx4(const uint8_t* codes, const uint8_t* scales) {
   return codes != nullptr && scales != nullptr && aligned16(codes) && aligned16(scales);
 }
 
+// Whether an [M][a] and an [M][b] matrix with rows lda and ldb elements of
+// `size` bytes apart may share memory.  Of one row distance (two stretches of
+// one matrix's columns) that is told exactly, else by the ends alone.
+bool may_overlap(const void* pa, int64_t a, int64_t lda, const void* pb, int64_t b, int64_t ldb, int64_t M,
+                 int64_t size) {
+  typedef __int128 wide;
+  const wide a0 = (wide) reinterpret_cast<uintptr_t>(pa), b0 = (wide) reinterpret_cast<uintptr_t>(pb);
+  const wide wa = (wide)a * size, wb = (wide)b * size, row = (wide)lda * size;
+  if (a0 + (M - 1) * row + wa <= b0 || b0 + (M - 1) * ((wide)ldb * size) + wb <= a0) return false;
+  if (M == 1 || lda != ldb) return true;
+  const wide between = ((b0 - a0) % row + row) % row;  // from a row of the first to the next row of the second
+  return between < wa || between + wb > row;
+}
+
 // Lanes (a power of two, 16 to 256) that take a row of pieces of `elems`, and how
 // many such stretches a row has.
 void row_shape(int64_t padded, int64_t elems, int* lanes_log2, int64_t* col_blocks) {
@@ -289,6 +303,8 @@ int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const
   const size_t need = shampoo_mx4_linear_workspace_bytes(M, N, K);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return SHAMPOO_EWORKSPACE;
   if (!aligned16(ws)) return SHAMPOO_EINVAL;
+  // With few rows every workgroup reads X for itself while others write Y.
+  if (K > 0 && may_overlap(x, K, ldx, y, N, ldy, M, dtype == SHAMPOO_T_BF16 ? 2 : 4)) return SHAMPOO_EINVAL;
   if (few_quantise(M, K)) {
     Mx4FewArgs f = {};
     f.p.b = w_codes;
