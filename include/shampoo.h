@@ -387,7 +387,8 @@ size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments);
  *   params, grads, copies   device tables of the same tensors in the same order
  *              (copies may be NULL: else p is also written there in bf16,
  *              rounded to nearest even; only with fp32 parameters).  The
- *              state offsets are those of `params`
+ *              state offsets are those of `params`.  No two tensors of
+ *              params and copies share memory (gradients may)
  *   hyper      device float[ntensors][2]: factor on lr, weight decay
  *   param_dtype, grad_dtype   SHAMPOO_T_F32 or SHAMPOO_T_BF16
  *   m, v       device state at the tensors' offsets, 16-byte aligned: float, or

@@ -134,6 +134,13 @@ def grad_norm(table, max_norm=float("inf"), out=None, stream=None):
     return out
 
 
+def _refuse_shared(tensors, name):
+    """Two segments of a step must not update the same memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError(f"{name} share memory")
+
+
 def _per_tensor(value, n, name):
     values = [float(v) for v in value] if isinstance(value, (list, tuple)) else [float(value)] * n
     if len(values) != n:
@@ -144,7 +151,8 @@ def _per_tensor(value, n, name):
 class AdamW:
     """AdamW (decoupled weight decay) over a list of tensors, updated in place.
 
-    params        float32 or bfloat16 tensors of one type, or a TensorTable.
+    params        float32 or bfloat16 tensors of one type, or a TensorTable, apart
+                  from one another (a tied weight is given once).
                   bfloat16 parameters are rounded stochastically, so that steps
                   below their spacing are kept on average
     weight_decay  a number, or one for each tensor
@@ -176,6 +184,7 @@ class AdamW:
             if p.dtype != torch.float32 or self.copies.dtype != torch.bfloat16:
                 raise ValueError("copies are bfloat16 copies of float32 parameters")
             self._same(self.copies, "copies")
+        _refuse_shared(p._keep + (self.copies._keep if self.copies else []), "parameters or copies")
         hyper = np.array([_per_tensor(lr_scale, p.n, "lr_scale"), _per_tensor(weight_decay, p.n, "weight_decay")],
                          dtype=np.float32).T
         self.hyper = torch.from_numpy(np.ascontiguousarray(hyper)).to(dev)

@@ -73,3 +73,23 @@ def test_an_eps_below_the_normal_range_divides_zero(eps):
     g[5] = 1.0
     opt.step([g])
     assert p[5].item() == 0.875 and p.sum().item() == 95.875
+
+
+def test_parameters_that_share_memory_are_refused():
+    """Two workgroups would update the same elements."""
+    flat = torch.zeros(200, device="cuda")
+    for bad in ([flat, flat], [flat[:40], flat[32:64]], [flat[100:], flat[:50], flat[40:60]]):
+        with pytest.raises(ValueError, match="share memory"):
+            AW.AdamW(bad)
+    opt = AW.AdamW([flat[100:], flat[:40], flat[40:60], flat[:0], flat[60:60]])   # apart from one another
+    opt.step([torch.ones(n, device="cuda") for n in (100, 40, 20, 0, 0)])
+    p = [torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")]
+    c = torch.zeros(100, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="share memory"):
+        AW.AdamW(p, copies=[c[:64], c[36:]])
+    with pytest.raises(ValueError, match="share memory"):
+        AW.AdamW(p, copies=[p[0].view(torch.bfloat16)[:64], c[:64]])
+    # gradients are only read: tied ones may be one tensor
+    g = torch.ones(64, device="cuda")
+    AW.AdamW(p).step([g, g])
+    assert torch.equal(p[0], p[1]) and p[0][0] != 0
