@@ -6,8 +6,8 @@
 The layer products run in MX4 (mx4.train_linear); the two weight matrices take
 Shampoo's direction with Adam's length per block (pipeline), the tensors that
 are not matrices take AdamW with 8-bit moments (adamw), and one norm over all
-gradients clips both.  Afterwards the weights are quantised once and single
-rows go through them.
+gradients clips both; a step whose norm is not finite changes nothing.
+Afterwards the weights are quantised once and single rows go through them.
 """
 import argparse
 import os
@@ -86,11 +86,14 @@ def train(steps=60, tokens=1024, width=256, hidden=512, block=128, lr=2e-2, seed
         for buf, g in zip(grads + vgrads, torch.autograd.grad(loss, params)):
             buf.copy_(g)
         clip = AW.grad_norm(everything, 1.0)[1:]
-        adamw.step(vtable, grad_scale=clip)
+        losses.append(loss.detach())
+        adamw.step(vtable, grad_scale=clip)      # by itself changes nothing where clip is not finite
+        if not torch.isfinite(clip):             # the factor averages would keep a NaN for good
+            log(f"step {step:4d}  skipped: the gradients' norm is not finite")
+            continue
         torch._foreach_mul_(grads, clip[0])
         shampoo.step(tables[0], tables[1])
         PL.graft_update(*tables, 0.5 * lr, 0.9, 0.95, 1e-8, step)
-        losses.append(loss.detach())
         if step % 10 == 1 or step == steps:
             log(f"step {step:4d}  loss {losses[-1].item():.4f}  clip {clip.item():.3f}")
 
