@@ -246,7 +246,7 @@ class AdamW:
         self.t += 1
 
     def moments(self, dtype=torch.float32, stream=None):
-        """The values of (m, v) as flat tensors in the state's layout."""
+        """The values of (m, v) as new flat tensors in the state's layout."""
         p = self.params
         if stream is not None:
             return _on_stream(stream, p.device, lambda: self.moments(dtype), self)
@@ -256,7 +256,7 @@ class AdamW:
         if dtype not in _TYPES:
             raise ValueError("dtype must be float32 or bfloat16")
         if self.m_scale is None:
-            return self.m.to(dtype), self.v.to(dtype)
+            return self.m.to(dtype, copy=True), self.v.to(dtype, copy=True)
         m, v = torch.empty_like(self.m, dtype=dtype), torch.empty_like(self.v, dtype=dtype)
         mc, vc, ms, vs = self._state_ptrs
         capi.check(capi.shampoo_adamw_moments(mc, ms, vc, vs, m.numel(), m.data_ptr(), v.data_ptr(), _TYPES[dtype],

@@ -93,3 +93,17 @@ def test_parameters_that_share_memory_are_refused():
     g = torch.ones(64, device="cuda")
     AW.AdamW(p).step([g, g])
     assert torch.equal(p[0], p[1]) and p[0][0] != 0
+
+
+@pytest.mark.parametrize("state", ["f32", "mx8"])
+def test_moments_are_copies(state):
+    p = torch.zeros(100, device="cuda")
+    opt = AW.AdamW([p], state=state)
+    opt.step([torch.ones_like(p)])
+    for dtype in (torch.float32, torch.bfloat16):
+        m, v = opt.moments(dtype)
+        kept = m.clone(), v.clone()
+        opt.step([torch.full_like(p, 3.0)])
+        assert torch.equal(m, kept[0]) and torch.equal(v, kept[1])
+        m.zero_(), v.zero_()
+        assert opt.m.count_nonzero() >= 100 and opt.v.count_nonzero() >= 100
