@@ -53,6 +53,10 @@ def _layout(t):
     return t.numel() if t.is_contiguous() else (tuple(t.shape), t.stride())
 
 
+def _nested_tuple(x):
+    return tuple(map(_nested_tuple, x)) if isinstance(x, (list, tuple)) else x
+
+
 class TensorTable:
     """Device table of tensors in their flat memory order (the tensors are kept
     alive with it).  All of one type, float32 or bfloat16, and dense.  A table
@@ -264,22 +268,32 @@ class AdamW:
         return m, v
 
     def state_dict(self):
-        """What a resume needs bit for bit: the moments as stored, the step count
-        and the seed.  Tensors are returned as they are."""
-        sd = {"m": self.m, "v": self.v, "t": int(self.t), "seed": int(self.seed)}
+        """What a resume needs bit for bit: the moments as stored, the layouts of
+        the tensors they belong to, the step count and the seed.  Tensors are
+        returned as they are."""
+        sd = {"m": self.m, "v": self.v, "t": int(self.t), "seed": int(self.seed), "layouts": list(self.params.layouts)}
         if self.m_scale is not None:
             sd.update(m_scale=self.m_scale, v_scale=self.v_scale)
         return sd
 
     def load_state_dict(self, sd):
-        """Restore a state_dict() of an AdamW over tensors of the same sizes and the same kind of state."""
+        """Restore a state_dict() of an AdamW over tensors of the same layouts, in
+        the same order, and the same kind of state.  Saved "layouts" may be
+        missing; then only the buffers' sizes are compared.  An error changes
+        nothing."""
         names = [k for k in ("m", "v", "m_scale", "v_scale") if getattr(self, k) is not None]
-        if {k for k in sd if k not in ("t", "seed")} != set(names):
+        if {k for k in sd if k not in ("t", "seed", "layouts")} != set(names):
             raise ValueError("the saved moments are of another kind")
+        if "layouts" in sd and _nested_tuple(sd["layouts"]) != self.params.layouts:
+            raise ValueError("the saved moments are of tensors of other layouts or in another order")
         for name in names:
             dst, src = getattr(self, name), sd[name]
             if tuple(src.shape) != tuple(dst.shape) or src.dtype != dst.dtype:
                 raise ValueError(f"{name}: saved {tuple(src.shape)} {src.dtype}, expected "
                                  f"{tuple(dst.shape)} {dst.dtype}")
-            dst.copy_(src)
-        self.t, self.seed = int(sd["t"]), int(sd["seed"])
+        t, seed = int(sd["t"]), int(sd["seed"])
+        if t < 0 or not 0 <= seed < 1 << 64:
+            raise ValueError(f"saved step count {t} or seed {seed} is out of range")
+        for name in names:
+            getattr(self, name).copy_(sd[name])
+        self.t, self.seed = t, seed

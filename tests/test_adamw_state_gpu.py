@@ -1,4 +1,5 @@
 """What the AdamW object keeps, saves and refuses, and the edges of its arithmetic."""
+import io
 import weakref
 
 import pytest
@@ -107,3 +108,39 @@ def test_moments_are_copies(state):
         assert torch.equal(m, kept[0]) and torch.equal(v, kept[1])
         m.zero_(), v.zero_()
         assert opt.m.count_nonzero() >= 100 and opt.v.count_nonzero() >= 100
+
+
+@pytest.mark.parametrize("state", ["f32", "mx8"])
+def test_moments_of_other_tensors_are_refused(state):
+    """Equal totals in another order, or another memory order of one tensor."""
+    sizes = [64, 128, 32]
+    make = lambda s: [torch.ones(n, device="cuda") for n in s]  # noqa: E731
+    saved = AW.AdamW(make(sizes), state=state)
+    saved.step(make(sizes))
+    for other in (make([128, 64, 32]), make([224]), [torch.ones(64, device="cuda"), torch.ones(32, 4, device="cuda").t(),
+                                                     torch.ones(32, device="cuda")]):
+        opt = AW.AdamW(other, state=state)
+        with pytest.raises(ValueError, match="saved"):
+            opt.load_state_dict(saved.state_dict())
+        assert opt.t == 0 and opt.m.count_nonzero() == 0 and opt.v.count_nonzero() == 0
+    f = io.BytesIO()
+    torch.save(saved.state_dict(), f)
+    f.seek(0)
+    opt = AW.AdamW(make(sizes), state=state, seed=4)
+    opt.load_state_dict(torch.load(f, weights_only=True))
+    assert opt.t == 1 and torch.equal(opt.m, saved.m) and torch.equal(opt.v, saved.v)
+    # saved without layouts: sizes are all that is checked
+    plain = {k: v for k, v in saved.state_dict().items() if k in ("m", "v", "m_scale", "v_scale", "t", "seed")}
+    AW.AdamW(make(sizes), state=state).load_state_dict(plain)
+
+
+def test_a_refused_state_changes_nothing():
+    p = torch.zeros(64, device="cuda")
+    opt = AW.AdamW([p])
+    sd = {"m": torch.ones(64, device="cuda"), "v": torch.ones(32, device="cuda"), "t": 5, "seed": 1}
+    with pytest.raises(ValueError, match="saved"):
+        opt.load_state_dict(sd)
+    sd = {"m": torch.ones(64, device="cuda"), "v": torch.ones(64, device="cuda"), "seed": 1}
+    with pytest.raises((ValueError, KeyError)):
+        opt.load_state_dict(sd)
+    assert opt.m.count_nonzero() == 0 and opt.t == 0 and opt.seed == 0
