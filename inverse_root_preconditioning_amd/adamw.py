@@ -50,7 +50,10 @@ def _dense(t):
 
 def _layout(t):
     """What two tensors must share for their flat orders to name the same elements."""
-    return t.numel() if t.is_contiguous() else (tuple(t.shape), t.stride())
+    if t.is_contiguous():
+        return t.numel()
+    # dimensions of one element are in no order
+    return tuple(size for size in t.shape if size != 1), tuple(st for st, size in zip(t.stride(), t.shape) if size != 1)
 
 
 def _nested_tuple(x):

@@ -144,3 +144,17 @@ def test_a_refused_state_changes_nothing():
     with pytest.raises((ValueError, KeyError)):
         opt.load_state_dict(sd)
     assert opt.m.count_nonzero() == 0 and opt.t == 0 and opt.seed == 0
+
+
+def test_layouts_differ_only_where_memory_does():
+    """Strides of dimensions of one element say nothing."""
+    p = torch.empty_strided((4, 1, 8), (1, 4, 4), device="cuda").zero_()
+    g = torch.empty_strided((4, 1, 8), (1, 77, 4), device="cuda").fill_(1.0)
+    h = torch.ones(8, 4, device="cuda").t()
+    assert not p.is_contiguous() and not g.is_contiguous()
+    opt = AW.AdamW([p], weight_decay=0.0, lr=0.5)
+    opt.step([g])
+    assert torch.all((p + 0.5).abs() < 1e-5)
+    opt.step([h])
+    with pytest.raises(ValueError, match="differ"):
+        opt.step([torch.ones(4, 1, 8, device="cuda")])
