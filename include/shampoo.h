@@ -394,6 +394,7 @@ size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments);
  *   m, v       device state at the tensors' offsets, 16-byte aligned: float, or
  *              for SHAMPOO_STATE_MX8 codes of one byte with m_scale and v_scale,
  *              one byte per SHAMPOO_GROUP elements (both NULL for SHAMPOO_STATE_F32)
+ *   nsegments  below 2^24 (SHAMPOO_EUNSUPPORTED: divide the list)
  *   step       1-based step count;  0 <= beta1, beta2 < 1;  eps >= 0
  *   seed       of the stochastic rounding below (unused for fp32 parameters
  *              with SHAMPOO_STATE_F32)
@@ -434,7 +435,9 @@ int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_
  *   codes  [R][Cp / 2]   two E2M1 values a byte, the lower column in the low half
  *   scales [R][Cp / 32]  one E8M0 byte s for 32 consecutive columns: 2^(s - 127)
  * with Cp = C rounded up to a multiple of 128; the columns from C to Cp hold
- * code 0.  Both arrays are 16-byte aligned.  (OCP microscaling MXFP4.) */
+ * code 0.  Both arrays are 16-byte aligned.  (OCP microscaling MXFP4.)
+ * Sides are at most 2^31, the columns of a product 2^24, and what would take
+ * 2^24 workgroups or more (from 2^28 rows of B, 2^29 of x) is SHAMPOO_EUNSUPPORTED. */
 #define SHAMPOO_MX4_PAD 128
 
 /*

@@ -11,7 +11,8 @@ using namespace shp;
 
 namespace {
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch has fewer than 2^32 threads along x, 256 of them in a workgroup.
+constexpr int64_t kMaxGrid = 0xffffffff / 256;
 constexpr int kNormBlocks = 1024;
 // Up to here one workgroup does it all: beyond, one compute unit's reading
 // (16 KB a segment) takes longer than a second launch.

@@ -10,7 +10,8 @@ using namespace shp;
 
 namespace {
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch has fewer than 2^32 threads along x, 256 of them in a workgroup.
+constexpr int64_t kMaxGrid = 0xffffffff / 256;
 constexpr int64_t kMaxSide = (int64_t)1 << 31;  // rows and columns of a matrix
 constexpr int64_t kMaxK = (int64_t)1 << 24;     // columns a product sums over (32-bit offsets within a tile)
 
