@@ -421,8 +421,10 @@ int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, con
                   uint8_t* v_scale, double lr, double beta1, double beta2, double eps, int step, uint64_t seed,
                   const float* grad_scale, hipStream_t stream);
 
-/* Values of n 8-bit moments (n a multiple of SHAMPOO_GROUP) as fp32 or bf16;
- * bf16 holds every value exactly.  Either of m and v may be NULL with its
+/* Values of n 8-bit moments (n a multiple of SHAMPOO_GROUP) as fp32 or bf16.
+ * fp32 holds every value exactly, bf16 those from 2^-126 up; smaller ones are
+ * rounded to nearest even (a v code of 1 beside the least scale is 2^-143,
+ * which becomes 0).  Either of m and v may be NULL with its
  * scale and output. */
 int shampoo_adamw_moments(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
                           int64_t n, void* m_out, void* v_out, int dtype, hipStream_t stream);

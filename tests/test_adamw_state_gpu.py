@@ -2,9 +2,11 @@
 import io
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import adamw_mx4_oracle as O
 from inverse_root_preconditioning_amd import adamw as AW
 from inverse_root_preconditioning_amd import capi
 
@@ -158,3 +160,19 @@ def test_layouts_differ_only_where_memory_does():
     opt.step([h])
     with pytest.raises(ValueError, match="differ"):
         opt.step([torch.ones(4, 1, 8, device="cuda")])
+
+
+@pytest.mark.parametrize("name", ["m", "v"])
+def test_moments_at_the_smallest_scales(name):
+    """Every code in groups of scales 1 to 40: fp32 is exact (its subnormals
+    included), bf16 is the fp32 value rounded to nearest even."""
+    opt = AW.AdamW([torch.zeros(40 * 256, device="cuda")], state="mx8")
+    codes = torch.arange(256, device="cuda").repeat(40).to(torch.uint8)
+    scale = torch.arange(1, 41, device="cuda").repeat_interleave(8).to(torch.uint8)
+    getattr(opt, name).copy_(codes)
+    getattr(opt, name + "_scale").copy_(scale)
+    i = 0 if name == "m" else 1
+    want = O.mx8_decode(codes.cpu().numpy(), scale.cpu().numpy(), **(O.M8 if name == "m" else O.V8))
+    f32 = opt.moments(torch.float32)[i]
+    assert np.array_equal(f32.double().cpu().numpy(), want)
+    assert torch.equal(opt.moments(torch.bfloat16)[i], f32.cpu().to(torch.bfloat16).cuda())
