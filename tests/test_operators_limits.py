@@ -61,3 +61,38 @@ def test_products_refuse_more_workgroups_than_a_launch_takes(dtype):
     assert product(1 << 31, 512) == f.EUNSUPPORTED
     N = 16 * BLOCKS
     assert f.shampoo_mx4_linear(FAKE, 64, FAKE, FAKE, 1, N, 64, FAKE + (1 << 20), N, dtype, 0, 0, 0) == f.EUNSUPPORTED
+
+
+SIZES = [-(1 << 63), -1, 0, 1, 16, 17, 64, 127, 128, 129, 8192, 1 << 24, (1 << 24) + 1, 1 << 31, (1 << 31) + 1,
+         (1 << 63) - 1]
+
+
+def _sides(*sizes):
+    """The code that the sizes alone decide, else None."""
+    if min(sizes) < 0:
+        return f.EINVAL
+    return f.EUNSUPPORTED if max(sizes) > 1 << 31 else None
+
+
+def test_every_size_is_refused_with_its_own_code():
+    """Without an output (or an input) every call ends before a launch: negative
+    sizes, then sizes beyond the limits, then empty results, then the pointer."""
+    big = (1 << 63) - 1
+    for m in SIZES:
+        for n in SIZES:
+            for k in SIZES:
+                want = _sides(m, n, k)
+                if want is None:
+                    want = f.EUNSUPPORTED if k > 1 << 24 else f.OK if m == 0 or n == 0 else f.EINVAL
+                assert f.shampoo_mx4_product(FAKE, FAKE, FAKE, FAKE, m, n, k, 1.0, 0.0, 0, f.T_F32, big, 0, 0, 0) == want
+                assert f.shampoo_mx4_linear(FAKE, big, FAKE, FAKE, m, n, k, 0, big, f.T_F32, 0, 0, 0) == want, (m, n, k)
+            want = _sides(m, n)
+            if want is None:
+                want = f.OK if m == 0 or n == 0 else f.EINVAL
+            assert f.shampoo_mx4_quantize(0, f.T_F32, m, n, big, FAKE, FAKE, 0, 0, 0) == want, (m, n)
+            assert f.shampoo_mx4_dequantize(FAKE, FAKE, m, n, 0, f.T_BF16, big, 0) == want, (m, n)
+        want = f.OK if m == 0 else f.EINVAL
+        assert f.shampoo_adamw(FAKE, FAKE, 0, FAKE, 1, FAKE, m, f.T_F32, f.T_F32, f.STATE_F32, 0, FAKE, 0, 0, 1e-3, 0.9,
+                               0.95, 1e-8, 1, 0, 0, 0) == want, m
+        want = f.EINVAL if m < 0 or m % 32 or m else f.OK
+        assert f.shampoo_adamw_moments(0, 0, 0, 0, m, 0, 0, f.T_F32, 0) == want, m
