@@ -87,6 +87,14 @@ def adamw(p, g, m, v, lr, b1, b2, eps, decay, step, coef=1.0):
     return p - lr * decay * p - lr * d, m, v
 
 
+def round_bf16(x, h16):
+    """x as bf16 values, stochastically: of two neighbours the one farther from 0 where f + (h + 1/2) / 65536 >= 1."""
+    a = np.abs(np.asarray(x, dtype=np.float64))
+    e = np.maximum(_floor_log2(np.where(a > 0, a, 1e-300)), -126) - 7       # of the spacing
+    n = np.floor(np.ldexp(a, -e) + (np.asarray(h16, dtype=np.float64) + 0.5) / 65536)
+    return np.copysign(np.ldexp(n, e), x)
+
+
 def grad_norm(tensors, max_norm):
     """(norm, clipping factor)."""
     n = math.sqrt(sum(float((np.asarray(t, dtype=np.float64) ** 2).sum()) for t in tensors))

@@ -1,5 +1,6 @@
 """What the AdamW object keeps, saves and refuses, and the edges of its arithmetic."""
 import io
+import math
 import weakref
 
 import numpy as np
@@ -176,3 +177,44 @@ def test_moments_at_the_smallest_scales(name):
     f32 = opt.moments(torch.float32)[i]
     assert np.array_equal(f32.double().cpu().numpy(), want)
     assert torch.equal(opt.moments(torch.bfloat16)[i], f32.cpu().to(torch.bfloat16).cuda())
+
+
+def test_bf16_parameters_round_by_the_hash():
+    """p rounds up where the hash's 16 bits say so.  fp32 leaves p within tol of
+    the exact value, so a code may differ, by one, where a threshold lies within
+    tol of it: of n places each with probability 2 tol / spacing at most."""
+    n, seed = 50000, 2 ** 33 + 1
+    r = np.random.Generator(np.random.PCG64(6))
+    p = torch.from_numpy(r.standard_normal(n)).to(torch.bfloat16).cuda()
+    opt = AW.AdamW([p], lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, seed=seed)
+    p0, m, v = p.double().cpu().numpy(), np.zeros(n), np.zeros(n)
+    for step in (1, 2, 3):
+        g = torch.from_numpy(r.standard_normal(n) * 0.1).float().cuda()
+        opt.step([g])
+        g = g.double().cpu().numpy()
+        tm = 4 * U * (0.9 * np.abs(m) + 0.1 * np.abs(g)) * 3          # of all steps so far
+        p1, m, v = O.adamw(p0, g, m, v, 1e-3, 0.9, 0.95, 1e-8, 0.1, step)
+        root = np.sqrt(v / (1 - 0.95 ** step)) + 1e-8
+        tol = 1e-3 * (32 * U * np.abs(m) + tm) / (1 - 0.9 ** step) / root + 4 * U * (np.abs(p0) + np.abs(p1))
+        bits = ((O.position_hash(np.arange(n), seed, step) * np.uint64(0x5A3C91E7)) & np.uint64(O.MASK)) >> np.uint64(16)
+        want = O.round_bf16(p1, bits)
+        got = p.double().cpu().numpy()
+        spacing = 2.0 ** (np.floor(np.log2(np.abs(p1))) - 7)
+        assert np.all(np.abs(got - want) <= spacing * 1.0001)
+        few = np.minimum(1.0, 2 * tol / spacing).sum()
+        assert (got != want).sum() <= few + 6 * math.sqrt(few) + 6
+        p0 = got
+
+
+def test_bf16_parameters_follow_small_steps_on_average():
+    """Steps of 2^-12 below 1, where bf16's spacing is 2^-8: after k of them the
+    mean over n entries is 1 - k 2^-12.  A rounding's deviation is at most half a
+    spacing, so the mean's is at most 2^-9 sqrt(k / n); fp32 adds k 2^-23."""
+    n, k = 1 << 16, 20
+    p = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    opt = AW.AdamW([p], lr=2.0 ** -12, betas=(0.9, 0.95), eps=0.0, weight_decay=0.0, seed=11)
+    g = torch.ones(n, device="cuda")
+    for _ in range(k):
+        opt.step([g])
+    mean = p.double().mean().item()
+    assert abs(mean - (1 - k * 2.0 ** -12)) <= 6 * 2.0 ** -9 * math.sqrt(k / n) + k * 2.0 ** -23

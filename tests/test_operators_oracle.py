@@ -113,3 +113,25 @@ def test_position_hash_halves_are_uniform_and_differ_by_step():
     assert abs(np.corrcoef(h.astype(float), other.astype(float))[0, 1]) < 5 / 512
     big = O.position_hash(np.array([5, 5 + (1 << 32)]), 1, 1)
     assert big[0] != big[1]
+
+
+def test_bf16_rounds_to_either_neighbour_with_the_right_mean():
+    x = np.concatenate([_rng(5).standard_normal(60), [1.0, -1.5, 2.0 ** -127, 0.0]])
+    x = x.astype(np.float32).astype(np.float64)
+    up = np.stack([O.round_bf16(x, np.full(64, h)) for h in range(0, 65536, 64)])
+    for row in (up[0], up[-1]):
+        assert np.array_equal(torch.from_numpy(row).to(torch.bfloat16).double().numpy(), row)
+    spacing = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -126))) - 7)
+    assert np.all(np.abs(up - x) < spacing) and np.all(np.abs(up.mean(0) - x) <= spacing / 1024)
+    assert np.all(up[:, 60:] == x[60:])                                  # bf16's own values stay
+
+
+def test_a_moment_that_vanishes_beside_its_group_keeps_a_root():
+    """Code 1 stands for at least 2^-33 of the group's largest v, 2^-16.5 of its root."""
+    worst = 1.0
+    for top in (1.0, 1.5, 1.99999):
+        x = np.zeros(32)
+        x[3] = top
+        v = O.mx8_decode(*O.mx8_encode(x, np.zeros(32), **O.V8), **O.V8)
+        worst = min(worst, math.sqrt(v[0] / top))
+    assert 2.0 ** -16.5 <= worst < 2.0 ** -16.49
