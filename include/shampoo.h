@@ -414,6 +414,13 @@ size_t shampoo_grad_norm_workspace_bytes(int64_t nsegments);
  * least 1: a moment that rounds to 0 cannot leave eps alone under m.
  * bf16 parameters round stochastically by the same rule (16 other bits of the
  * hash), fp32 parameters to nearest even.
+ *
+ * The bias corrections and the hash's key are formed from step and seed when
+ * the call is made.  Captured into a graph, the call repeats them on every
+ * replay: one step's bias correction, and one step's random bits, so that the
+ * rounding of 8-bit moments and bf16 parameters, unbiased over steps, is not so
+ * over replays.  Capture a call for each step, or call outside the graph, where that
+ * matters.
  */
 int shampoo_adamw(const shampoo_tensor* params, const shampoo_tensor* grads, const shampoo_tensor* copies,
                   const float* hyper, int64_t ntensors, const shampoo_segment* segments, int64_t nsegments,

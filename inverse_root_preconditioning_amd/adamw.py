@@ -169,7 +169,11 @@ class AdamW:
     seed          of the stochastic rounding: equal seeds give equal bits
 
     The moments live in flat buffers, every tensor starting at a multiple of
-    32 elements (`offsets`).  `t` counts the steps taken."""
+    32 elements (`offsets`).  `t` counts the steps taken; a step captured into a
+    graph keeps its count, so that every replay repeats its bias correction and
+    its random bits (whose rounding is then no longer unbiased over the steps),
+    and `t` does not advance.  The parameters change outside autograd's sight:
+    run a backward pass that needs their old values before the step."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, lr_scale=1.0, state="f32",
                  copies=None, seed=0):
