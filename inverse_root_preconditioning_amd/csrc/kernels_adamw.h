@@ -141,7 +141,6 @@ struct AdamwArgs {
   double omb1, omb2;                             // 1 - beta
   float lr, beta1, beta2, eps, rbc1, rsbc2;      // rbc1 = 1 / (1 - beta1^t), rsbc2 = 1 / sqrt(1 - beta2^t)
   uint32_t key;
-  int tiny_roots;                                // whether the root of a subnormal v counts beside eps
 };
 
 // One workgroup a segment (of 2048: 4096 are 1 to 5% slower on large sets and 14%
@@ -150,12 +149,14 @@ struct AdamwArgs {
 // consecutive elements, or 8 where all but the 8-bit moments are bf16 (16 bytes
 // either way: 8 floats a lane would read half cache lines).  The square root
 // and the reciprocal are the hardware's (1 ulp): they reach the parameter only,
-// far below its rounding.
+// far below its rounding.  The root takes a subnormal v for 0: with TINY, for an
+// eps that does not cover that, it is taken of v 2^64 (done for every eps that
+// costs bf16 with 8-bit moments 5%).
 //
 // HBM-bound.  302e6 parameters: fp32 throughout 1.48 ms (5.7 TB/s, the rate of a
 // large copy; 1.58 ms through the caches), bf16 with 8-bit moments 0.52 ms
 // (5.9 TB/s; 5% more with 4 elements a lane).
-template <bool PARAM_BF16, bool GRAD_BF16, bool MX8, bool COPY>
+template <bool PARAM_BF16, bool GRAD_BF16, bool MX8, bool COPY, bool TINY>
 __global__ void __launch_bounds__(256) adamw_kernel(const AdamwArgs P) {
 // Which operations are fused is written out: the codes that the moments round
 // to must not depend on the compiler's choice.
@@ -250,23 +251,11 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamwArgs P) {
         store_f32<V, kWhole>(P.m, pos, left, m);
         store_f32<V, kWhole>(P.v, pos, left, v);
       }
-      // The hardware's square root takes a subnormal for 0.  Where eps does not
-      // cover that, v 2^64 has the same significand (done for every v it costs
-      // bf16 with 8-bit moments 5%).
-      float root[V];
-      if (P.tiny_roots) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const bool tiny = v[e] < FLT_MIN;
-          root[e] = __builtin_amdgcn_sqrtf(tiny ? v[e] * 0x1p64f : v[e]) * (tiny ? 0x1p-32f : 1.f);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) root[e] = __builtin_amdgcn_sqrtf(v[e]);
-      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(root[e], P.rsbc2, P.eps));
+        const float root = TINY && v[e] < FLT_MIN ? __builtin_amdgcn_sqrtf(v[e] * 0x1p64f) * 0x1p-32f
+                                                  : __builtin_amdgcn_sqrtf(v[e]);
+        const float d = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(root, P.rsbc2, P.eps));
         p[e] = __builtin_fmaf(-step, d, p[e] * keep);
       }
       if constexpr (PARAM_BF16) {
