@@ -39,6 +39,8 @@
  *    executed the call, and one workspace must not be shared by calls that may
  *    run concurrently.  (shampoo_graft_update_noalloc takes no workspace: it
  *    uses a static device array of the library instead.)
+ *  - The stream and the memory are of the calling thread's current device (a
+ *    stream of 0 is that device's default stream).
  *  - Argument errors are returned synchronously as negative codes and nothing is
  *    enqueued.  A count of 0 (no blocks / factors) is a valid no-op.
  *  - Numerical trouble is reported per factor in a caller int32 status array on

@@ -132,7 +132,7 @@ struct Mx4Piece {
 
 // Rows only: 8 elements a lane, 4 lanes a group; a workgroup takes `lanes` x 8
 // columns of 4 x 256 / lanes rows.  Memory-bound: 16384 x 8192 bf16 in 60 us
-// (5.6 TB/s).
+// (5.6 TB/s), fp32 in 110 us (5.5).
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(const Mx4QuantArgs P) {
   constexpr int kPasses = 4;
@@ -285,8 +285,8 @@ struct Mx4DequantArgs {
 };
 
 // 16 bytes of output a lane (8 bf16, 4 floats), the rows kernel's shape.
-// Memory-bound: 16384 x 8192 to bf16 in 62 us (5.5 TB/s), to fp32 in 106 us
-// (5.8; 153 us with 8 floats a lane, half cache lines a store).
+// Memory-bound: 16384 x 8192 to bf16 in 62 us (5.5 TB/s), to fp32 in 108 us
+// (5.6; 153 us with 8 floats a lane, half cache lines a store).
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs P) {
   constexpr int kPasses = 4, E = BF16 ? 8 : 4;
@@ -398,16 +398,20 @@ __device__ __forceinline__ floatx16 mfma_mx4(const intx4& a, const intx4& b, con
 //  - A workgroup of the 256-tile stays on its compute unit and takes every 256th
 //    tile where the columns are whole scale blocks of 1024: the loads ahead of a
 //    tile's last chunks are the next tile's, and its stores end under the next
-//    tile's MFMAs (8192 x 8192 x 2048 92 -> 83 us, 8190 x 8190 x 2048 103 -> 88,
-//    16384 x 2048 x 8192 129.5 -> 126).
+//    tile's MFMAs (8192 x 8192 x 2048 91.4 -> 83.5 us, 8190 x 8190 x 2048 101.8
+//    -> 94.7, 16384 x 8192 x 1024 121.8 -> 103.9, 16384 x 2048 x 8192 132.3 -> 129.4,
+//    one box, in turn).
 //
-// Measured, 16384 x 2048 x 8192 to bf16: 126 us, 4.4 PFLOP/s, matrix cores busy
-// half of the cycles.  It is bound by power: the same MFMAs fed from registers
-// reach 9.0 PFLOP/s on zeros but 5.9 on random operands (the clock falls from
-// 2.4 to 1.4 GHz), and 8 waves a tile, which take 5% fewer cycles, take the
-// same time.  8192 x 8192 x 2048: 83 us (3.3), whose 128 MiB of output take 25
-// by themselves.  1024 x 1024 x 4096 on 64 x 64 tiles: 8.3 us, 1.3 us for 1024
-// columns.
+// Measured, 16384 x 2048 x 8192 to bf16: 128 to 142 us by box and heat, 3.9 to
+// 4.3 PFLOP/s.  A launch takes 219 600 cycles, of which the MFMAs take 131 100
+// (60%); the rest are waits, the output's among them: there is one wave a SIMD, and
+// every chunk ends in a wait for all loads.  The clock is what power leaves: 1.7 to 1.8 GHz on
+// random operands, 2.4 on zeros, where the same cycles take 93 us.  Fewer cycles
+// alone need not pay: MFMAs fed from registers fall to 1.4 GHz on random operands
+// (5.9 PFLOP/s; 9.0 on zeros), and 8 waves a tile, with 5% fewer cycles, took
+// the same time.  8192 x 8192 x 2048: 83 to 91 us (3.0 to 3.3 PFLOP/s; MFMAs in
+// 44% of the cycles), whose 128 MiB of output take 25 by themselves.
+// 1024 x 1024 x 4096 on 64 x 64 tiles: 8.3 us, 1.3 us for 1024 columns.
 // ---------------------------------------------------------------------------
 constexpr int kMx4Chunk = 256;              // columns
 constexpr int kMx4RowBytes = kMx4Chunk / 2;
@@ -817,8 +821,8 @@ __global__ void __launch_bounds__(256, 1) mx4_product_kernel(const Mx4ProductArg
 // the codes.  A may still be fp32 or bf16 (at most kMx4FewElems elements): then
 // the workgroup quantises it into LDS while its first rows of B are on their
 // way, which saves a launch and A's way through memory.  Measured, one bf16 row
-// by 8192 x 2048: 3.6 us (a launch alone takes 2), by 8192 x 8192: 8.4 us
-// (4.2 TB/s); 16 rows by 8192 x 8192, B read for two tiles at a time: 10.3 us.
+// by 8192 x 2048: 4.2 us (a launch alone takes 2), by 8192 x 8192: 9.0 us
+// (4.2 TB/s); 16 rows by 8192 x 8192, B read for two tiles at a time: 10.4 us.
 // ---------------------------------------------------------------------------
 enum { MX4_A_MX4 = 0, MX4_A_F32 = 1, MX4_A_BF16 = 2 };
 constexpr int kMx4FewElems = 16384;
