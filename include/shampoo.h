@@ -19,6 +19,9 @@
  *   shampoo_mx4_quantize     4-bit microscaled (MX4) copies of a matrix, along its rows and columns
  *   shampoo_mx4_product      C <- alpha A B^T + beta C on MX4 operands
  *   shampoo_mx4_linear       Y = mx4(X) W^T with an MX4 weight
+ *   shampoo_mx8_quantize     8-bit microscaled (MX8) copies of activations
+ *   shampoo_activation       f(a) or f(a) b, the inputs kept in MX8 for the gradient
+ *   shampoo_join             a block's output normed, gated, added to the residual and normed for the next block
  *
  * Sources (cited by page title and section): "DASH: Faster Shampoo via Batched
  * Block Preconditioning and Efficient Inverse-Root Solvers", the howistudyai.com
@@ -497,6 +500,165 @@ int shampoo_mx4_linear(const void* x, int64_t ldx, const uint8_t* w_codes, const
 /* Workspace sizes of the two calls above (0 for invalid sizes too). */
 size_t shampoo_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* -------------------------------------------------------------------------
+ * MX8: activations kept in 8 bits
+ * ---------------------------------------------------------------------- */
+
+/* An MX8 matrix of R rows and C columns is a pair of byte arrays,
+ *   codes  [R][Cp]        sign + OCP E4M3 (bias 7), one value a byte
+ *   scales [R][Cp / 32]   one byte s for 32 consecutive columns: 2^(s - 127)
+ * with Cp = C rounded up to a multiple of 32; the columns from C to Cp hold
+ * code 0.  Both arrays are 16-byte aligned.  (The format of AdamW's 8-bit first moments,
+ * by rows and rounded to nearest even.)  At most 2^31 rows and 2^29 columns; beyond these, and where 2^24 workgroups
+ * would be needed, calls here and of the activations are SHAMPOO_EUNSUPPORTED. */
+
+/*
+ * shampoo_mx8_quantize -- MX8 copy of x, a device matrix [rows][cols] of dtype
+ * with row stride ld >= cols.  s = max(E - 7, 1) with E the exponent field of
+ * the group's largest magnitude as fp32; codes round to nearest even and none
+ * saturates.  A group with an entry that is not finite gets codes 0 and s = 255
+ * (NaN).
+ */
+int shampoo_mx8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                         uint8_t* scales, hipStream_t stream);
+
+/* Values of an MX8 matrix, as fp32 (exact) or bf16 (exact from 2^-126 up,
+ * smaller ones rounded to nearest even), row stride ld >= cols. */
+int shampoo_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                           int dtype, int64_t ld, hipStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * Activations
+ * ---------------------------------------------------------------------- */
+
+enum {
+  SHAMPOO_ACT_SILU = 0,       /* x / (1 + exp(-x)) */
+  SHAMPOO_ACT_GELU = 1,       /* x Phi(x), Phi the normal distribution */
+  SHAMPOO_ACT_GELU_TANH = 2,  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+  SHAMPOO_ACT_RELU = 3,       /* max(x, 0), slope 0 at 0 */
+  SHAMPOO_ACT_RELU2 = 4       /* max(x, 0)^2 */
+};
+
+/*
+ * shampoo_activation -- y = f(a), or y = f(a) b where b is given; fp32
+ * arithmetic, rounded once.
+ *
+ *   a, b, y    device matrices [rows][cols] of dtype, row strides lda, ldb, ldy;
+ *              b may be NULL; y apart from a and b.  a and b may be halves
+ *              of one matrix
+ *   a_codes .. b_scales   NULL, or MX8 matrices that receive a (and b, where
+ *              there is one) for the backward pass
+ */
+int shampoo_activation(int act, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols,
+                       int dtype, void* y, int64_t ldy, uint8_t* a_codes, uint8_t* a_scales, uint8_t* b_codes,
+                       uint8_t* b_scales, hipStream_t stream);
+
+/*
+ * shampoo_activation_backward -- da = dy f'(a) [b], db = dy f(a).
+ *
+ *   gated      whether there is a b
+ *   a, b       the inputs, or where a_codes is given, their MX8 copies (a and b
+ *              are then not used)
+ *   da, db     of dtype; either may be NULL.  They may be halves of one matrix
+ */
+int shampoo_activation_backward(int act, const void* dy, int64_t lddy, const void* a, int64_t lda, const void* b,
+                                int64_t ldb, const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                                const uint8_t* b_scales, int gated, int64_t rows, int64_t cols, int dtype, void* da,
+                                int64_t ldda, void* db, int64_t lddb, hipStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * Norms, and the join of a block with its residual
+ * ---------------------------------------------------------------------- */
+
+enum {
+  SHAMPOO_NORM_NONE = 0,
+  SHAMPOO_NORM_RMS = 1,
+  SHAMPOO_NORM_LAYER = 2
+};
+
+enum {
+  SHAMPOO_GATE_NONE = 0,
+  SHAMPOO_GATE_ROWS = 1,   /* [rows / gate_rows][cols]: a row of the gate for every gate_rows rows */
+  SHAMPOO_GATE_TOKEN = 2   /* [rows]: a number for each row */
+};
+
+/* N(x) = (x - mean) s w + b over each row: RMS: mean = 0, s = 1 / sqrt(mean of
+ * x^2 + eps); layer: s = 1 / sqrt(variance + eps).  Vectors of `cols` elements,
+ * NULL: w = 1, b = 0. */
+typedef struct shampoo_norm {
+  int64_t kind;
+  double eps;              /* > 0; as fp32 */
+  const void* weight;
+  int64_t weight_dtype;
+  const void* bias;
+  int64_t bias_dtype;
+} shampoo_norm;
+
+/*
+ * A join: with the residual r and a block's output y,
+ *   z = N1(y),  h = scale r + gate z,  u = N2(h)       (N1 = after, N2 = before)
+ * Either norm may be absent (kind SHAMPOO_NORM_NONE: z = y, no u), and so may y:
+ * then h = r, nothing is written for it, and the join is the norm of r.
+ *
+ * Every matrix is [rows][cols] in device memory with a row stride (ld_) of at
+ * least cols, of stream_dtype (r, h and their gradients) or branch_dtype (y, u
+ * and theirs): equal, or fp32 and bf16.  Outputs are apart from inputs and each
+ * other.  1 <= cols <= SHAMPOO_NORM_COLS for what has rows.  All members are 8
+ * bytes wide; unused ones are 0.
+ */
+#define SHAMPOO_NORM_COLS 16384
+typedef struct shampoo_join {
+  int64_t rows, cols, stream_dtype, branch_dtype;
+  const void* residual;
+  int64_t ld_residual;
+  const void* branch;      /* NULL: a norm only */
+  int64_t ld_branch;
+  double scale;            /* as fp32 */
+  shampoo_norm after, before;
+  int64_t gate_kind;       /* SHAMPOO_GATE_*; the gate is dense */
+  const void* gate;
+  int64_t gate_dtype, gate_rows;
+  /* Kept for the backward pass: MX8 copies of the inputs (all NULL: backward
+   * is given the inputs themselves), and fp32 [rows][2] mean and s of each norm
+   * (NULL in a forward pass without a backward one). */
+  uint8_t *residual_codes, *residual_scales, *branch_codes, *branch_scales;
+  float *after_stats, *before_stats;
+} shampoo_join;
+
+/*
+ * shampoo_join_forward -- h and u (each needed where the join has one).  The MX8
+ * copies and statistics that have an address are written.
+ */
+int shampoo_join_forward(const shampoo_join* join, void* h, int64_t ld_h, void* u, int64_t ld_u, hipStream_t stream);
+
+/* Gradients: of the outputs, where there is one (NULL: zero), and of what is
+ * wanted (else NULL).  Those of parameters have the parameters' types, and
+ * the gate's layout. */
+typedef struct shampoo_join_grads {
+  const void* d_h;
+  int64_t ld_d_h;
+  const void* d_u;
+  int64_t ld_d_u;
+  void* d_residual;
+  int64_t ld_d_residual;
+  void* d_branch;
+  int64_t ld_d_branch;
+  void *d_after_weight, *d_after_bias, *d_gate, *d_before_weight, *d_before_bias;
+} shampoo_join_grads;
+
+/*
+ * shampoo_join_backward -- the inputs are taken as shampoo_join_forward kept them: with codes,
+ * from these (residual and branch then only have to be not NULL where there is such an
+ * input); the row statistics are read, never formed again.  Sums over rows
+ * are of fixed order: the same call gives the same bits.  The residual's codes
+ * are read only where there is d_u, the branch's only with a norm after
+ * it, a gate or d_u.
+ *   ws         shampoo_join_workspace_bytes(rows, cols, gate_rows of SHAMPOO_GATE_ROWS else 0) bytes
+ */
+int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* grads, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+size_t shampoo_join_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows);
 
 /* Workspace size in bytes for an operation (op = SHAMPOO_OP_*).  `count` is
  * nfactors for SCALE/NEWTON/CHEBY and nblocks for ACCUMULATE/PRECONDITION;

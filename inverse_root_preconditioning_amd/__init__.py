@@ -6,4 +6,4 @@ torch-tensor convenience layer.  ``workloads`` holds the seeded synthetic
 inputs.  Importing the package does not load the library; the first call
 into ``capi`` does, and raises if it has not been built.
 """
-__all__ = ["adamw", "capi", "mx4", "pipeline", "workloads"]
+__all__ = ["adamw", "capi", "layers", "mx4", "mx8", "pipeline", "workloads"]

@@ -20,8 +20,10 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libshampoo_mi355x.so")
 ARCH = os.environ.get("SHAMPOO_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["shampoo.hip", "adamw.hip", "mx4.hip"]
-HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h", "vector_io.h", "kernels_adamw.h", "kernels_mx4.h"]
+SOURCES = ["shampoo.hip", "adamw.hip", "mx4.hip", "layers.hip", "norm.hip", "norm_back_bf16.hip", "norm_back_f32.hip",
+           "norm_back_mixed.hip"]
+HEADERS = ["common.h", "gemm_f32.h", "gemm_bf16.h", "kernels_misc.h", "vector_io.h", "kernels_adamw.h", "kernels_mx4.h",
+           "host.h", "kernels_mx8.h", "kernels_act.h", "kernels_norm.h", "kernels_norm_sums.h", "norm_launch.h"]
 
 
 def hipcc():

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libshampoo_mi355x.so")
@@ -57,6 +58,19 @@ STATE_MX8 = 1
 GROUP = 32                # elements that share a scale byte
 SEGMENT = 2048
 MX4_PAD = 128             # columns of an MX4 matrix are padded to a multiple of this
+# Activations, norms and gates of the layers
+ACT_SILU = 0
+ACT_GELU = 1
+ACT_GELU_TANH = 2
+ACT_RELU = 3
+ACT_RELU2 = 4
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
+GATE_NONE = 0
+GATE_ROWS = 1
+GATE_TOKEN = 2
+NORM_COLS = 16384         # most columns of a norm
 
 ABI_VERSION = 3
 
@@ -75,6 +89,33 @@ class shampoo_tensor(ctypes.Structure):
 
 class shampoo_segment(ctypes.Structure):
     _fields_ = [("tensor", c_int32), ("index", c_int32)]
+
+
+class shampoo_norm(ctypes.Structure):
+    _fields_ = [("kind", c_int64), ("eps", c_double), ("weight", c_void_p), ("weight_dtype", c_int64),
+                ("bias", c_void_p), ("bias_dtype", c_int64)]
+
+
+class shampoo_join(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("stream_dtype", c_int64), ("branch_dtype", c_int64),
+                ("residual", c_void_p), ("ld_residual", c_int64), ("branch", c_void_p), ("ld_branch", c_int64),
+                ("scale", c_double), ("after", shampoo_norm), ("before", shampoo_norm),
+                ("gate_kind", c_int64), ("gate", c_void_p), ("gate_dtype", c_int64), ("gate_rows", c_int64),
+                ("residual_codes", c_void_p), ("residual_scales", c_void_p),
+                ("branch_codes", c_void_p), ("branch_scales", c_void_p),
+                ("after_stats", c_void_p), ("before_stats", c_void_p)]
+
+
+class shampoo_join_grads(ctypes.Structure):
+    _fields_ = [("d_h", c_void_p), ("ld_d_h", c_int64), ("d_u", c_void_p), ("ld_d_u", c_int64),
+                ("d_residual", c_void_p), ("ld_d_residual", c_int64), ("d_branch", c_void_p), ("ld_d_branch", c_int64),
+                ("d_after_weight", c_void_p), ("d_after_bias", c_void_p), ("d_gate", c_void_p),
+                ("d_before_weight", c_void_p), ("d_before_bias", c_void_p)]
+
+
+# The same layouts for one call of pack (a tenth of the time of filling a Structure).
+JOIN = struct.Struct("=4qQqQqdqdQqQqqdQqQqqQqq6Q")
+JOIN_GRADS = struct.Struct("=QqQqQqQq5Q")
 
 
 class ShampooError(RuntimeError):
@@ -129,6 +170,16 @@ _SIGNATURES = {
                                    c_int64, c_int, c_void_p, c_size_t, c_void_p]),
     "shampoo_mx4_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
     "shampoo_mx4_linear_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "shampoo_mx8_quantize": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "shampoo_mx8_dequantize": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int, c_int64, c_void_p]),
+    "shampoo_activation": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p,
+                                   c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "shampoo_activation_backward": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                            c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_int, c_void_p,
+                                            c_int64, c_void_p, c_int64, c_void_p]),
+    "shampoo_join_forward": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "shampoo_join_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "shampoo_join_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -272,3 +323,36 @@ def shampoo_mx4_workspace_bytes(M, N, K):
 
 def shampoo_mx4_linear_workspace_bytes(M, N, K):
     return load().shampoo_mx4_linear_workspace_bytes(M, N, K)
+
+
+def shampoo_mx8_quantize(x, dtype, rows, cols, ld, codes, scales, stream):
+    return load().shampoo_mx8_quantize(x, dtype, rows, cols, ld, codes, scales, stream)
+
+
+def shampoo_mx8_dequantize(codes, scales, rows, cols, out, dtype, ld, stream):
+    return load().shampoo_mx8_dequantize(codes, scales, rows, cols, out, dtype, ld, stream)
+
+
+def shampoo_activation(act, a, lda, b, ldb, rows, cols, dtype, y, ldy, a_codes, a_scales, b_codes, b_scales, stream):
+    return load().shampoo_activation(act, a, lda, b, ldb, rows, cols, dtype, y, ldy, a_codes, a_scales, b_codes,
+                                     b_scales, stream)
+
+
+def shampoo_activation_backward(act, dy, lddy, a, lda, b, ldb, a_codes, a_scales, b_codes, b_scales, gated, rows, cols,
+                                dtype, da, ldda, db, lddb, stream):
+    return load().shampoo_activation_backward(act, dy, lddy, a, lda, b, ldb, a_codes, a_scales, b_codes, b_scales, gated,
+                                              rows, cols, dtype, da, ldda, db, lddb, stream)
+
+
+def shampoo_join_forward(join, h, ld_h, u, ld_u, stream):
+    """join: bytes of JOIN.pack, or the address of a shampoo_join."""
+    return load().shampoo_join_forward(join, h, ld_h, u, ld_u, stream)
+
+
+def shampoo_join_backward(join, grads, ws, ws_bytes, stream):
+    """join, grads: bytes of JOIN.pack and JOIN_GRADS.pack, or addresses of the structures."""
+    return load().shampoo_join_backward(join, grads, ws, ws_bytes, stream)
+
+
+def shampoo_join_workspace_bytes(rows, cols, gate_rows):
+    return load().shampoo_join_workspace_bytes(rows, cols, gate_rows)

@@ -1,0 +1,200 @@
+// Activations y = f(a) and gated activations y = f(a) b with their gradients,
+// elementwise over matrices, the inputs optionally kept as MX8 rows.
+#pragma once
+
+#include "kernels_mx8.h"
+
+namespace shp {
+
+// exp(-v) for 0 <= v <= 150.  FINE: to about an ulp, v (given in two floats)
+// times log2(e) in two floats, so that the error of a large exponent does not
+// reach the result.  Else within 2^-15: v's own rounding and that of the
+// product, up to 300 ulps where v is large, which a bf16 result (half a step: 2^-9) does not show.
+template <bool FINE>
+__device__ __forceinline__ float exp_minus(float v, float v_low = 0.f) {
+  constexpr float kHi = 1.44269504088896341f, kLo = 1.9259629911e-8f;  // log2(e) and what fp32 leaves of it
+  const float t = -v * kHi;
+  const float e = __builtin_amdgcn_exp2f(t);
+  if constexpr (!FINE) return e;
+  const float low = __builtin_fmaf(-v_low, kHi, __builtin_fmaf(-v, kLo, __builtin_fmaf(-v, kHi, -t)));
+  return __builtin_fmaf(e, low * 0.693147180559945309f, e);
+}
+
+// x within +-limit; a NaN stays one.
+__device__ __forceinline__ float clamp_abs(float x, float limit) {
+  x = x > limit ? limit : x;
+  return x < -limit ? -limit : x;
+}
+
+// f(x) and, with SLOPE, f'(x); FINE for fp32 results (see exp_minus).  Beyond the
+// clamps f is 0 or x and f' 0 or 1 to the last bit, and no intermediate result overflows into a
+// NaN.  (The exponential is 0 below 2^-126, so that far tails end there.)
+template <int ACT, bool SLOPE, bool FINE>
+__device__ __forceinline__ void activation(float x, float& f, float& d) {
+  if constexpr (ACT == SHAMPOO_ACT_RELU) {
+    f = x < 0.f ? 0.f : x;
+    if (SLOPE) d = x > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == SHAMPOO_ACT_RELU2) {
+    const float r = x < 0.f ? 0.f : x;
+    f = r * r;
+    if (SLOPE) d = 2.f * r;
+  } else if constexpr (ACT == SHAMPOO_ACT_GELU) {
+    // x Phi(x), with Phi(-z) = exp(-z^2/2) t Q(t), t = 1 / (1 + 0.225 z): Q is
+    // the polynomial of degree 10 nearest to erfcx(z / sqrt 2) / (2 t) on all of
+    // z >= 0 (relative 1.0e-8; reweighted least squares at 400 Chebyshev
+    // points of t).  The tail keeps its relative precision, which 1 + erf loses.
+    const float c = clamp_abs(x, 15.f), z = fabsf(c);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.225f, z, 1.f));
+    float q = 0.016711030155420303f;
+    q = __builtin_fmaf(q, t, -0.07665678858757019f);
+    q = __builtin_fmaf(q, t, 0.11226222664117813f);
+    q = __builtin_fmaf(q, t, -0.0657426118850708f);
+    q = __builtin_fmaf(q, t, 0.07158230245113373f);
+    q = __builtin_fmaf(q, t, 0.03579634428024292f);
+    q = __builtin_fmaf(q, t, 0.06539952754974365f);
+    q = __builtin_fmaf(q, t, 0.07589364796876907f);
+    q = __builtin_fmaf(q, t, 0.08523055911064148f);
+    q = __builtin_fmaf(q, t, 0.08976174890995026f);
+    q = __builtin_fmaf(q, t, 0.08976201713085175f);
+    const float h = 0.5f * z, s = h * z;
+    const float e = exp_minus<FINE>(s, __builtin_fmaf(h, z, -s));
+    const float tail = e * (q * t);
+    const float p = x < 0.f ? tail : 1.f - tail;
+    f = x * p;
+    if (SLOPE) d = __builtin_fmaf(c * e, 0.398942280401432678f, p);
+  } else {
+    // x p with p = 1 / (1 + exp(-v)): v = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)
+    constexpr bool kTanh = ACT == SHAMPOO_ACT_GELU_TANH;
+    constexpr float kA = 1.59576912160573071f, kALow = -4.534068054e-8f, kB = 0.044715f, kBLow = 1.546144435e-9f;
+    const float c = clamp_abs(x, kTanh ? 11.f : 105.f);  // v at most 112 and 105: e is 0 in fp32 from 104 on
+    float v, v_low = 0.f;
+    if constexpr (kTanh && FINE) {
+#pragma clang fp contract(off)
+      // A c (1 + B c^2) in two floats: every product's error by a fused one, the sum's by its own terms
+      const float q = c * c, q_low = __builtin_fmaf(c, c, -q);
+      const float m = kB * q, m_low = __builtin_fmaf(kB, q, -m) + __builtin_fmaf(kB, q_low, kBLow * q);
+      const float w = 1.f + m, back = w - 1.f;
+      const float w_low = (1.f - (w - back)) + (m - back) + m_low;
+      const float u = kA * c, u_low = __builtin_fmaf(kA, c, -u) + kALow * c;
+      v = u * w;
+      v_low = __builtin_fmaf(u, w, -v) + __builtin_fmaf(u, w_low, u_low * w);
+      v_low = v < 0.f ? -v_low : v_low;
+    } else {
+      v = kTanh ? kA * __builtin_fmaf(kB * c, c * c, c) : c;
+    }
+    const float e = exp_minus<FINE>(fabsf(v), v_low);
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    const float er = e * r;
+    const float p = x < 0.f ? er : r;
+    f = x * p;
+    if (SLOPE) {
+      const float slope = kTanh ? kA * __builtin_fmaf(3.f * kB, c * c, 1.f) : 1.f;
+      d = __builtin_fmaf(c * slope, er * r, p);
+    }
+  }
+}
+
+struct ActArgs {
+  const void *a, *b, *dy;
+  void *y, *da, *db;
+  int64_t lda, ldb, lddy, ldy, ldda, lddb;
+  int64_t rows;
+  uint32_t cols;
+  Mx8Rows ka, kb;  // kept inputs
+  RowShape shape;
+};
+
+constexpr int kActPasses = 4;
+
+template <bool BF16, int ACT, bool GATED, bool KEEP>
+__global__ void __launch_bounds__(256) act_forward_kernel(const ActArgs P) {
+  constexpr int V = BF16 ? 8 : 4;
+  const uint32_t rb = blockIdx.x / P.shape.col_blocks, cb = blockIdx.x - rb * P.shape.col_blocks;
+  const int lanes = 1 << P.shape.lanes_log2, per_pass = 256 >> P.shape.lanes_log2;
+  const uint32_t col = (cb * lanes + (threadIdx.x & (lanes - 1))) * V;
+  const int64_t row0 = (int64_t)rb * kActPasses * per_pass + (threadIdx.x >> P.shape.lanes_log2);
+  Piece<BF16, V> a[kActPasses], b[kActPasses];
+#pragma unroll
+  for (int i = 0; i < kActPasses; ++i) {
+    const int64_t r = min(row0 + i * per_pass, P.rows - 1);
+    a[i] = load_row<BF16, V>(row_at<BF16>(P.a, r, P.lda), P.cols, col);
+    if constexpr (GATED) b[i] = load_row<BF16, V>(row_at<BF16>(P.b, r, P.ldb), P.cols, col);
+  }
+#pragma unroll
+  for (int i = 0; i < kActPasses; ++i) {
+    const int64_t r = row0 + i * per_pass;
+    if constexpr (KEEP) {
+      Mx8Piece<V> q;
+      q.encode(a[i]);
+      if (r < P.rows) q.store(P.ka, r, col);
+      if constexpr (GATED) {
+        q.encode(b[i]);
+        if (r < P.rows) q.store(P.kb, r, col);
+      }
+    }
+    if (r < P.rows) {
+      float y[V], unused;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        activation<ACT, false, !BF16>(elem(a[i], e), y[e], unused);
+        if constexpr (GATED) y[e] *= elem(b[i], e);
+      }
+      store_row<BF16, V>(row_at<BF16>(P.y, r, P.ldy), P.cols, col, y);
+    }
+  }
+}
+
+template <bool BF16, int ACT, bool GATED, bool KEEP>
+__global__ void __launch_bounds__(256) act_backward_kernel(const ActArgs P) {
+  constexpr int V = BF16 ? 8 : 4;
+  const uint32_t rb = blockIdx.x / P.shape.col_blocks, cb = blockIdx.x - rb * P.shape.col_blocks;
+  const int lanes = 1 << P.shape.lanes_log2, per_pass = 256 >> P.shape.lanes_log2;
+  const uint32_t col = (cb * lanes + (threadIdx.x & (lanes - 1))) * V;
+  const int64_t row0 = (int64_t)rb * kActPasses * per_pass + (threadIdx.x >> P.shape.lanes_log2);
+  if (col >= P.cols) return;
+  Piece<BF16, V> dy[kActPasses], a[kActPasses], b[kActPasses];
+  Mx8Piece<V> qa[kActPasses], qb[kActPasses];
+#pragma unroll
+  for (int i = 0; i < kActPasses; ++i) {
+    const int64_t r = min(row0 + i * per_pass, P.rows - 1);
+    dy[i] = load_row<BF16, V>(row_at<BF16>(P.dy, r, P.lddy), P.cols, col);
+    if constexpr (KEEP) {
+      qa[i].load(P.ka, r, col);
+      if constexpr (GATED) qb[i].load(P.kb, r, col);
+    } else {
+      a[i] = load_row<BF16, V>(row_at<BF16>(P.a, r, P.lda), P.cols, col);
+      if constexpr (GATED) b[i] = load_row<BF16, V>(row_at<BF16>(P.b, r, P.ldb), P.cols, col);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kActPasses; ++i) {
+    const int64_t r = row0 + i * per_pass;
+    if (r >= P.rows) return;
+    float av[V], bv[V], da[V], db[V];
+    if constexpr (KEEP) {
+      qa[i].decode(av);
+      if constexpr (GATED) qb[i].decode(bv);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if constexpr (!KEEP) {
+        av[e] = elem(a[i], e);
+        if constexpr (GATED) bv[e] = elem(b[i], e);
+      }
+      float f, d;
+      activation<ACT, true, !BF16>(av[e], f, d);
+      const float g = elem(dy[i], e);
+      da[e] = g * d;
+      if constexpr (GATED) {
+        da[e] *= bv[e];
+        db[e] = g * f;
+      }
+    }
+    if (P.da != nullptr) store_row<BF16, V>(row_at<BF16>(P.da, r, P.ldda), P.cols, col, da);
+    if constexpr (GATED) {
+      if (P.db != nullptr) store_row<BF16, V>(row_at<BF16>(P.db, r, P.lddb), P.cols, col, db);
+    }
+  }
+}
+
+}  // namespace shp

@@ -25,13 +25,6 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t top_bits) {
 // nearest even and saturate at 6.
 __device__ __forceinline__ float mx4_scale_float(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
 
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
-                                                                __builtin_bit_cast(u16x2, b)));
-}
-__device__ __forceinline__ uint32_t abs_halves(uint32_t a) { return a & 0x7fff7fffu; }
-
 // Byte SEL of `old` replaced by the codes of two values.
 template <int SEL>
 __device__ __forceinline__ uint32_t mx4_codes_bf16(uint32_t old, uint32_t pair, float scale) {
@@ -52,68 +45,10 @@ struct Mx4QuantArgs {
   int lanes_log2;                    // rows kernel: lanes on a row
 };
 
-// V consecutive elements of a row: bf16, two a word, or fp32 bits.
+// A piece of a row with its codes.
 template <bool BF16, int V>
-struct Mx4Piece {
-  static constexpr int kElems = V, kWords = BF16 ? V / 2 : V;
-  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
-  Words w;
-  __device__ __forceinline__ void load(const void* x, int64_t at) {
-    if constexpr (BF16) {
-      w = ldg_any<Words, 2>(static_cast<const uint16_t*>(x) + at);
-    } else {
-      w = ldg_any<Words, 4>(static_cast<const float*>(x) + at);
-    }
-  }
-  // The piece at (row, col) of a matrix whose edge it may cross (or pass), zero
-  // outside.  No branch on the lane: V elements that are there, shifted down.
-  __device__ __forceinline__ void load_edge(const void* x, int64_t rows, int64_t cols, int64_t ld, int64_t row,
-                                            int64_t col) {
-    if (cols >= V) {
-      const int64_t from = min(col, cols - V);
-      const uint32_t d = row < rows ? (uint32_t)min<int64_t>(col - from, V) : (uint32_t)V;
-      load(x, min(row, rows - 1) * ld + from);
-      if constexpr (BF16) {
-        if (d & 1) {
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) w[i] = (w[i] >> 16) | (i + 1 < kWords ? w[i + 1] << 16 : 0u);
-        }
-      }
-#pragma unroll
-      for (int b = 1; b < kWords; b *= 2) {
-        if (d & (BF16 ? 2 * b : b)) {
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) w[i] = i + b < kWords ? w[i + b] : 0u;
-        }
-      }
-      if (d == V) w = (Words)0u;
-    } else {
-      w = (Words)0u;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (row < rows && col + e < cols) {
-          if constexpr (BF16) {
-            w[e / 2] |= (uint32_t)ldg(static_cast<const uint16_t*>(x) + row * ld + col + e) << (16 * (e & 1));
-          } else {
-            w[e] = ldg(static_cast<const uint32_t*>(x) + row * ld + col + e);
-          }
-        }
-      }
-    }
-  }
-  // Bits, as fp32, of the largest magnitude.
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0;
-    if constexpr (BF16) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) m = max_halves(m, abs_halves(w[i]));
-      return max(m & 0xffff0000u, m << 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
-      return m;
-    }
-  }
+struct Mx4Piece : Piece<BF16, V> {
+  using Piece<BF16, V>::w;
   // V / 2 bytes of codes.
   __device__ __forceinline__ uint32_t encode(float scale) const {
     uint32_t c = 0;

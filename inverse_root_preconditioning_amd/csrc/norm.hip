@@ -1,0 +1,270 @@
+// C entry points of norms and joins (gfx950): arguments are checked on the
+// host, kernels enqueued on the caller's stream; nothing is allocated and
+// nothing synchronises.
+#include <algorithm>
+#include <cmath>
+
+#include "kernels_norm_sums.h"
+#include "norm_launch.h"
+
+using namespace shp;
+
+namespace {
+
+template <bool SB, bool BB>
+int forward(const JoinArgs& a, hipStream_t stream) {
+  return with_row_shape<SB ? 8 : 4>(a.cols, [&](auto w, auto p) {
+    constexpr int W = decltype(w)::value, P = decltype(p)::value;
+    const int64_t blocks = std::min<int64_t>((a.rows + kRowLanes<W> - 1) / kRowLanes<W>, 1 << 20);
+    const dim3 grid((uint32_t)blocks), block(kRowThreads<W>);
+    if (a.y != nullptr) {
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true>), grid, block, 0, stream, a);
+    } else {
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false>), grid, block, 0, stream, a);
+    }
+    return check_launch();
+  });
+}
+
+int valid_norm(const shampoo_norm& n) {
+  if (n.kind == SHAMPOO_NORM_NONE) return SHAMPOO_OK;
+  if (n.kind != SHAMPOO_NORM_RMS && n.kind != SHAMPOO_NORM_LAYER) return SHAMPOO_EUNSUPPORTED;
+  if (!((float)n.eps > 0.f) || !std::isfinite((float)n.eps)) return SHAMPOO_EINVAL;
+  if (n.weight != nullptr && !valid_type(n.weight_dtype)) return SHAMPOO_EUNSUPPORTED;
+  if (n.bias != nullptr && !valid_type(n.bias_dtype)) return SHAMPOO_EUNSUPPORTED;
+  return SHAMPOO_OK;
+}
+
+NormSide norm_side(const shampoo_norm& n) {
+  NormSide s = {};
+  s.kind = (int)n.kind;
+  if (n.kind == SHAMPOO_NORM_NONE) return s;
+  s.w = n.weight;
+  s.b = n.bias;
+  s.w_bf16 = n.weight_dtype == SHAMPOO_T_BF16;
+  s.b_bf16 = n.bias_dtype == SHAMPOO_T_BF16;
+  s.eps = (float)n.eps;
+  return s;
+}
+
+// What both directions check; `empty` where there is nothing to do.
+int common(const shampoo_join* j, JoinArgs* a, bool* empty) {
+  if (j == nullptr) return SHAMPOO_EINVAL;
+  *empty = false;
+  if (!valid_type(j->stream_dtype) || !valid_type(j->branch_dtype)) return SHAMPOO_EUNSUPPORTED;
+  if (j->stream_dtype == SHAMPOO_T_BF16 && j->branch_dtype == SHAMPOO_T_F32) return SHAMPOO_EUNSUPPORTED;
+  int rc = check_sides(j->rows, j->cols);
+  if (rc != SHAMPOO_OK) return rc;
+  if (j->cols > SHAMPOO_NORM_COLS) return SHAMPOO_EUNSUPPORTED;
+  if ((rc = valid_norm(j->after)) != SHAMPOO_OK || (rc = valid_norm(j->before)) != SHAMPOO_OK) return rc;
+  if (j->gate_kind < SHAMPOO_GATE_NONE || j->gate_kind > SHAMPOO_GATE_TOKEN) return SHAMPOO_EUNSUPPORTED;
+  const bool join = j->branch != nullptr;
+  if (!join && (j->after.kind != SHAMPOO_NORM_NONE || j->gate_kind != SHAMPOO_GATE_NONE ||
+                j->before.kind == SHAMPOO_NORM_NONE))
+    return SHAMPOO_EINVAL;
+  if (j->gate_kind != SHAMPOO_GATE_NONE && !valid_type(j->gate_dtype)) return SHAMPOO_EUNSUPPORTED;
+  if (j->gate_kind == SHAMPOO_GATE_ROWS && (j->gate_rows < 1 || j->gate_rows > kMaxRows || j->rows % j->gate_rows != 0))
+    return SHAMPOO_EINVAL;
+  if (join && !std::isfinite((float)j->scale)) return SHAMPOO_EINVAL;
+  if (j->rows == 0 || j->cols == 0) {
+    *empty = true;
+    return SHAMPOO_OK;
+  }
+  if (j->gate_kind != SHAMPOO_GATE_NONE && j->gate == nullptr) return SHAMPOO_EINVAL;
+  *a = JoinArgs{};
+  a->rows = j->rows;
+  a->cols = (uint32_t)j->cols;
+  a->scale = join ? (float)j->scale : 1.f;
+  a->r = j->residual;
+  a->y = j->branch;
+  a->ldr = j->ld_residual;
+  a->ldy = j->ld_branch;
+  const uint32_t padded = (uint32_t)mx8_padded(j->cols);
+  a->kr = Mx8Rows{j->residual_codes, j->residual_scales, padded};
+  a->ky = Mx8Rows{j->branch_codes, j->branch_scales, padded};
+  if ((a->kr.codes != nullptr || a->kr.scales != nullptr) && !valid_mx8(a->kr.codes, a->kr.scales))
+    return SHAMPOO_EINVAL;
+  if ((a->ky.codes != nullptr || a->ky.scales != nullptr) && !valid_mx8(a->ky.codes, a->ky.scales))
+    return SHAMPOO_EINVAL;
+  if (!join && a->ky.codes != nullptr) return SHAMPOO_EINVAL;
+  a->after = norm_side(j->after);
+  a->before = norm_side(j->before);
+  a->gate_kind = (int)j->gate_kind;
+  a->gate = j->gate;
+  a->gate_bf16 = j->gate_dtype == SHAMPOO_T_BF16;
+  a->gate_rows = (uint32_t)(j->gate_kind == SHAMPOO_GATE_ROWS ? j->gate_rows : j->rows);
+  a->stats1 = j->after_stats;
+  a->stats2 = j->before_stats;
+  return SHAMPOO_OK;
+}
+
+// How the rows go to workgroups: about kBackBlocks of them, each within one run
+// of rows that share a gate, or (short runs) with whole ones.
+constexpr int64_t kBackBlocks = 512;
+struct Split {
+  int64_t groups, pieces, blocks;
+  uint32_t per_group, per_block, piece_rows;
+};
+Split split_rows(int64_t rows, int64_t gate_rows) {
+  Split s;
+  const int64_t run = gate_rows > 0 ? gate_rows : rows;
+  const int64_t want = std::max<int64_t>((rows + kBackBlocks - 1) / kBackBlocks, 4);
+  s.groups = rows / run;
+  s.per_group = (uint32_t)((run + want - 1) / want);
+  s.piece_rows = (uint32_t)((run + s.per_group - 1) / s.per_group);
+  s.per_group = (uint32_t)((run + s.piece_rows - 1) / s.piece_rows);
+  s.pieces = s.groups * s.per_group;
+  s.per_block = (uint32_t)std::max<int64_t>(1, want / run);
+  s.blocks = (s.pieces + s.per_block - 1) / s.per_block;
+  return s;
+}
+
+int64_t pitch_of(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+}  // namespace
+
+extern "C" {
+
+int shampoo_join_forward(const shampoo_join* join, void* h, int64_t ld_h, void* u, int64_t ld_u, hipStream_t stream) {
+  JoinArgs a;
+  bool empty;
+  const int rc = common(join, &a, &empty);
+  if (rc != SHAMPOO_OK) return rc;
+  const bool has_y = join->branch != nullptr, has_u = join->before.kind != SHAMPOO_NORM_NONE;
+  const int64_t cols = join->cols;
+  if (join->ld_residual < cols || (has_y && (join->ld_branch < cols || ld_h < cols)) || (has_u && ld_u < cols))
+    return SHAMPOO_EINVAL;
+  if (empty) return SHAMPOO_OK;
+  if (a.r == nullptr || (has_y && h == nullptr) || (has_u && u == nullptr)) return SHAMPOO_EINVAL;
+  a.h = h;
+  a.ldh = ld_h;
+  a.u = u;
+  a.ldu = ld_u;
+  if (join->stream_dtype == SHAMPOO_T_BF16) return forward<true, true>(a, stream);
+  return join->branch_dtype == SHAMPOO_T_BF16 ? forward<false, true>(a, stream) : forward<false, false>(a, stream);
+}
+
+size_t shampoo_join_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {
+  if (check_sides(rows, cols) != SHAMPOO_OK || cols > SHAMPOO_NORM_COLS || rows == 0 || cols == 0) return 0;
+  if (gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return 0;
+  const Split s = split_rows(rows, gate_rows);
+  return (size_t)(2 * s.pieces + 2 * s.blocks) * (size_t)pitch_of(cols) * sizeof(float);
+}
+
+int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+  JoinArgs a;
+  bool empty;
+  int rc = common(join, &a, &empty);
+  if (rc != SHAMPOO_OK) return rc;
+  if (g == nullptr) return SHAMPOO_EINVAL;
+  const bool has_y = join->branch != nullptr, has1 = join->after.kind != SHAMPOO_NORM_NONE;
+  const bool has2 = join->before.kind != SHAMPOO_NORM_NONE && g->d_u != nullptr;
+  const bool gated = join->gate_kind != SHAMPOO_GATE_NONE;
+  const int64_t cols = join->cols;
+  if ((g->d_h != nullptr && g->ld_d_h < cols) || (g->d_u != nullptr && g->ld_d_u < cols) ||
+      (g->d_residual != nullptr && g->ld_d_residual < cols) || (g->d_branch != nullptr && g->ld_d_branch < cols))
+    return SHAMPOO_EINVAL;
+  if (!has_y && (g->d_h != nullptr || g->d_branch != nullptr)) return SHAMPOO_EINVAL;
+  if (g->d_u != nullptr && join->before.kind == SHAMPOO_NORM_NONE) return SHAMPOO_EINVAL;
+  if ((g->d_after_weight != nullptr && (!has1 || join->after.weight == nullptr)) ||
+      (g->d_after_bias != nullptr && (!has1 || join->after.bias == nullptr)) || (g->d_gate != nullptr && !gated) ||
+      (g->d_before_weight != nullptr && (!has2 || join->before.weight == nullptr)) ||
+      (g->d_before_bias != nullptr && (!has2 || join->before.bias == nullptr)))
+    return SHAMPOO_EINVAL;
+  if (empty) return SHAMPOO_OK;
+  if (g->d_h == nullptr && !has2) return SHAMPOO_EINVAL;
+  // what is read: inputs, or their copies
+  const bool need_r = has2, need_y = has_y && (has1 || gated || has2);
+  const bool keep = a.kr.codes != nullptr || a.ky.codes != nullptr;
+  if (keep) {
+    if ((need_r && a.kr.codes == nullptr) || (need_y && a.ky.codes == nullptr)) return SHAMPOO_EINVAL;
+  } else {
+    if (need_r && (a.r == nullptr || join->ld_residual < cols)) return SHAMPOO_EINVAL;
+    if (need_y && join->ld_branch < cols) return SHAMPOO_EINVAL;
+  }
+  if ((has1 && a.stats1 == nullptr) || (has2 && a.stats2 == nullptr)) return SHAMPOO_EINVAL;
+  const int64_t gate_rows = join->gate_kind == SHAMPOO_GATE_ROWS ? join->gate_rows : 0;
+  const size_t need = shampoo_join_workspace_bytes(join->rows, cols, gate_rows);
+  if (ws == nullptr || ws_bytes < need) return SHAMPOO_EWORKSPACE;
+  if (!aligned16(ws)) return SHAMPOO_EINVAL;
+  const Split s = split_rows(join->rows, gate_rows);
+  if (s.blocks > kMaxThreads / 512) return SHAMPOO_EUNSUPPORTED;
+  a.dh = g->d_h;
+  a.lddh = g->ld_d_h;
+  a.du = has2 ? g->d_u : nullptr;
+  a.lddu = g->ld_d_u;
+  a.dr = g->d_residual;
+  a.lddr = g->ld_d_residual;
+  a.dy = g->d_branch;
+  a.lddy = g->ld_d_branch;
+  a.has2 = has2;
+  a.pieces = s.pieces;
+  a.per_group = s.per_group;
+  a.per_block = s.per_block;
+  a.piece_rows = s.piece_rows;
+  a.pitch = (uint32_t)pitch_of(cols);
+  if (join->gate_kind == SHAMPOO_GATE_TOKEN) {
+    a.dtoken = g->d_gate;
+    a.dtoken_bf16 = a.gate_bf16;
+  }
+  const bool gate_sums = gate_rows > 0 && g->d_gate != nullptr;
+  float* const part = static_cast<float*>(ws);
+  const int64_t many = s.pieces * a.pitch;
+  if (g->d_after_weight != nullptr || gate_sums) a.pa = part;
+  if (g->d_after_bias != nullptr || (gate_sums && a.after.b != nullptr)) a.pb = part + many;
+  if (g->d_before_weight != nullptr) a.pw = part + 2 * many;
+  if (g->d_before_bias != nullptr) a.pc = part + 2 * many + s.blocks * a.pitch;
+  const bool bias = a.pb != nullptr || a.pc != nullptr;
+  const uint32_t blocks = (uint32_t)s.blocks;
+  if (join->stream_dtype == SHAMPOO_T_BF16) {
+    rc = join_backward_bf16(a, has_y, keep, bias, blocks, stream);
+  } else if (join->branch_dtype == SHAMPOO_T_BF16) {
+    rc = join_backward_mixed(a, has_y, keep, bias, blocks, stream);
+  } else {
+    rc = join_backward_f32(a, has_y, keep, bias, blocks, stream);
+  }
+  if (rc != SHAMPOO_OK) return rc;
+  SumArgs m = {};
+  auto job = [&](const float* from, int64_t count, bool gate, void* out, bool bf16) {
+    if (out == nullptr) return;
+    SumJob& J = m.job[m.jobs++];
+    J.part = from;
+    J.count = count;
+    J.gate = gate ? a.gate : nullptr;
+    J.gate_bf16 = a.gate_bf16;
+    J.out = out;
+    J.out_bf16 = bf16;
+  };
+  job(a.pw, s.blocks, false, g->d_before_weight, a.before.w_bf16);
+  job(a.pc, s.blocks, false, g->d_before_bias, a.before.b_bf16);
+  job(a.pa, s.pieces, gate_rows > 0, g->d_after_weight, a.after.w_bf16);
+  job(a.pb, s.pieces, gate_rows > 0, g->d_after_bias, a.after.b_bf16);
+  m.per_group = s.per_group;
+  m.cols = cols;
+  m.pitch = a.pitch;
+  int64_t rows_y = m.jobs;
+  if (gate_sums) {
+    m.pa = a.pa;
+    m.pb = a.after.b != nullptr ? a.pb : nullptr;
+    m.after = a.after;
+    m.dgate = g->d_gate;
+    m.dgate_bf16 = a.gate_bf16;
+    m.groups = s.groups;
+    // Rows with some pieces each are summed like the jobs, beside them; else an element a thread.
+    if (s.per_group > 4 && s.groups <= 1024) {
+      rows_y += s.groups;
+    } else {
+      const int64_t elems = s.groups * cols;
+      hipLaunchKernelGGL(join_gate_kernel, dim3((uint32_t)std::min<int64_t>((elems + 255) / 256, 8192)), dim3(256), 0,
+                         stream, m);
+      if ((rc = check_launch()) != SHAMPOO_OK) return rc;
+    }
+  }
+  if (rows_y == 0) return SHAMPOO_OK;
+  hipLaunchKernelGGL(join_sums_kernel, dim3((uint32_t)((cols + 63) / 64), (uint32_t)rows_y), dim3(64 * kSumLanes), 0,
+                     stream, m);
+  return check_launch();
+}
+
+}  // extern "C"

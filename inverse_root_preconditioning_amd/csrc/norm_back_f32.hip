@@ -1,0 +1,10 @@
+// Backward kernels of norms and joins with an fp32 stream and branch.
+#include "norm_launch.h"
+
+namespace shp {
+
+int join_backward_f32(const JoinArgs& a, bool join, bool keep, bool bias, uint32_t blocks, hipStream_t stream) {
+  return launch_join_backward<false, false>(a, join, keep, bias, blocks, stream);
+}
+
+}  // namespace shp

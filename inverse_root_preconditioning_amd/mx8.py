@@ -1,0 +1,153 @@
+"""8-bit microscaled (MX8) matrices: E4M3 values with one power-of-two scale for
+32 consecutive columns, the form in which activations wait for the backward
+pass (see layers, whose calls keep and read them by themselves).  All the
+arithmetic runs in the HIP library (see capi and include/shampoo.h).
+
+    q = quantize(x)                  # 1.03 bytes an element
+    x = dequantize(q, x.dtype)       # within 2^-4 of each element, or 2^-18 of the largest of its 32
+    with saved_tensors():            # what any torch operation keeps inside is kept so
+        y = block(x)
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import capi
+from .adamw import _TYPES, _current_device, _on_stream, _raw_stream
+from .mx4 import _matrix
+
+
+def _padded(cols):
+    return (cols + 31) & -32         # capi.GROUP
+
+
+def _bytes(rows, cols):
+    """Codes and scales of a matrix in one buffer, rounded up so that another may follow."""
+    n = rows * _padded(cols)
+    return (n + n // 32 + 15) & -16
+
+
+class MX8Matrix:
+    """A quantised matrix [rows, cols].  codes: uint8 [rows, padded], scales:
+    uint8 [rows, padded / 32]; padded: cols rounded up to a multiple of 32."""
+
+    __slots__ = ("_buf", "_codes", "_scales", "codes_ptr", "scales_ptr", "rows", "cols", "device")
+
+    def __init__(self, codes, scales, rows, cols):
+        k = _padded(cols)
+        for name, t, width in (("codes", codes, k), ("scales", scales, k // capi.GROUP)):
+            if not (t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor")
+            if tuple(t.shape) != (rows, width):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
+            if t.data_ptr() % 16:
+                raise ValueError(f"{name} must be 16-byte aligned")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on one device")
+        self._buf, self._codes, self._scales = None, codes, scales
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self.rows, self.cols, self.device = rows, cols, codes.device
+
+    @classmethod
+    def empty(cls, rows, cols, like):
+        """Uninitialised storage on the device of the tensor `like`: one buffer, scales after codes."""
+        return cls._over(like.new_empty((_bytes(rows, cols),), dtype=torch.uint8), rows, cols)
+
+    @classmethod
+    def _over(cls, buf, rows, cols):
+        """The matrix in a buffer of empty's layout."""
+        m = cls.__new__(cls)
+        m._buf = buf
+        m._codes = m._scales = None
+        m.codes_ptr = buf.data_ptr()
+        m.scales_ptr = m.codes_ptr + rows * _padded(cols)
+        m.rows, m.cols, m.device = rows, cols, buf.device
+        return m
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            k = _padded(self.cols)
+            self._codes = self._buf[:self.rows * k].view(self.rows, k)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            n, k = self.rows * _padded(self.cols), _padded(self.cols) // capi.GROUP
+            self._scales = self._buf[n:n + self.rows * k].view(self.rows, k)
+        return self._scales
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream."""
+        for t in (self._codes, self._scales) if self._buf is None else (self._buf,):
+            t.record_stream(stream)
+
+
+def quantize(x, stream=None):
+    """x [rows, cols] as MX8, 32 consecutive columns sharing a scale; nearest even."""
+    if stream is not None:
+        return _on_stream(stream, x.device, lambda: quantize(x), x)
+    dtype, ld = _matrix(x, "x")
+    index = x.device.index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return quantize(x)
+    rows, cols = x.shape
+    q = MX8Matrix.empty(rows, cols, x)
+    rc = capi.load().shampoo_mx8_quantize(x.data_ptr(), dtype, rows, cols, ld, q.codes_ptr, q.scales_ptr,
+                                          _raw_stream(index))
+    if rc:
+        capi.check(rc, "shampoo_mx8_quantize")
+    return q
+
+
+def dequantize(q, dtype=torch.float32, stream=None):
+    """The values of q."""
+    if stream is not None:
+        return _on_stream(stream, q.device, lambda: dequantize(q, dtype), q)
+    code = _TYPES.get(dtype)
+    if code is None:
+        raise ValueError("dtype must be float32 or bfloat16")
+    rows, cols, device = q.rows, q.cols, q.device
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return dequantize(q, dtype)
+    out = torch.empty((rows, cols), dtype=dtype, device=device)
+    rc = capi.load().shampoo_mx8_dequantize(q.codes_ptr, q.scales_ptr, rows, cols, out.data_ptr(), code, cols,
+                                            _raw_stream(device.index))
+    if rc:
+        capi.check(rc, "shampoo_mx8_dequantize")
+    return out
+
+
+def saved_tensors(min_elements=1 << 14):
+    """A context in which autograd keeps activations in MX8: every float32 or
+    bfloat16 CUDA tensor of at least `min_elements` that an operation inside
+    saves for its backward pass, but for leaves that require a gradient
+    (parameters) and views of them.  Backward then computes from the rounded values.
+    The operations of mx4 and layers save integers or are told by themselves
+    what to keep (keep=); their inputs are rounded like any others."""
+    def pack(t):
+        if t.dtype not in _TYPES or not t.is_cuda or t.numel() < max(min_elements, 1):
+            return t
+        base = t if t._base is None else t._base
+        if base.requires_grad and base.is_leaf or t.layout != torch.strided:
+            return t
+        t = t.detach()
+        # a row shorter than two groups would be mostly padding
+        flat = t.reshape(-1, t.shape[-1]) if t.dim() and t.shape[-1] >= 2 * capi.GROUP else t.reshape(1, -1)
+        return quantize(flat.contiguous()), t.dtype, t.shape
+
+    def unpack(kept):
+        if isinstance(kept, torch.Tensor):
+            return kept
+        q, dtype, shape = kept
+        return dequantize(q, dtype).view(shape)
+    return torch.autograd.graph.saved_tensors_hooks(pack, unpack)
