@@ -508,8 +508,8 @@ size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 /* An MX8 matrix of R rows and C columns is a pair of byte arrays,
  *   codes  [R][Cp]        sign + OCP E4M3 (bias 7), one value a byte
  *   scales [R][Cp / 32]   one byte s for 32 consecutive columns: 2^(s - 127)
- * with Cp = C rounded up to a multiple of 32; the columns from C to Cp hold
- * code 0.  Both arrays are 16-byte aligned.  (The format of AdamW's 8-bit first moments,
+ * with Cp = C rounded up to a multiple of 32; the columns from C to Cp are
+ * those of zeros.  Both arrays are 16-byte aligned.  (The format of AdamW's 8-bit first moments,
  * by rows and rounded to nearest even.)  At most 2^31 rows and 2^29 columns; beyond these, and where 2^24 workgroups
  * would be needed, calls here and of the activations are SHAMPOO_EUNSUPPORTED. */
 
@@ -517,13 +517,13 @@ size_t shampoo_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * shampoo_mx8_quantize -- MX8 copy of x, a device matrix [rows][cols] of dtype
  * with row stride ld >= cols.  s = max(E - 7, 1) with E the exponent field of
  * the group's largest magnitude as fp32; codes round to nearest even and none
- * saturates.  A group with an entry that is not finite gets codes 0 and s = 255
- * (NaN).
+ * saturates.  A group with an entry that is not finite gets s = 255, and codes
+ * that are E4M3's NaN (0x7f).
  */
 int shampoo_mx8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                          uint8_t* scales, hipStream_t stream);
 
-/* Values of an MX8 matrix, as fp32 (exact) or bf16 (exact from 2^-126 up,
+/* Values of an MX8 matrix (s = 255: NaN), as fp32 (exact) or bf16 (exact from 2^-126 up,
  * smaller ones rounded to nearest even), row stride ld >= cols. */
 int shampoo_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
                            int dtype, int64_t ld, hipStream_t stream);
@@ -653,12 +653,13 @@ typedef struct shampoo_join_grads {
  * input); the row statistics are read, never formed again.  Sums over rows
  * are of fixed order: the same call gives the same bits.  The residual's codes
  * are read only where there is d_u, the branch's only with a norm after
- * it, a gate or d_u.
- *   ws         shampoo_join_workspace_bytes(rows, cols, gate_rows of SHAMPOO_GATE_ROWS else 0) bytes
+ * it, a gate or d_u.  Copies are as shampoo_mx8_quantize writes them (NaN codes beside s = 255).
+ *   ws         shampoo_join_workspace_bytes(join) bytes
  */
 int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* grads, void* ws, size_t ws_bytes,
                           hipStream_t stream);
-size_t shampoo_join_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows);
+/* 0 for a join that is refused, and for one without rows or columns. */
+size_t shampoo_join_workspace_bytes(const shampoo_join* join);
 
 /* Workspace size in bytes for an operation (op = SHAMPOO_OP_*).  `count` is
  * nfactors for SCALE/NEWTON/CHEBY and nblocks for ACCUMULATE/PRECONDITION;

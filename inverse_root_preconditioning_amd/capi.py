@@ -179,7 +179,7 @@ _SIGNATURES = {
                                             c_int64, c_void_p, c_int64, c_void_p]),
     "shampoo_join_forward": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
     "shampoo_join_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "shampoo_join_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "shampoo_join_workspace_bytes": (c_size_t, [c_void_p]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -354,5 +354,5 @@ def shampoo_join_backward(join, grads, ws, ws_bytes, stream):
     return load().shampoo_join_backward(join, grads, ws, ws_bytes, stream)
 
 
-def shampoo_join_workspace_bytes(rows, cols, gate_rows):
-    return load().shampoo_join_workspace_bytes(rows, cols, gate_rows)
+def shampoo_join_workspace_bytes(join):
+    return load().shampoo_join_workspace_bytes(join)

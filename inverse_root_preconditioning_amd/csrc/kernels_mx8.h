@@ -51,12 +51,12 @@ struct Mx8Piece {
         w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, elem(x, 4 * i), elem(x, 4 * i + 1), scale, false);
         w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, elem(x, 4 * i + 2), elem(x, 4 * i + 3), scale, true);
       }
-      c[i] = s == 255 ? 0u : __builtin_bit_cast(uint32_t, w);
+      c[i] = s == 255 ? 0x7f7f7f7fu : __builtin_bit_cast(uint32_t, w);  // NaN, four times
     });
   }
   __device__ __forceinline__ void store(const Mx8Rows& m, int64_t row, uint32_t col) const {
     if (col < m.padded) {
-      stg(reinterpret_cast<Words*>(m.codes + row * (int64_t)m.padded + col), c);
+      stg_once<Words, 4>(m.codes + row * (int64_t)m.padded + col, c);
       if (col % kMx8Group == 0) stg(m.scales + row * (int64_t)(m.padded / kMx8Group) + col / kMx8Group, (uint8_t)s);
     }
   }
@@ -64,20 +64,31 @@ struct Mx8Piece {
     c = (Words)0u;
     s = 1;
     if (col < m.padded) {
-      c = ldg(reinterpret_cast<const Words*>(m.codes + row * (int64_t)m.padded + col));
+      c = ldg_once<Words, 4>(m.codes + row * (int64_t)m.padded + col);
       s = ldg(m.scales + row * (int64_t)(m.padded / kMx8Group) + col / kMx8Group);
     }
   }
+  // The same without a branch: beyond the row's end codes that are there, to be cleared when they have come.
+  __device__ __forceinline__ void load_near(const Mx8Rows& m, int64_t row, uint32_t col) {
+    const uint32_t from = min(col, m.padded - V);
+    c = ldg_once<Words, 4>(m.codes + row * (int64_t)m.padded + from);
+    s = ldg(m.scales + row * (int64_t)(m.padded / kMx8Group) + from / kMx8Group);
+  }
+  __device__ __forceinline__ void clear() {
+    c = (Words)0u;
+    s = 1;
+  }
+  // The values; where s = 255 those of the codes quantisation writes beside it, NaN.
   __device__ __forceinline__ void decode(float (&x)[V]) const {
-    const float scale = s == 255 ? __builtin_nanf("") : __builtin_bit_cast(float, s << 23);
+    const float scale = __builtin_bit_cast(float, s << 23);
     static_for<V / 4>([&](auto I) __attribute__((always_inline)) {
       constexpr int i = decltype(I)::value;
-      const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((uint32_t)c[i], false);
-      const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((uint32_t)c[i], true);
-      x[4 * i] = lo[0] * scale;
-      x[4 * i + 1] = lo[1] * scale;
-      x[4 * i + 2] = hi[0] * scale;
-      x[4 * i + 3] = hi[1] * scale;
+      const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)c[i], scale, false);
+      const f32x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)c[i], scale, true);
+      x[4 * i] = lo[0];
+      x[4 * i + 1] = lo[1];
+      x[4 * i + 2] = hi[0];
+      x[4 * i + 3] = hi[1];
     });
   }
 };
@@ -139,6 +150,10 @@ __global__ void __launch_bounds__(256) mx8_dequantize_kernel(const Mx8Args P) {
     if (r >= P.rows) return;
     float x[V];
     q[i].decode(x);
+    if (q[i].s == 255) {  // whatever the codes are
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = __builtin_nanf("");
+    }
     store_row<BF16, V>(row_at<BF16>(P.out, r, P.ld), P.cols, col, x);
   }
 }

@@ -6,7 +6,8 @@
 //
 // W waves hold a row of up to 64 W P V columns in registers, each lane P pieces
 // of V consecutive elements, so that a row is read once however many sums over
-// it the formulas need.
+// it the formulas need; the parameters' columns stay in registers over all the rows
+// that a workgroup takes.
 #pragma once
 
 #include "kernels_mx8.h"
@@ -22,14 +23,14 @@ struct NormSide {
 
 struct JoinArgs {
   int64_t rows;
-  uint32_t cols;
+  uint32_t cols, flags;
   float scale;
   const void *r, *y;  // the inputs; y unused without a join
   int64_t ldr, ldy;
   Mx8Rows kr, ky;     // their MX8 copies: written forward where codes is given, read backward with KEEP
   NormSide after, before;
   const void* gate;
-  int gate_kind, gate_bf16;
+  int gate_bf16;
   uint32_t gate_rows;        // rows that share a row of the gate
   float *stats1, *stats2;    // [rows][2]: mean and s of N1 and of N2
   // forward
@@ -40,27 +41,43 @@ struct JoinArgs {
   int64_t lddh, lddu;
   void *dr, *dy, *dtoken;
   int64_t lddr, lddy;
-  int dtoken_bf16;
-  int has2;                  // du is there
   // Pieces of consecutive rows, `per_group` of them for each run of gate_rows
   // rows; a workgroup takes `per_block` pieces.
-  int64_t pieces;
-  uint32_t per_group, per_block, piece_rows;
+  uint32_t pieces, per_group, per_block, piece_rows;
   float *pa, *pb, *pw, *pc;  // partial sums: [pieces] of dt yn, dt; [workgroups] of du hn, du (NULL: not wanted)
   uint32_t pitch;            // floats between their rows
+};
+
+// The same value, which the compiler cannot take for the one of the row before.
+// Else every comparison with the row's end and every flag that a row's work tests
+// is kept in scalar registers over the loop, which then do not suffice: a hundred moves
+// a row from where they are put instead, a third of the instructions.
+__device__ __forceinline__ uint32_t anew(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t anew_uniform(uint32_t v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// What there is to do, in one word.
+enum : uint32_t {
+  kJoinNorm1 = 1,     // N1
+  kJoinMean1 = 2,     // with a mean
+  kJoinNorm2 = 4,     // N2 (backward: and its gradient)
+  kJoinMean2 = 8,
+  kJoinRuns = 16,     // a gate row for runs of rows
+  kJoinToken = 32,    // a gate for each row
+  kJoinDh = 64,       // a gradient of h
+  kJoinNeedY = 128,   // the branch is read backward
+  kJoinCodesR = 256,  // MX8 copies are written
+  kJoinCodesY = 512
 };
 
 // ---------------------------------------------------------------------------
 // Sums over a row
 // ---------------------------------------------------------------------------
-
-// The same number, which the compiler cannot take for the one of the last row:
-// else it keeps every comparison with the row's end, 8 a piece, in registers
-// over the loop (186 vector registers for 60, and scratch beyond 8 elements a lane).
-__device__ __forceinline__ uint32_t anew(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 // Sum over a wave in every lane, in a fixed order.
 __device__ __forceinline__ float wave_total(float v) {
@@ -81,7 +98,7 @@ __device__ __forceinline__ float wave_total(float v) {
 // reads of this one.
 template <int W>
 struct RowSums {
-  float* lds;  // [2][2][W]
+  float* lds;  // [2][2][W] of this row
   int turn = 0;
   template <int N>
   __device__ __forceinline__ void total(float (&v)[N]) {
@@ -89,7 +106,7 @@ struct RowSums {
     for (int n = 0; n < N; ++n) v[n] = wave_total(v[n]);
     if constexpr (W > 1) {
       float* const at = lds + turn * 2 * W;
-      const int wave = threadIdx.x / kWave;
+      const int wave = threadIdx.x / kWave % W;
       if (threadIdx.x % kWave == 0) {
 #pragma unroll
         for (int n = 0; n < N; ++n) at[n * W + wave] = v[n];
@@ -112,50 +129,140 @@ struct RowSums {
 };
 
 // ---------------------------------------------------------------------------
-// Parameters
+// Pieces of a row
 // ---------------------------------------------------------------------------
 
-// V columns of a vector of parameters, 0 beyond its end; without the vector, `none`.
-template <int V>
-__device__ __forceinline__ void load_param(const void* p, int bf16, uint32_t cols, uint32_t col, float none,
+// The places of a lane's P pieces.  Loads are of V elements that are there (at
+// the row's end those before it), so that no branch stands between them; `fix`
+// puts right what a piece beyond the end, or over it, has read, when it has come.
+// WHOLE: the columns are a multiple of V.
+template <int W, int P, int V, bool WHOLE>
+struct Places {
+  uint32_t cols, lane;
+  __device__ __forceinline__ Places(uint32_t columns, uint32_t thread) : cols(columns), lane(thread % (kWave * W)) {}
+  __device__ __forceinline__ uint32_t col(int p) const { return (p * W * kWave + lane) * V; }
+
+  template <bool BF16>
+  __device__ __forceinline__ Piece<BF16, V> load(const void* row, int p) const {
+    if constexpr (WHOLE) {
+      Piece<BF16, V> x;
+      x.load_once(row, min(col(p), cols - V));
+      return x;
+    } else if (cols >= V) {
+      Piece<BF16, V> x;
+      x.load_once(row, min(col(p), cols - V));
+      return x;
+    } else {
+      return load_row<BF16, V>(row, cols, col(p));
+    }
+  }
+  template <bool BF16>
+  __device__ __forceinline__ void fix(Piece<BF16, V>& x, int p) const {
+    if constexpr (WHOLE) {
+      if (col(p) >= cols) x.w = 0u;
+    } else if (cols >= V) {
+      const uint32_t over = col(p) + V;  // (cols - V itself is above 2^31 for no columns)
+      if (over > cols) x.shift_down(min(over - cols, (uint32_t)V));
+    }
+  }
+  template <bool BF16>
+  __device__ __forceinline__ void store(void* row, int p, const float (&x)[V]) const {
+    if constexpr (WHOLE) {
+      if (col(p) < cols) store_row<BF16, V, true>(row, cols, col(p), x);
+    } else {
+      store_row<BF16, V>(row, cols, col(p), x);
+    }
+  }
+  // Whether element e of piece p is a column.
+  __device__ __forceinline__ bool valid(int p, int e) const { return col(p) + (WHOLE ? 0 : e) < cols; }
+};
+
+// Piece p of a vector of parameters, 0 beyond its end; without the vector, `none`.
+template <int W, int P, int V, bool WHOLE>
+__device__ __forceinline__ void load_param(const Places<W, P, V, WHOLE>& at, int p, const void* v, int bf16, float none,
                                            float (&x)[V]) {
-  if (p == nullptr) {
+  const uint32_t col = at.col(p);
+  if (v == nullptr) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = col + e < cols ? none : 0.f;
+    for (int e = 0; e < V; ++e) x[e] = at.valid(p, e) ? none : 0.f;
   } else if (bf16) {
-    const Piece<true, V> q = load_row<true, V>(p, cols, col);
+    const Piece<true, V> q = load_row<true, V>(v, at.cols, col);
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = elem(q, e);
   } else {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const Piece<false, 4> q = load_row<false, 4>(p, cols, col + 4 * i);
+    for (int k = 0; k < V / 4; ++k) {
+      const Piece<false, 4> q = load_row<false, 4>(v, at.cols, col + 4 * k);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * i + e] = elem(q, e);
+      for (int e = 0; e < 4; ++e) x[4 * k + e] = elem(q, e);
     }
   }
 }
 
-// The gate's row for a row of the stream: NULL where it is one value (or none).
-__device__ __forceinline__ const void* gate_row(const JoinArgs& A, uint32_t row) {
-  if (A.gate_kind != SHAMPOO_GATE_ROWS) return nullptr;
-  const int64_t at = (int64_t)(row / A.gate_rows) * A.cols;
-  return static_cast<const uint8_t*>(A.gate) + at * (A.gate_bf16 ? 2 : 4);
-}
-__device__ __forceinline__ float gate_value(const JoinArgs& A, uint32_t row) {
-  if (A.gate_kind != SHAMPOO_GATE_TOKEN) return 1.f;
+// Parameters of a lane's pieces: kept in registers, or where those do not
+// suffice, read again for every use.
+template <int W, int P, int V, bool WHOLE, bool BIAS, bool KEPT>
+struct Parameters {
+  static constexpr bool kKept = KEPT;
+  typedef Places<W, P, V, WHOLE> At;
+  float w[kKept ? P : 1][V], b[kKept ? P : 1][V];
+  uint32_t run;
+
+  // w and b of a norm; of N1 times the gate's row of a run, where the gate is
+  // one for runs of rows, so that gate N1 = w yn + b.
+  __device__ __forceinline__ void load(const At& at, const JoinArgs& A, const NormSide& n, bool gated, int p, float (&w)[V],
+                                       float (&b)[V]) const {
+    load_param(at, p, n.w, n.w_bf16, 1.f, w);
+    if constexpr (BIAS) load_param(at, p, n.b, n.b_bf16, 0.f, b);
+    if (gated) {
+      const void* const row = static_cast<const uint8_t*>(A.gate) + (int64_t)run * A.cols * (A.gate_bf16 ? 2 : 4);
+      float g[V];
+      load_param(at, p, row, A.gate_bf16, 1.f, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        w[e] *= g[e];
+        if constexpr (BIAS) b[e] *= g[e];
+      }
+    }
+  }
+  __device__ __forceinline__ void keep(const At& at, const JoinArgs& A, const NormSide& n, bool gated, uint32_t new_run) {
+    run = new_run;
+    if constexpr (kKept) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) load(at, A, n, gated, p, w[p], b[p]);
+    }
+  }
+  __device__ __forceinline__ void get(const At& at, const JoinArgs& A, const NormSide& n, bool gated, int p, float (&wp)[V],
+                                      float (&bp)[V]) const {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        wp[e] = w[p][e];
+        bp[e] = BIAS ? b[p][e] : 0.f;
+      }
+    } else {
+      __builtin_amdgcn_sched_barrier(0);  // one piece's parameters at a time
+      load(At(at.cols, anew(at.lane)), A, n, gated, p, wp, bp);
+      if constexpr (!BIAS) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) bp[e] = 0.f;
+      }
+    }
+  }
+};
+__device__ __forceinline__ float load_token(const JoinArgs& A, int64_t row) {
   if (A.gate_bf16) return __builtin_bit_cast(float, (uint32_t)ldg(static_cast<const uint16_t*>(A.gate) + row) << 16);
   return ldg(static_cast<const float*>(A.gate) + row);
 }
 
 // Mean and s of a row held in pieces, zero beyond its end.
-template <int W, int P, int V>
-__device__ __forceinline__ void row_stats(const float (&x)[P][V], const NormSide& n, uint32_t cols, uint32_t lane,
-                                          RowSums<W>& sums, float& mean, float& s) {
-  const float over = 1.f / (float)cols;
+template <int W, int P, int V, bool WHOLE>
+__device__ __forceinline__ void row_stats(const Places<W, P, V, WHOLE>& at, const float (&x)[P][V], bool centred,
+                                          float eps, RowSums<W>& sums, float& mean, float& s) {
+  const float over = 1.f / (float)at.cols;
   mean = 0.f;
   float ss = 0.f;
-  if (n.kind == SHAMPOO_NORM_LAYER) {
+  if (centred) {
     float t = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -164,10 +271,9 @@ __device__ __forceinline__ void row_stats(const float (&x)[P][V], const NormSide
     mean = sums.total1(t) * over;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t col = (p * W * kWave + lane) * V;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = col + e < cols ? x[p][e] - mean : 0.f;
+        const float d = at.valid(p, e) ? x[p][e] - mean : 0.f;
         ss = __builtin_fmaf(d, d, ss);
       }
     }
@@ -177,110 +283,132 @@ __device__ __forceinline__ void row_stats(const float (&x)[P][V], const NormSide
 #pragma unroll
       for (int e = 0; e < V; ++e) ss = __builtin_fmaf(x[p][e], x[p][e], ss);
   }
-  s = 1.f / sqrtf(sums.total1(ss) * over + n.eps);
+  s = 1.f / sqrtf(sums.total1(ss) * over + eps);
 }
 
-// Rows that a workgroup holds at once: 4 of a wave each, or one.
+// Rows that a workgroup of the forward kernel holds at once: 4 of a wave each, or one.
 template <int W>
 constexpr int kRowLanes = W == 1 ? 4 : 1;
 template <int W>
-constexpr int kRowThreads = W == 1 ? 256 : 64 * W;
+constexpr int kRowThreads = kWave * W * kRowLanes<W>;
+
+// Of the backward kernel: 16 waves' worth, so that there are few partial sums,
+// or 4 where a lane needs more registers than 16 waves leave it.
+template <int W, bool MANY>
+constexpr int kBackLanes = W <= (MANY ? 4 : 16) ? (MANY ? 4 : 16) / W : 1;
+template <int W, bool MANY>
+constexpr int kBackThreads = kWave * W * kBackLanes<W, MANY>;
 
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
 
-template <bool SB, bool BB, int W, int P, bool JOIN>
+template <bool SB, bool BB, int W, int P, bool JOIN, bool WHOLE>
 __global__ void __launch_bounds__(kRowThreads<W>) join_forward_kernel(const JoinArgs A) {
   constexpr int V = SB ? 8 : 4, L = kRowLanes<W>;
+  typedef Places<W, P, V, WHOLE> At;
   __shared__ float red[4 * W];
   RowSums<W> sums{red};
-  const uint32_t lane0 = threadIdx.x % (kWave * W);
-  const int64_t first = (int64_t)blockIdx.x * L + __builtin_amdgcn_readfirstlane(threadIdx.x / (kWave * W));
-  for (int64_t row = first; row < A.rows; row += (int64_t)gridDim.x * L) {
-    const uint32_t lane = anew(lane0);
-    Piece<SB, V> r[P];
-    Piece<BB, V> y[P];
-    float x[P][V];
+  const int64_t step = (int64_t)gridDim.x * L;
+  int64_t row = (int64_t)blockIdx.x * L + __builtin_amdgcn_readfirstlane(threadIdx.x / (kWave * W));
+  if (row >= A.rows) return;  // a wave by itself (W = 1), or the whole workgroup
+  Piece<SB, V> r[P];
+  Piece<BB, V> y[P];
+  auto load = [&](const At& at, int64_t from) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-      r[p] = load_row<SB, V>(row_at<SB>(A.r, row, A.ldr), A.cols, (p * W * kWave + lane) * V);
-    if constexpr (JOIN) {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        y[p] = load_row<BB, V>(row_at<BB>(A.y, row, A.ldy), A.cols, (p * W * kWave + lane) * V);
+    for (int p = 0; p < P; ++p) {
+      r[p] = at.template load<SB>(row_at<SB>(A.r, from, A.ldr), p);
+      if constexpr (JOIN) y[p] = at.template load<BB>(row_at<BB>(A.y, from, A.ldy), p);
     }
-    if (A.kr.codes != nullptr) {
+  };
+  Parameters<W, P, V, WHOLE, true, (P * V <= 8)> n1, n2;
+  {
+    const At at(A.cols, threadIdx.x);
+    load(at, row);
+    if constexpr (JOIN)
+      n1.keep(at, A, A.after, A.flags & kJoinRuns, __builtin_amdgcn_readfirstlane((uint32_t)row / A.gate_rows));
+    n2.keep(at, A, A.before, false, 0);
+  }
+  while (true) {
+    const At at(A.cols, anew(threadIdx.x));
+    const uint32_t flags = anew_uniform(A.flags);
+    float x[P][V], rf[P][V];
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
+    for (int p = 0; p < P; ++p) {
+      at.fix(r[p], p);
+#pragma unroll
+      for (int e = 0; e < V; ++e) rf[p][e] = elem(r[p], e);
+      if (flags & kJoinCodesR) {
         Mx8Piece<V> q;
         q.encode(r[p]);
-        q.store(A.kr, row, (p * W * kWave + lane) * V);
+        q.store(A.kr, row, at.col(p));
       }
-    }
-    if constexpr (JOIN) {
-      if (A.ky.codes != nullptr) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          Mx8Piece<V> q;
-          q.encode(y[p]);
-          q.store(A.ky, row, (p * W * kWave + lane) * V);
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p)
+      if constexpr (JOIN) {
+        at.fix(y[p], p);
 #pragma unroll
         for (int e = 0; e < V; ++e) x[p][e] = elem(y[p], e);
-      float mean = 0.f, s = 1.f;
-      if (A.after.kind != SHAMPOO_NORM_NONE) {
-        row_stats<W, P, V>(x, A.after, A.cols, lane, sums, mean, s);
-        if (A.stats1 != nullptr && lane == 0) {
-          stg(A.stats1 + 2 * row, mean);
-          stg(A.stats1 + 2 * row + 1, s);
+        if (flags & kJoinCodesY) {
+          Mx8Piece<V> q;
+          q.encode(y[p]);
+          q.store(A.ky, row, at.col(p));
         }
       }
-      const void* const grow = gate_row(A, (uint32_t)row);
-      const float token = gate_value(A, (uint32_t)row);
+    }
+    const int64_t next = row + step;
+    if (next < A.rows) load(at, next);  // in flight while this row is worked on
+    if constexpr (JOIN) {
+      float mean = 0.f, s = 1.f;
+      if (flags & kJoinNorm1) {
+        row_stats(at, x, (flags & kJoinMean1) != 0, A.after.eps, sums, mean, s);
+        if (A.stats1 != nullptr && at.lane == 0) stg(reinterpret_cast<f32x2_t*>(A.stats1) + row, f32x2_t{mean, s});
+      }
+      if (flags & kJoinRuns) {
+        const uint32_t now = __builtin_amdgcn_readfirstlane((uint32_t)row / A.gate_rows);
+        if (now != n1.run) n1.keep(at, A, A.after, true, now);
+      }
+      // (x - mean) s as one operation: the product mean s is rounded by no more than the mean itself
+      const float c = -mean * s;
+      const float token = flags & kJoinToken ? load_token(A, row) : 1.f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const uint32_t col = (p * W * kWave + lane) * V;
-        float g[V], w[V], b[V];
-        load_param(grow, A.gate_bf16, A.cols, col, token, g);
-        load_param(A.after.w, A.after.w_bf16, A.cols, col, 1.f, w);
-        load_param(A.after.b, A.after.b_bf16, A.cols, col, 0.f, b);
+        float w[V], b[V];
+        n1.get(at, A, A.after, flags & kJoinRuns, p, w, b);
+        if (flags & kJoinToken) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float z = __builtin_fmaf((x[p][e] - mean) * s, w[e], b[e]);
-          x[p][e] = __builtin_fmaf(g[e], z, A.scale * elem(r[p], e));
+          for (int e = 0; e < V; ++e) {
+            const float z = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], b[e]);
+            x[p][e] = __builtin_fmaf(token, z, A.scale * rf[p][e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            x[p][e] = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], __builtin_fmaf(A.scale, rf[p][e], b[e]));
         }
-        store_row<SB, V>(row_at<SB>(A.h, row, A.ldh), A.cols, col, x[p]);
-        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int p = 0; p < P; ++p) at.template store<SB>(row_at<SB>(A.h, row, A.ldh), p, x[p]);
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[p][e] = elem(r[p], e);
+        for (int e = 0; e < V; ++e) x[p][e] = rf[p][e];
     }
-    if (A.before.kind != SHAMPOO_NORM_NONE) {
+    if (flags & kJoinNorm2) {
       float mean, s;
-      row_stats<W, P, V>(x, A.before, A.cols, lane, sums, mean, s);
-      if (A.stats2 != nullptr && lane == 0) {
-        stg(A.stats2 + 2 * row, mean);
-        stg(A.stats2 + 2 * row + 1, s);
-      }
+      row_stats(at, x, (flags & kJoinMean2) != 0, A.before.eps, sums, mean, s);
+      if (A.stats2 != nullptr && at.lane == 0) stg(reinterpret_cast<f32x2_t*>(A.stats2) + row, f32x2_t{mean, s});
+      const float c = -mean * s;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const uint32_t col = (p * W * kWave + lane) * V;
-        float w[V], b[V], u[V];
-        load_param(A.before.w, A.before.w_bf16, A.cols, col, 1.f, w);
-        load_param(A.before.b, A.before.b_bf16, A.cols, col, 0.f, b);
+        float u[V], w[V], b[V];
+        n2.get(at, A, A.before, false, p, w, b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = __builtin_fmaf((x[p][e] - mean) * s, w[e], b[e]);
-        store_row<BB, V>(row_at<BB>(A.u, row, A.ldu), A.cols, col, u);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int e = 0; e < V; ++e) u[e] = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], b[e]);
+        at.template store<BB>(row_at<BB>(A.u, row, A.ldu), p, u);
       }
     }
+    if (next >= A.rows) return;
+    row = next;
   }
 }
 
@@ -294,13 +422,15 @@ __global__ void __launch_bounds__(kRowThreads<W>) join_forward_kernel(const Join
 // workgroup, then go to memory for join_sums_kernel: no atomics, a fixed order.
 // ---------------------------------------------------------------------------
 
-// A lane's sums, added over the rows held side by side, to row `at` of partial sums.
-template <int W, int P, int V>
-__device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, uint32_t pitch, uint32_t lane, float* lds) {
-  if constexpr (W > 1) {
+// A lane's sums, added over the rows held side by side, to a row of partial sums.
+template <int W, int P, int V, int L>
+__device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, uint32_t pitch, uint32_t lane, int part,
+                                           float* lds) {
+  constexpr uint32_t kCols = kWave * W * V;  // of a piece
+  if constexpr (L == 1) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t col = (p * W * kWave + lane) * V;
+      const uint32_t col = p * kCols + lane * V;
       if (col < pitch) {
 #pragma unroll
         for (int q = 0; q < V / 4; ++q)
@@ -309,19 +439,25 @@ __device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, 
       }
     }
   } else {
-    constexpr int kCols = kWave * V;
-    const int wave = threadIdx.x / kWave;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
+      __syncthreads();  // the last piece, or the rows' sums, have been read
 #pragma unroll
-      for (int e = 0; e < V; ++e) lds[wave * kCols + lane * V + e] = acc[p][e];
+      for (int q = 0; q < V / 4; ++q)
+        reinterpret_cast<floatx4*>(lds + part * kCols + lane * V)[q] =
+            floatx4{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
       __syncthreads();
-      for (int c = threadIdx.x; c < kCols; c += 256) {
+      for (uint32_t c = threadIdx.x; c < kCols; c += kWave * W * L) {
         const uint32_t col = p * kCols + c;
-        if (col < pitch) stg(to + col, (lds[c] + lds[kCols + c]) + (lds[2 * kCols + c] + lds[3 * kCols + c]));
+        if (col < pitch) {
+          float v = lds[c];
+#pragma unroll
+          for (int i = 1; i < L; ++i) v += lds[i * kCols + c];
+          stg(to + col, v);
+        }
       }
-      __syncthreads();
     }
+    __syncthreads();  // before the rows' sums write here again
   }
 }
 
@@ -330,213 +466,272 @@ template <bool KEEP, bool BF16, int V>
 struct Kept {
   Piece<BF16, V> x;
   Mx8Piece<V> q;
-  __device__ __forceinline__ void load(const void* from, int64_t ld, const Mx8Rows& m, int64_t row, uint32_t cols,
-                                       uint32_t col) {
+  template <class At>
+  __device__ __forceinline__ void load(const At& at, const void* from, int64_t ld, const Mx8Rows& m, int64_t row, int p) {
     if constexpr (KEEP) {
-      q.load(m, row, col);
+      q.load_near(m, row, at.col(p));
     } else {
-      x = load_row<BF16, V>(row_at<BF16>(from, row, ld), cols, col);
+      x = at.template load<BF16>(row_at<BF16>(from, row, ld), p);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[V]) const {
+  __device__ __forceinline__ void clear() {
     if constexpr (KEEP) {
+      q.clear();
+    } else {
+      x.w = 0u;
+    }
+  }
+  template <class At>
+  __device__ __forceinline__ void get(const At& at, const Mx8Rows& m, int p, float (&v)[V]) {
+    if constexpr (KEEP) {
+      if (at.col(p) >= m.padded) q.clear();
       q.decode(v);
     } else {
+      at.fix(x, p);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = elem(x, e);
     }
   }
 };
 
-template <bool SB, bool BB, int W, int P, bool JOIN, bool KEEP, bool BIAS>
-__global__ void __launch_bounds__(kRowThreads<W>) join_backward_kernel(const JoinArgs A) {
-  constexpr int V = SB ? 8 : 4, L = kRowLanes<W>;
-  __shared__ __attribute__((aligned(16))) float lds[W == 1 ? 4 * kWave * V : 4 * W];
-  RowSums<W> sums{lds};
-  const uint32_t lane0 = threadIdx.x % (kWave * W);
+template <bool SB, bool BB, int W, int P, bool JOIN, bool KEEP, bool BIAS, bool WHOLE>
+__global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backward_kernel(const JoinArgs A) {
+  constexpr int V = SB ? 8 : 4, L = kBackLanes<W, JOIN && BIAS>;
+  typedef Places<W, P, V, WHOLE> At;
+  __shared__ __attribute__((aligned(16))) float lds[L == 1 ? 4 * W : L * kWave * W * V];
   const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / (kWave * W));
+  // Parameters in registers and the next row's loads in flight, where there are registers for
+  // them: 128 in a workgroup of 16 waves.  (4096 rows of 16384 without this rule: 690 us, in scratch memory.)
+  constexpr bool kAhead = P * V <= 8 && !(JOIN && BIAS && W == 16);
+  RowSums<W> sums{lds + part * 4 * W};
   const float over = 1.f / (float)A.cols;
-  const bool has1 = JOIN && A.after.kind != SHAMPOO_NORM_NONE, has2 = A.has2 != 0;
-  const bool need_y = JOIN && (has1 || A.gate_kind != SHAMPOO_GATE_NONE || has2);
+
+  // One row's inputs, as they come from memory.
+  Piece<SB, V> dh[P];
+  Piece<BB, V> du[P];
+  Kept<KEEP, SB, V> r[P];
+  Kept<KEEP, BB, V> y[P];
+  f32x2_t st1 = {0.f, 1.f}, st2 = {0.f, 1.f};
+  auto load = [&](const At& at, uint32_t flags, int64_t row) __attribute__((always_inline)) {
+    if (flags & kJoinNorm2) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        du[p] = at.template load<BB>(row_at<BB>(A.du, row, A.lddu), p);
+        r[p].load(at, A.r, A.ldr, A.kr, row, p);
+      }
+      st2 = ldg(reinterpret_cast<const f32x2_t*>(A.stats2) + row);
+    }
+    if constexpr (JOIN) {
+      if (flags & kJoinNeedY) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) y[p].load(at, A.y, A.ldy, A.ky, row, p);
+      }
+      if (flags & kJoinDh) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) dh[p] = at.template load<SB>(row_at<SB>(A.dh, row, A.lddh), p);
+      }
+      if (flags & kJoinNorm1) st1 = ldg(reinterpret_cast<const f32x2_t*>(A.stats1) + row);
+    }
+  };
+
+  const uint32_t begin = blockIdx.x * A.per_block;
+  const uint32_t end = min(begin + A.per_block, A.pieces);
+  Parameters<W, P, V, WHOLE, BIAS, kAhead> n1;
+  Parameters<W, P, V, WHOLE, false, kAhead> n2;
+  n2.keep(At(A.cols, threadIdx.x), A, A.before, false, 0);
   float aw[P][V] = {}, ac[P][V] = {}, aa[P][V], ab[P][V];
-  const int64_t begin = (int64_t)blockIdx.x * A.per_block;
-  const int64_t end = begin + A.per_block < A.pieces ? begin + A.per_block : A.pieces;
-  for (int64_t piece = begin; piece < end; ++piece) {
-    const int64_t group = piece / A.per_group;
-    const int64_t group0 = group * A.gate_rows, group1 = group0 + A.gate_rows;
-    const int64_t row0 = group0 + (piece - group * A.per_group) * A.piece_rows;
+  for (uint32_t piece = begin; piece < end; ++piece) {
+    const uint32_t group = __builtin_amdgcn_readfirstlane(piece / A.per_group);
+    const int64_t group0 = (int64_t)group * A.gate_rows, group1 = group0 + A.gate_rows;
+    const int64_t row0 = group0 + (int64_t)(piece - group * A.per_group) * A.piece_rows;
     const int64_t row1 = row0 + A.piece_rows < group1 ? row0 + A.piece_rows : group1;
+    {
+      const At at(A.cols, anew(threadIdx.x));
+      if (kAhead) load(at, A.flags, min(row0 + part, row1 - 1));
+      if constexpr (JOIN) n1.keep(at, A, A.after, A.flags & kJoinRuns, group);
+    }
     if constexpr (JOIN) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int e = 0; e < V; ++e) aa[p][e] = ab[p][e] = 0.f;
     }
-    for (int64_t row = row0 + part; row < row1; row += L) {
-      const uint32_t lane = anew(lane0);
-      Piece<SB, V> dh[P];
-      Piece<BB, V> du[P];
-      Kept<KEEP, SB, V> r[P];
-      Kept<KEEP, BB, V> y[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t col = (p * W * kWave + lane) * V;
-        if (has2) {
-          du[p] = load_row<BB, V>(row_at<BB>(A.du, row, A.lddu), A.cols, col);
-          r[p].load(A.r, A.ldr, A.kr, row, A.cols, col);
-        }
-        if constexpr (JOIN) {
-          if (need_y) y[p].load(A.y, A.ldy, A.ky, row, A.cols, col);
-          dh[p].w = 0u;
-          if (A.dh != nullptr) dh[p] = load_row<SB, V>(row_at<SB>(A.dh, row, A.lddh), A.cols, col);
-        }
-      }
-      float mean1 = 0.f, s1 = 1.f, mean2 = 0.f, s2 = 1.f, token = 1.f;
-      if (has1) {
-        mean1 = ldg(A.stats1 + 2 * row);
-        s1 = ldg(A.stats1 + 2 * row + 1);
-      }
-      if (has2) {
-        mean2 = ldg(A.stats2 + 2 * row);
-        s2 = ldg(A.stats2 + 2 * row + 1);
-      }
-      const void* grow = nullptr;
-      if constexpr (JOIN) {
-        grow = gate_row(A, (uint32_t)row);
-        token = gate_value(A, (uint32_t)row);
-      }
-      float yn[P][V], hn[P][V], dt[P][V];
-      float t[2] = {0.f, 0.f};
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t col = (p * W * kWave + anew(lane)) * V;
-        if constexpr (JOIN) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            yn[p][e] = 0.f;
-            dt[p][e] = elem(dh[p], e);
-          }
-          if (need_y) {
-            y[p].get(yn[p]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) yn[p][e] = (yn[p][e] - mean1) * s1;
-          }
-        }
-        if (has2) {
-          r[p].get(hn[p]);
-          if constexpr (JOIN) {
-            float g[V], w[V], b[V];
-            load_param(grow, A.gate_bf16, A.cols, col, token, g);
-            load_param(A.after.w, A.after.w_bf16, A.cols, col, 1.f, w);
-            load_param(A.after.b, A.after.b_bf16, A.cols, col, 0.f, b);
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-              hn[p][e] = __builtin_fmaf(g[e], __builtin_fmaf(yn[p][e], w[e], b[e]), A.scale * hn[p][e]);
-          }
-          float w[V];
-          load_param(A.before.w, A.before.w_bf16, A.cols, col, 1.f, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            hn[p][e] = (hn[p][e] - mean2) * s2;
-            const float d = elem(du[p], e), g = d * w[e];
-            aw[p][e] = __builtin_fmaf(d, hn[p][e], aw[p][e]);
-            if constexpr (BIAS) ac[p][e] += d;
-            t[0] = __builtin_fmaf(g, hn[p][e], t[0]);
-            t[1] += g;
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (has2) {
-        sums.total(t);
-        const float m0 = t[0] * over, m1 = A.before.kind == SHAMPOO_NORM_LAYER ? t[1] * over : 0.f;
+    for (int64_t base = row0; base < row1; base += L) {
+      const int64_t row = base + part;
+      const bool here = L == 1 || row < row1;  // else the waves of `part` only meet the others at the barriers
+      const At at(A.cols, anew(threadIdx.x));
+      const uint32_t flags = anew_uniform(A.flags);
+      if (!kAhead) load(at, flags, min(row, row1 - 1));
+      if (!here) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const uint32_t col = (p * W * kWave + anew(lane)) * V;
-          float w[V];
-          load_param(A.before.w, A.before.w_bf16, A.cols, col, 1.f, w);
+          du[p].w = 0u;
+          dh[p].w = 0u;
+          r[p].clear();
+          y[p].clear();
+        }
+        st1 = st2 = f32x2_t{0.f, 1.f};
+      }
+      float yn[P][V], hn[P][V], dt[P][V], gu[P][V];
+      float t[2] = {0.f, 0.f};
+      const float s1 = st1[1], c1 = -st1[0] * st1[1], s2 = st2[1], c2 = -st2[0] * st2[1];
+      float token = 1.f;
+      if constexpr (JOIN) {
+        if (here && (flags & kJoinToken)) token = load_token(A, row);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float g = elem(du[p], e) * w[e];
-            const float d = s2 * (g - m1 - hn[p][e] * m0);
-            if constexpr (JOIN) {
-              dt[p][e] += d;
-            } else {
-              dt[p][e] = d;
-            }
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int e = 0; e < V; ++e) yn[p][e] = dt[p][e] = 0.f;
+        if (flags & kJoinDh) {
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            at.fix(dh[p], p);
+#pragma unroll
+            for (int e = 0; e < V; ++e) dt[p][e] = elem(dh[p], e);
           }
-          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (flags & kJoinNeedY) {
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            y[p].get(at, A.ky, p, yn[p]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) yn[p][e] = __builtin_fmaf(yn[p][e], s1, c1);
+          }
         }
       }
-      if (A.dr != nullptr) {
+      if (flags & kJoinNorm2) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          r[p].get(at, A.kr, p, hn[p]);
+          at.fix(du[p], p);
+          float w[V], b[V];
+          if constexpr (JOIN) {
+            n1.get(at, A, A.after, flags & kJoinRuns, p, w, b);
+            if (flags & kJoinToken) {
+#pragma unroll
+              for (int e = 0; e < V; ++e)
+                hn[p][e] = __builtin_fmaf(token, __builtin_fmaf(yn[p][e], w[e], b[e]), A.scale * hn[p][e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < V; ++e) {
+                hn[p][e] = BIAS ? __builtin_fmaf(A.scale, hn[p][e], b[e]) : A.scale * hn[p][e];
+                hn[p][e] = __builtin_fmaf(yn[p][e], w[e], hn[p][e]);
+              }
+            }
+          }
+          n2.get(at, A, A.before, false, p, w, b);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            hn[p][e] = __builtin_fmaf(hn[p][e], s2, c2);
+            const float d = elem(du[p], e);
+            gu[p][e] = d * w[e];
+            aw[p][e] = __builtin_fmaf(d, hn[p][e], aw[p][e]);
+            if constexpr (BIAS) ac[p][e] += d;
+            t[0] = __builtin_fmaf(gu[p][e], hn[p][e], t[0]);
+          }
+          if (flags & kJoinMean2) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[1] += gu[p][e];
+          }
+        }
+      }
+      if (kAhead && base + L < row1) load(at, flags, min(row + L, row1 - 1));  // in flight while this row is worked on
+      if (flags & kJoinNorm2) {
+        float m1 = 0.f;
+        if (flags & kJoinMean2) {
+          sums.total(t);
+          m1 = -s2 * (t[1] * over);
+        } else {
+          t[0] = sums.total1(t[0]);
+        }
+        const float m0 = -s2 * (t[0] * over);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            // s (g - mean(g) - hn mean(g hn))
+            const float d = __builtin_fmaf(hn[p][e], m0, JOIN ? dt[p][e] + m1 : m1);
+            dt[p][e] = __builtin_fmaf(gu[p][e], s2, d);
+          }
+        }
+      }
+      if (here && A.dr != nullptr) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float o[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = A.scale * dt[p][e];
-          store_row<SB, V>(row_at<SB>(A.dr, row, A.lddr), A.cols, (p * W * kWave + lane) * V, o);
+          for (int e = 0; e < V; ++e) o[e] = JOIN ? A.scale * dt[p][e] : dt[p][e];
+          at.template store<SB>(row_at<SB>(A.dr, row, A.lddr), p, o);
         }
       }
       if constexpr (JOIN) {
-        t[0] = t[1] = 0.f;
         float dtoken = 0.f;
+        t[0] = t[1] = 0.f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const uint32_t col = (p * W * kWave + anew(lane)) * V;
-          float g[V], w[V], b[V];
-          load_param(grow, A.gate_bf16, A.cols, col, 1.f, g);
-          load_param(A.after.w, A.after.w_bf16, A.cols, col, 1.f, w);
-          load_param(A.after.b, A.after.b_bf16, A.cols, col, 0.f, b);
+          float w[V], b[V];
+          n1.get(at, A, A.after, flags & kJoinRuns, p, w, b);
+          if (flags & kJoinToken) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              dtoken = __builtin_fmaf(dt[p][e], __builtin_fmaf(yn[p][e], w[e], b[e]), dtoken);
+              dt[p][e] *= token;
+            }
+          }
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            dtoken = __builtin_fmaf(dt[p][e], __builtin_fmaf(yn[p][e], w[e], b[e]), dtoken);
-            const float d = dt[p][e] * token;
-            aa[p][e] = __builtin_fmaf(d, yn[p][e], aa[p][e]);
-            if constexpr (BIAS) ab[p][e] += d;
-            dt[p][e] = d * g[e] * w[e];  // dz w1
+            aa[p][e] = __builtin_fmaf(dt[p][e], yn[p][e], aa[p][e]);
+            if constexpr (BIAS) ab[p][e] += dt[p][e];
+            dt[p][e] *= w[e];  // dz w
             t[0] = __builtin_fmaf(dt[p][e], yn[p][e], t[0]);
-            t[1] += dt[p][e];
           }
-          __builtin_amdgcn_sched_barrier(0);
+          if (flags & kJoinMean1) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[1] += dt[p][e];
+          }
         }
         float m0 = 0.f, m1 = 0.f;
-        if (has1) {
+        if (flags & kJoinMean1) {
           sums.total(t);
-          m0 = t[0] * over;
-          m1 = A.after.kind == SHAMPOO_NORM_LAYER ? t[1] * over : 0.f;
+          m0 = -s1 * (t[0] * over);
+          m1 = -s1 * (t[1] * over);
+        } else if (flags & kJoinNorm1) {
+          m0 = -s1 * (sums.total1(t[0]) * over);
         }
         if (A.dtoken != nullptr) {
           dtoken = sums.total1(dtoken);
-          if (lane == 0) {
-            if (A.dtoken_bf16) {
+          if (here && at.lane == 0) {
+            if (A.gate_bf16) {
               stg(static_cast<uint16_t*>(A.dtoken) + row, f32_to_bf16_bits(dtoken));
             } else {
               stg(static_cast<float*>(A.dtoken) + row, dtoken);
             }
           }
         }
-        if (A.dy != nullptr) {
+        if (here && A.dy != nullptr) {
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             float o[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = s1 * (dt[p][e] - m1 - yn[p][e] * m0);
-            store_row<BB, V>(row_at<BB>(A.dy, row, A.lddy), A.cols, (p * W * kWave + lane) * V, o);
+            for (int e = 0; e < V; ++e) o[e] = __builtin_fmaf(dt[p][e], s1, __builtin_fmaf(yn[p][e], m0, m1));
+            at.template store<BB>(row_at<BB>(A.dy, row, A.lddy), p, o);
           }
         }
       }
     }
+    const uint32_t lane = threadIdx.x % (kWave * W);
     if constexpr (JOIN) {
-      if (A.pa != nullptr) store_sums<W, P, V>(aa, A.pa + piece * (int64_t)A.pitch, A.pitch, lane0, lds);
+      if (A.pa != nullptr) store_sums<W, P, V, L>(aa, A.pa + piece * (int64_t)A.pitch, A.pitch, lane, part, lds);
       if constexpr (BIAS) {
-        if (A.pb != nullptr) store_sums<W, P, V>(ab, A.pb + piece * (int64_t)A.pitch, A.pitch, lane0, lds);
+        if (A.pb != nullptr) store_sums<W, P, V, L>(ab, A.pb + piece * (int64_t)A.pitch, A.pitch, lane, part, lds);
       }
     }
   }
-  if (has2) {
-    if (A.pw != nullptr) store_sums<W, P, V>(aw, A.pw + (int64_t)blockIdx.x * A.pitch, A.pitch, lane0, lds);
+  if (A.flags & kJoinNorm2) {
+    const uint32_t lane = threadIdx.x % (kWave * W);
+    if (A.pw != nullptr) store_sums<W, P, V, L>(aw, A.pw + blockIdx.x * (int64_t)A.pitch, A.pitch, lane, part, lds);
     if constexpr (BIAS) {
-      if (A.pc != nullptr) store_sums<W, P, V>(ac, A.pc + (int64_t)blockIdx.x * A.pitch, A.pitch, lane0, lds);
+      if (A.pc != nullptr) store_sums<W, P, V, L>(ac, A.pc + blockIdx.x * (int64_t)A.pitch, A.pitch, lane, part, lds);
     }
   }
 }

@@ -39,19 +39,20 @@ __device__ __forceinline__ void store_param(void* p, int bf16, int64_t i, float 
   }
 }
 
-constexpr int kSumLanes = 16;  // rows of partial sums that a workgroup reads side by side
+constexpr int kSumLanes = 64;  // rows of partial sums that a workgroup reads side by side
+constexpr int kSumCols = 16;   // columns of a workgroup
 
-// 64 columns a workgroup, blockIdx.y the job or (after the jobs) the gate's row.
-__global__ void __launch_bounds__(64 * kSumLanes) join_sums_kernel(const SumArgs S) {
-  __shared__ float lds[kSumLanes][64];
-  const int c = threadIdx.x % 64, part = threadIdx.x / 64;
-  const int64_t col = (int64_t)blockIdx.x * 64 + c;
+// kSumCols columns a workgroup, blockIdx.y the job or (after the jobs) the gate's row.
+__global__ void __launch_bounds__(kSumCols * kSumLanes) join_sums_kernel(const SumArgs S) {
+  __shared__ float lds[kSumLanes][kSumCols];
+  const int c = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
+  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
   const bool in = col < S.cols;
   float v = 0.f;
   if ((int)blockIdx.y < S.jobs) {
     const SumJob J = S.job[blockIdx.y];
     if (in) {
-#pragma unroll 8
+#pragma unroll 16
       for (int64_t s = part; s < J.count; s += kSumLanes) {
         float g = 1.f;
         if (J.gate != nullptr) g = param_at(J.gate, J.gate_bf16, (s / S.per_group) * S.cols + col);

@@ -11,16 +11,28 @@ using namespace shp;
 
 namespace {
 
+// Most workgroups of 256 threads (and their like in larger ones) of a forward pass; each
+// takes every so-many-th row.  Rows by rows of 2048 bf16 columns, 16384 of them: 68 us with 4096 and with 1536
+// (all that are resident), 75 with 2048 (a third of them alone at the end) and with one a row.
+constexpr int64_t kForwardBlocks = 4096;
+
 template <bool SB, bool BB>
 int forward(const JoinArgs& a, hipStream_t stream) {
-  return with_row_shape<SB ? 8 : 4>(a.cols, [&](auto w, auto p) {
+  constexpr int V = SB ? 8 : 4;
+  return with_row_shape<V>(a.cols, [&](auto w, auto p) {
     constexpr int W = decltype(w)::value, P = decltype(p)::value;
-    const int64_t blocks = std::min<int64_t>((a.rows + kRowLanes<W> - 1) / kRowLanes<W>, 1 << 20);
+    const int64_t blocks =
+        std::min<int64_t>((a.rows + kRowLanes<W> - 1) / kRowLanes<W>, kForwardBlocks * 256 / kRowThreads<W>);
     const dim3 grid((uint32_t)blocks), block(kRowThreads<W>);
-    if (a.y != nullptr) {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true>), grid, block, 0, stream, a);
+    const bool whole = a.cols % V == 0;
+    if (a.y != nullptr && whole) {
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true, true>), grid, block, 0, stream, a);
+    } else if (a.y != nullptr) {
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true, false>), grid, block, 0, stream, a);
+    } else if (whole) {
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false, true>), grid, block, 0, stream, a);
     } else {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false, false>), grid, block, 0, stream, a);
     }
     return check_launch();
   });
@@ -35,6 +47,9 @@ int valid_norm(const shampoo_norm& n) {
   return SHAMPOO_OK;
 }
 
+bool has_bias(const shampoo_join& j) { return (j.after.kind != SHAMPOO_NORM_NONE && j.after.bias != nullptr) ||
+                                              (j.before.kind != SHAMPOO_NORM_NONE && j.before.bias != nullptr); }
+
 NormSide norm_side(const shampoo_norm& n) {
   NormSide s = {};
   s.kind = (int)n.kind;
@@ -45,6 +60,10 @@ NormSide norm_side(const shampoo_norm& n) {
   s.b_bf16 = n.bias_dtype == SHAMPOO_T_BF16;
   s.eps = (float)n.eps;
   return s;
+}
+
+uint32_t norm_flags(int64_t kind, uint32_t norm, uint32_t mean) {
+  return kind == SHAMPOO_NORM_NONE ? 0 : kind == SHAMPOO_NORM_LAYER ? norm | mean : norm;
 }
 
 // What both directions check; `empty` where there is nothing to do.
@@ -89,29 +108,43 @@ int common(const shampoo_join* j, JoinArgs* a, bool* empty) {
   if (!join && a->ky.codes != nullptr) return SHAMPOO_EINVAL;
   a->after = norm_side(j->after);
   a->before = norm_side(j->before);
-  a->gate_kind = (int)j->gate_kind;
   a->gate = j->gate;
   a->gate_bf16 = j->gate_dtype == SHAMPOO_T_BF16;
   a->gate_rows = (uint32_t)(j->gate_kind == SHAMPOO_GATE_ROWS ? j->gate_rows : j->rows);
+  a->flags = norm_flags(j->after.kind, kJoinNorm1, kJoinMean1) | norm_flags(j->before.kind, kJoinNorm2, kJoinMean2);
+  if (j->gate_kind == SHAMPOO_GATE_ROWS) a->flags |= kJoinRuns;
+  if (j->gate_kind == SHAMPOO_GATE_TOKEN) a->flags |= kJoinToken;
   a->stats1 = j->after_stats;
   a->stats2 = j->before_stats;
   return SHAMPOO_OK;
 }
 
-// How the rows go to workgroups: about kBackBlocks of them, each within one run
-// of rows that share a gate, or (short runs) with whole ones.
-constexpr int64_t kBackBlocks = 512;
+// How the rows go to the backward kernel's workgroups: as many as are resident,
+// each within one run of rows that share a gate row, or (short runs) with whole ones.
 struct Split {
   int64_t groups, pieces, blocks;
   uint32_t per_group, per_block, piece_rows;
 };
-Split split_rows(int64_t rows, int64_t gate_rows) {
+Split split_rows(const shampoo_join& j) {
+  const bool bias = has_bias(j);
+  int64_t lanes = 1, resident = 256;
+  auto shape = [&](auto w, auto) {
+    constexpr int W = decltype(w)::value;
+    const bool many = bias && j.branch != nullptr;
+    lanes = many ? kBackLanes<W, true> : kBackLanes<W, false>;
+    resident = many && W <= 4 ? 768 : 256;
+    return 0;
+  };
+  if (j.stream_dtype == SHAMPOO_T_BF16) {
+    with_row_shape<8>((uint32_t)j.cols, shape);
+  } else {
+    with_row_shape<4>((uint32_t)j.cols, shape);
+  }
   Split s;
-  const int64_t run = gate_rows > 0 ? gate_rows : rows;
-  const int64_t want = std::max<int64_t>((rows + kBackBlocks - 1) / kBackBlocks, 4);
-  s.groups = rows / run;
-  s.per_group = (uint32_t)((run + want - 1) / want);
-  s.piece_rows = (uint32_t)((run + s.per_group - 1) / s.per_group);
+  const int64_t run = j.gate_kind == SHAMPOO_GATE_ROWS ? j.gate_rows : j.rows;
+  const int64_t want = (((j.rows + resident - 1) / resident) + lanes - 1) / lanes * lanes;
+  s.groups = j.rows / run;
+  s.piece_rows = (uint32_t)std::min<int64_t>(want, run);
   s.per_group = (uint32_t)((run + s.piece_rows - 1) / s.piece_rows);
   s.pieces = s.groups * s.per_group;
   s.per_block = (uint32_t)std::max<int64_t>(1, want / run);
@@ -136,6 +169,8 @@ int shampoo_join_forward(const shampoo_join* join, void* h, int64_t ld_h, void* 
     return SHAMPOO_EINVAL;
   if (empty) return SHAMPOO_OK;
   if (a.r == nullptr || (has_y && h == nullptr) || (has_u && u == nullptr)) return SHAMPOO_EINVAL;
+  if (a.kr.codes != nullptr) a.flags |= kJoinCodesR;
+  if (a.ky.codes != nullptr) a.flags |= kJoinCodesY;
   a.h = h;
   a.ldh = ld_h;
   a.u = u;
@@ -144,11 +179,12 @@ int shampoo_join_forward(const shampoo_join* join, void* h, int64_t ld_h, void* 
   return join->branch_dtype == SHAMPOO_T_BF16 ? forward<false, true>(a, stream) : forward<false, false>(a, stream);
 }
 
-size_t shampoo_join_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {
-  if (check_sides(rows, cols) != SHAMPOO_OK || cols > SHAMPOO_NORM_COLS || rows == 0 || cols == 0) return 0;
-  if (gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0)) return 0;
-  const Split s = split_rows(rows, gate_rows);
-  return (size_t)(2 * s.pieces + 2 * s.blocks) * (size_t)pitch_of(cols) * sizeof(float);
+size_t shampoo_join_workspace_bytes(const shampoo_join* join) {
+  JoinArgs a;
+  bool empty;
+  if (common(join, &a, &empty) != SHAMPOO_OK || empty) return 0;
+  const Split s = split_rows(*join);
+  return (size_t)((s.pieces + s.blocks) * (has_bias(*join) ? 2 : 1)) * (size_t)pitch_of(join->cols) * sizeof(float);
 }
 
 int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g, void* ws, size_t ws_bytes,
@@ -185,11 +221,11 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   }
   if ((has1 && a.stats1 == nullptr) || (has2 && a.stats2 == nullptr)) return SHAMPOO_EINVAL;
   const int64_t gate_rows = join->gate_kind == SHAMPOO_GATE_ROWS ? join->gate_rows : 0;
-  const size_t need = shampoo_join_workspace_bytes(join->rows, cols, gate_rows);
+  const size_t need = shampoo_join_workspace_bytes(join);
   if (ws == nullptr || ws_bytes < need) return SHAMPOO_EWORKSPACE;
   if (!aligned16(ws)) return SHAMPOO_EINVAL;
-  const Split s = split_rows(join->rows, gate_rows);
-  if (s.blocks > kMaxThreads / 512) return SHAMPOO_EUNSUPPORTED;
+  const Split s = split_rows(*join);
+  if (s.blocks > kMaxThreads / 1024) return SHAMPOO_EUNSUPPORTED;
   a.dh = g->d_h;
   a.lddh = g->ld_d_h;
   a.du = has2 ? g->d_u : nullptr;
@@ -198,24 +234,29 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   a.lddr = g->ld_d_residual;
   a.dy = g->d_branch;
   a.lddy = g->ld_d_branch;
-  a.has2 = has2;
-  a.pieces = s.pieces;
+  if (!has2) a.flags &= ~(kJoinNorm2 | kJoinMean2);
+  if (need_y) a.flags |= kJoinNeedY;
+  if (a.dh != nullptr) a.flags |= kJoinDh;
+  a.pieces = (uint32_t)s.pieces;
   a.per_group = s.per_group;
   a.per_block = s.per_block;
   a.piece_rows = s.piece_rows;
   a.pitch = (uint32_t)pitch_of(cols);
   if (join->gate_kind == SHAMPOO_GATE_TOKEN) {
     a.dtoken = g->d_gate;
-    a.dtoken_bf16 = a.gate_bf16;
   }
   const bool gate_sums = gate_rows > 0 && g->d_gate != nullptr;
-  float* const part = static_cast<float*>(ws);
-  const int64_t many = s.pieces * a.pitch;
-  if (g->d_after_weight != nullptr || gate_sums) a.pa = part;
-  if (g->d_after_bias != nullptr || (gate_sums && a.after.b != nullptr)) a.pb = part + many;
-  if (g->d_before_weight != nullptr) a.pw = part + 2 * many;
-  if (g->d_before_bias != nullptr) a.pc = part + 2 * many + s.blocks * a.pitch;
-  const bool bias = a.pb != nullptr || a.pc != nullptr;
+  float* part = static_cast<float*>(ws);
+  auto place = [&](bool wanted, int64_t rows) {
+    float* const at = wanted ? part : nullptr;
+    if (wanted) part += rows * a.pitch;
+    return at;
+  };
+  a.pa = place(g->d_after_weight != nullptr || gate_sums, s.pieces);
+  a.pw = place(g->d_before_weight != nullptr, s.blocks);
+  a.pb = place(g->d_after_bias != nullptr || (gate_sums && a.after.b != nullptr), s.pieces);
+  a.pc = place(g->d_before_bias != nullptr, s.blocks);
+  const bool bias = has_bias(*join);
   const uint32_t blocks = (uint32_t)s.blocks;
   if (join->stream_dtype == SHAMPOO_T_BF16) {
     rc = join_backward_bf16(a, has_y, keep, bias, blocks, stream);
@@ -262,7 +303,8 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
     }
   }
   if (rows_y == 0) return SHAMPOO_OK;
-  hipLaunchKernelGGL(join_sums_kernel, dim3((uint32_t)((cols + 63) / 64), (uint32_t)rows_y), dim3(64 * kSumLanes), 0,
+  hipLaunchKernelGGL(join_sums_kernel, dim3((uint32_t)((cols + kSumCols - 1) / kSumCols), (uint32_t)rows_y),
+                     dim3(kSumCols * kSumLanes), 0,
                      stream, m);
   return check_launch();
 }

@@ -67,6 +67,10 @@ struct Piece {
   __device__ __forceinline__ void load_at(const void* row, uint32_t col) {
     w = ldg_any<Words, BF16 ? 2 : 4>(static_cast<const uint8_t*>(row) + col * (BF16 ? 2u : 4u));
   }
+  // The same for what is read once.
+  __device__ __forceinline__ void load_once(const void* row, uint32_t col) {
+    w = ldg_once<Words, BF16 ? 2 : 4>(static_cast<const uint8_t*>(row) + col * (BF16 ? 2u : 4u));
+  }
   // Element e + d at e, 0 from V - d on (0 <= d <= V).
   __device__ __forceinline__ void shift_down(uint32_t d) {
     if constexpr (BF16) {
@@ -159,8 +163,8 @@ __device__ __forceinline__ float elem(const Piece<BF16, V>& x, int e) {
   }
 }
 
-// x rounded to nearest even into those of the V columns from col that are below cols.
-template <bool BF16, int V>
+// x rounded to nearest even into those of the V columns from col that are below cols (WHOLE: all are).
+template <bool BF16, int V, bool WHOLE = false>
 __device__ __forceinline__ void store_row(void* row, uint32_t cols, uint32_t col, const float (&x)[V]) {
   Piece<BF16, V> o;
 #pragma unroll
@@ -172,8 +176,8 @@ __device__ __forceinline__ void store_row(void* row, uint32_t cols, uint32_t col
     }
   }
   typedef typename Piece<BF16, V>::Words Words;
-  if (col + V <= cols) {
-    stg_any<Words, BF16 ? 2 : 4>(static_cast<uint8_t*>(row) + col * (BF16 ? 2u : 4u), o.w);
+  if (WHOLE || col + V <= cols) {
+    stg_once<Words, BF16 ? 2 : 4>(static_cast<uint8_t*>(row) + col * (BF16 ? 2u : 4u), o.w);
   } else {
 #pragma unroll
     for (int e = 0; e < V; ++e) {

@@ -384,13 +384,13 @@ class _Join(torch.autograd.Function):
         at = given.data_ptr()
         cols = spec.cols
         lib = capi.load()
-        size = lib.shampoo_join_workspace_bytes(spec.rows, cols, spec.run)
+        packed = spec.pack((at if r is None else r.data_ptr(), ldr),
+                           ((at if y is None else y.data_ptr()) if spec.join else 0, ldy), *parameters, buf, stats)
+        size = lib.shampoo_join_workspace_bytes(packed)
         ws = given.new_empty((size,), dtype=torch.uint8)
         rc = lib.shampoo_join_backward(
-            spec.pack((at if r is None else r.data_ptr(), ldr),
-                      ((at if y is None else y.data_ptr()) if spec.join else 0, ldy), *parameters, buf, stats),
-            capi.JOIN_GRADS.pack(0 if dh is None else dh.data_ptr(), lddh, 0 if du is None else du.data_ptr(), lddu,
-                                 ptr[0], cols, ptr[1], cols, *ptr[2:]),
+            packed, capi.JOIN_GRADS.pack(0 if dh is None else dh.data_ptr(), lddh, 0 if du is None else du.data_ptr(), lddu,
+                                         ptr[0], cols, ptr[1], cols, *ptr[2:]),
             ws.data_ptr(), size, _raw_stream(index))
         if rc:
             capi.check(rc, "shampoo_join_backward")

@@ -26,7 +26,8 @@ def mx8_codes(x):
     m = torch.round(torch.ldexp(a, 3 - e)).long()          # 0 ... 16, to nearest even
     e, m = torch.where(m == 16, e + 1, e), torch.where(m == 16, 8, m)
     code = torch.where(m >= 8, (e.long() + 7) * 8 + m - 8, m)
-    code = code + 128 * ((torch.copysign(torch.ones_like(y), y) < 0) & ~bad[..., None])
+    code = code + 128 * (torch.copysign(torch.ones_like(y), y) < 0)
+    code = torch.where(bad[..., None], 0x7f, code)
     return code.reshape(rows, -1), s
 
 

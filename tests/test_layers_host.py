@@ -61,7 +61,7 @@ def test_every_size_is_refused_with_its_own_code():
             if want == f.OK and cols > f.NORM_COLS:
                 want = f.EUNSUPPORTED
             assert _join(rows=rows, cols=cols, residual=0, ld=BIG) == want, (rows, cols)
-            need = f.shampoo_join_workspace_bytes(rows, cols, 0)
+            need = f.shampoo_join_workspace_bytes(_struct(rows=rows, cols=cols, ld=BIG))
             assert (need > 0) == (0 < rows <= 1 << 31 and 0 < cols <= f.NORM_COLS)
 
 
@@ -170,11 +170,17 @@ def test_join_backward_refuses(bad):
 
 
 def test_join_backward_needs_its_workspace():
-    need = f.shampoo_join_workspace_bytes(4, 64, 0)
-    assert need >= 4 * 64 * 4
+    need = f.shampoo_join_workspace_bytes(_struct())
+    assert need >= 4 * 64 * 4 // 16
     assert _back(n=need - 1) == f.EWORKSPACE and _back(ws=0, n=need) == f.EWORKSPACE
-    assert f.shampoo_join_workspace_bytes(4, 64, 3) == 0 and f.shampoo_join_workspace_bytes(4, 64, -1) == 0
+    size = f.shampoo_join_workspace_bytes
+    assert size(0) == 0 and size(_struct(y=FAKE, gate=(f.GATE_ROWS, FAKE, 0, 3))) == 0 and size(_struct(stream=7)) == 0
     # a row of partial sums for every run of rows that shares a row of the gate
-    assert f.shampoo_join_workspace_bytes(1 << 20, 64, 1) >= (1 << 20) * 64 * 4
-    # at most about 512 otherwise
-    assert f.shampoo_join_workspace_bytes(1 << 31, 16384, 0) <= 4 * 520 * 16384 * 4
+    assert size(_struct(rows=1 << 20, y=FAKE, gate=(f.GATE_ROWS, FAKE, 0, 1))) >= (1 << 20) * 64 * 4
+    # at most about 768 otherwise
+    biased = (f.NORM_LAYER, 1e-6, 0, 0, FAKE, 0)
+    for cols in (1, 512, 1000, 4096, 16384):
+        for y in (0, FAKE):
+            for stream in (f.T_F32, f.T_BF16):
+                one = size(_struct(rows=1 << 31, cols=cols, ld=BIG, ldy=BIG, y=y, stream=stream, branch=f.T_BF16, before=biased))
+                assert 0 < one <= 4 * 800 * (cols + 8) * 4
