@@ -10,11 +10,14 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libshampoo_mi355x.so")
+
+LAYERS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_layers.so")
 
 # Return codes
 OK = 0
@@ -211,6 +214,24 @@ def load(path=None):
     if path is None:
         _lib = lib
     return lib
+
+
+_layers = None
+
+
+def load_layers():
+    """Load (once) and return the extension module of the layers; raises if it is missing."""
+    global _layers
+    if _layers is None:
+        load()
+        if not os.path.exists(LAYERS_PATH):
+            raise RuntimeError(f"extension not built: {LAYERS_PATH} is missing "
+                               "(run `python -m inverse_root_preconditioning_amd.build`)")
+        spec = importlib.util.spec_from_file_location("_layers", LAYERS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _layers = module
+    return _layers
 
 
 def strerror(code):
