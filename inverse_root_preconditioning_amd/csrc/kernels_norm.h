@@ -142,19 +142,21 @@ struct Places {
   __device__ __forceinline__ Places(uint32_t columns, uint32_t thread) : cols(columns), lane(thread % (kWave * W)) {}
   __device__ __forceinline__ uint32_t col(int p) const { return (p * W * kWave + lane) * V; }
 
-  template <bool BF16>
+  // ONCE: it is read once.
+  template <bool BF16, bool ONCE = true>
   __device__ __forceinline__ Piece<BF16, V> load(const void* row, int p) const {
-    if constexpr (WHOLE) {
-      Piece<BF16, V> x;
-      x.load_once(row, min(col(p), cols - V));
-      return x;
-    } else if (cols >= V) {
-      Piece<BF16, V> x;
-      x.load_once(row, min(col(p), cols - V));
-      return x;
+    Piece<BF16, V> x;
+    if (WHOLE || cols >= V) {
+      const uint32_t from = min(col(p), cols - V);
+      if constexpr (ONCE) {
+        x.load_once(row, from);
+      } else {
+        x.load_at(row, from);
+      }
     } else {
-      return load_row<BF16, V>(row, cols, col(p));
+      x = load_row<BF16, V>(row, cols, col(p));
     }
+    return x;
   }
   template <bool BF16>
   __device__ __forceinline__ void fix(Piece<BF16, V>& x, int p) const {
@@ -181,18 +183,30 @@ struct Places {
 template <int W, int P, int V, bool WHOLE>
 __device__ __forceinline__ void load_param(const Places<W, P, V, WHOLE>& at, int p, const void* v, int bf16, float none,
                                            float (&x)[V]) {
-  const uint32_t col = at.col(p);
   if (v == nullptr) {
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = at.valid(p, e) ? none : 0.f;
   } else if (bf16) {
-    const Piece<true, V> q = load_row<true, V>(v, at.cols, col);
+    Piece<true, V> q = at.template load<true, false>(v, p);
+    at.fix(q, p);
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = elem(q, e);
+  } else if constexpr (V == 4) {
+    Piece<false, V> q = at.template load<false, false>(v, p);
+    at.fix(q, p);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = elem(q, e);
+  } else if constexpr (WHOLE) {
+    const uint32_t col = min(at.col(p), at.cols - V);
+    Piece<false, 4> q[V / 4];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) q[k].load_at(v, col + 4 * k);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = at.valid(p, e) ? elem(q[e / 4], e % 4) : 0.f;
   } else {
 #pragma unroll
     for (int k = 0; k < V / 4; ++k) {
-      const Piece<false, 4> q = load_row<false, 4>(v, at.cols, col + 4 * k);
+      const Piece<false, 4> q = load_row<false, 4>(v, at.cols, at.col(p) + 4 * k);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[4 * k + e] = elem(q, e);
     }

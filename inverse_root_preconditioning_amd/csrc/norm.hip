@@ -11,18 +11,23 @@ using namespace shp;
 
 namespace {
 
-// Most workgroups of 256 threads (and their like in larger ones) of a forward pass; each
-// takes every so-many-th row.  Rows by rows of 2048 bf16 columns, 16384 of them: 68 us with 4096 and with 1536
-// (all that are resident), 75 with 2048 (a third of them alone at the end) and with one a row.
-constexpr int64_t kForwardBlocks = 4096;
+// Rows that a workgroup of the forward kernel takes in turn, where that leaves
+// one for every compute unit: enough that the parameters' loads do not count
+// and a row's loads overlap the row before, few enough that the workgroups end
+// together.  Joins of 2^25 bf16 elements with 8-bit copies, us by turns:
+// rows of 512:  1: 70, 2: 63, 4: 64;   of 4096 (8 waves):   1: 84, 2: 68, 4: 65, 6: 67;
+// of 8192 (16 waves):  1: 97, 4: 68, 8: 65, 12: 80.
+template <int W>
+constexpr int64_t kTurns = W > 4 ? W / 2 : 2;
 
 template <bool SB, bool BB>
 int forward(const JoinArgs& a, hipStream_t stream) {
   constexpr int V = SB ? 8 : 4;
   return with_row_shape<V>(a.cols, [&](auto w, auto p) {
     constexpr int W = decltype(w)::value, P = decltype(p)::value;
-    const int64_t blocks =
-        std::min<int64_t>((a.rows + kRowLanes<W> - 1) / kRowLanes<W>, kForwardBlocks * 256 / kRowThreads<W>);
+    const int64_t rows = (a.rows + kRowLanes<W> - 1) / kRowLanes<W>;
+    const int64_t blocks = std::min<int64_t>(
+        std::max<int64_t>((rows + kTurns<W> - 1) / kTurns<W>, std::min<int64_t>(rows, 256)), kMaxThreads / 1024);
     const dim3 grid((uint32_t)blocks), block(kRowThreads<W>);
     const bool whole = a.cols % V == 0;
     if (a.y != nullptr && whole) {
