@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define SHAMPOO_ABI_VERSION 3
+#define SHAMPOO_ABI_VERSION 4
 
 /* Return codes. */
 enum {

@@ -75,7 +75,7 @@ GATE_ROWS = 1
 GATE_TOKEN = 2
 NORM_COLS = 16384         # most columns of a norm
 
-ABI_VERSION = 3
+ABI_VERSION = 4
 
 
 class shampoo_block(ctypes.Structure):

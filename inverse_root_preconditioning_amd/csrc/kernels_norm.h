@@ -41,9 +41,9 @@ struct JoinArgs {
   int64_t lddh, lddu;
   void *dr, *dy, *dtoken;
   int64_t lddr, lddy;
-  // Pieces of consecutive rows, `per_group` of them for each run of gate_rows
-  // rows; a workgroup takes `per_block` pieces.
-  uint32_t pieces, per_group, per_block, piece_rows;
+  // The rows' division: `per_group` pieces of each run of gate_rows rows; a
+  // workgroup takes `per_block` pieces.
+  uint32_t pieces, per_group, per_block;
   float *pa, *pb, *pw, *pc;  // partial sums: [pieces] of dt yn, dt; [workgroups] of du hn, du (NULL: not wanted)
   uint32_t pitch;            // floats between their rows
 };
@@ -307,7 +307,10 @@ template <int W>
 constexpr int kRowThreads = kWave * W * kRowLanes<W>;
 
 // Of the backward kernel: 16 waves' worth, so that there are few partial sums,
-// or 4 where a lane needs more registers than 16 waves leave it.
+// or 4 where a lane needs more registers than 16 waves leave it (MANY: a join
+// with biases, 146).  Joins and norms of 2^25 bf16 elements, us with 16, 8 and
+// 4 waves: rows of 512 66, 67, - and 34, 35, -; of 2048 73, 72, 78 and 37, 38, 38;
+// 1000 rows of 2048 14, 16, - and 10, 12, -.
 template <int W, bool MANY>
 constexpr int kBackLanes = W <= (MANY ? 4 : 16) ? (MANY ? 4 : 16) / W : 1;
 template <int W, bool MANY>
@@ -556,9 +559,9 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
   float aw[P][V] = {}, ac[P][V] = {}, aa[P][V], ab[P][V];
   for (uint32_t piece = begin; piece < end; ++piece) {
     const uint32_t group = __builtin_amdgcn_readfirstlane(piece / A.per_group);
-    const int64_t group0 = (int64_t)group * A.gate_rows, group1 = group0 + A.gate_rows;
-    const int64_t row0 = group0 + (int64_t)(piece - group * A.per_group) * A.piece_rows;
-    const int64_t row1 = row0 + A.piece_rows < group1 ? row0 + A.piece_rows : group1;
+    // every per_group-th set of L rows of the run: workgroups side by side read side by side
+    const int64_t row0 = (int64_t)group * A.gate_rows + (int64_t)(piece - group * A.per_group) * L;
+    const int64_t row1 = (int64_t)(group + 1) * A.gate_rows, step = (int64_t)A.per_group * L;
     {
       const At at(A.cols, anew(threadIdx.x));
       if (kAhead) load(at, A.flags, min(row0 + part, row1 - 1));
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
 #pragma unroll
         for (int e = 0; e < V; ++e) aa[p][e] = ab[p][e] = 0.f;
     }
-    for (int64_t base = row0; base < row1; base += L) {
+    for (int64_t base = row0; base < row1; base += step) {
       const int64_t row = base + part;
       const bool here = L == 1 || row < row1;  // else the waves of `part` only meet the others at the barriers
       const At at(A.cols, anew(threadIdx.x));
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
           }
         }
       }
-      if (kAhead && base + L < row1) load(at, flags, min(row + L, row1 - 1));  // in flight while this row is worked on
+      if (kAhead && base + step < row1) load(at, flags, min(row + step, row1 - 1));  // in flight while this row is worked on
       if (flags & kJoinNorm2) {
         float m1 = 0.f;
         if (flags & kJoinMean2) {

@@ -78,6 +78,7 @@ struct Rows {
   void* ptr() const { return t.data_ptr(); }
 };
 Rows rows_of(const Tensor& t) {
+  if (t.is_neg()) return rows_of(t.resolve_neg());  // a view that negates what is in memory
   const int64_t n = t.dim();
   if (t.is_contiguous()) return {t, t.size(-1)};
   if (n > 1 && t.numel() > 0 && t.stride(-1) == 1 && t.stride(-2) >= t.size(-1)) {
@@ -255,7 +256,7 @@ struct Inputs {
 void place_parameters(shampoo_join& j, Inputs& in) {
   auto place = [&](int i, const void*& ptr, int64_t& type) {
     if (!in.t[i].defined()) return;
-    if (!in.t[i].is_contiguous()) in.t[i] = in.t[i].contiguous();
+    if (!in.t[i].is_contiguous() || in.t[i].is_neg()) in.t[i] = in.t[i].resolve_neg().contiguous();
     ptr = in.t[i].data_ptr();
     type = type_of(in.t[i]);
   };
@@ -498,6 +499,7 @@ std::pair<Tensor, Tensor> join(const Tensor& residual, const OptTensor& branch, 
 }  // namespace
 
 PYBIND11_MODULE(_layers, m) {
+  if (shampoo_abi_version() != SHAMPOO_ABI_VERSION) throw py::import_error("libshampoo_mi355x.so ABI version mismatch");
   m.def("activate", &activate, py::call_guard<py::gil_scoped_release>());
   m.def("join", &join, py::call_guard<py::gil_scoped_release>());
 }

@@ -128,7 +128,7 @@ int common(const shampoo_join* j, JoinArgs* a, bool* empty) {
 // each within one run of rows that share a gate row, or (short runs) with whole ones.
 struct Split {
   int64_t groups, pieces, blocks;
-  uint32_t per_group, per_block, piece_rows;
+  uint32_t per_group, per_block;
 };
 Split split_rows(const shampoo_join& j) {
   const bool bias = has_bias(j);
@@ -149,8 +149,7 @@ Split split_rows(const shampoo_join& j) {
   const int64_t run = j.gate_kind == SHAMPOO_GATE_ROWS ? j.gate_rows : j.rows;
   const int64_t want = (((j.rows + resident - 1) / resident) + lanes - 1) / lanes * lanes;
   s.groups = j.rows / run;
-  s.piece_rows = (uint32_t)std::min<int64_t>(want, run);
-  s.per_group = (uint32_t)((run + s.piece_rows - 1) / s.piece_rows);
+  s.per_group = (uint32_t)((run + want - 1) / want);
   s.pieces = s.groups * s.per_group;
   s.per_block = (uint32_t)std::max<int64_t>(1, want / run);
   s.blocks = (s.pieces + s.per_block - 1) / s.per_block;
@@ -245,7 +244,6 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   a.pieces = (uint32_t)s.pieces;
   a.per_group = s.per_group;
   a.per_block = s.per_block;
-  a.piece_rows = s.piece_rows;
   a.pitch = (uint32_t)pitch_of(cols);
   if (join->gate_kind == SHAMPOO_GATE_TOKEN) {
     a.dtoken = g->d_gate;

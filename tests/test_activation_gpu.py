@@ -146,7 +146,8 @@ def test_shapes_strides_and_expanded_gradients():
     gen = torch.Generator(device="cuda").manual_seed(4)
     x = normal(gen, 3, 5, 4, 64)
     cases = {"transposed": x.transpose(0, 2), "sliced": x[:, 1:4], "columns apart": strided(x, "apart"),
-             "one dimension": x[0, 0, 0], "padded": strided(x, "padded"), "expanded": x[:1].expand(3, 5, 4, 64)}
+             "negated view": torch.view_as_complex(normal(gen, 5, 64, 2)).conj().imag, "one dimension": x[0, 0, 0],
+             "padded": strided(x, "padded"), "expanded": x[:1].expand(3, 5, 4, 64)}
     for name, t in cases.items():
         want = L.activation(t.contiguous())
         assert torch.equal(L.activation(t), want), name
