@@ -4,10 +4,11 @@
 // (RMS: mean = 0) or variance (layer) + eps); either norm may be absent, and
 // the norm alone is the join without y: h = r.
 //
-// W waves hold a row of up to 64 W P V columns in registers, each lane P pieces
-// of V consecutive elements, so that a row is read once however many sums over
-// it the formulas need; the parameters' columns stay in registers over all the rows
-// that a workgroup takes.
+// `waves` waves (1 to 16) hold a row of up to 64 waves P V columns in registers,
+// each lane P pieces of V consecutive elements, so that a row is read once
+// however many sums over it the formulas need; the parameters' columns stay in
+// registers over all the rows that a workgroup takes.  The waves are a number of
+// the call, so that few lanes are idle whatever the width.
 #pragma once
 
 #include "kernels_mx8.h"
@@ -24,6 +25,7 @@ struct NormSide {
 struct JoinArgs {
   int64_t rows;
   uint32_t cols, flags;
+  uint32_t waves, lanes;     // of a row; rows that a workgroup holds side by side
   float scale;
   const void *r, *y;  // the inputs; y unused without a join
   int64_t ldr, ldy;
@@ -93,30 +95,42 @@ __device__ __forceinline__ float wave_total(float v) {
   return (r0 + r1) + (r2 + r3);
 }
 
-// Sums over the W waves of a row.  Two buffers in turn: a wave writes one again
-// only after the barrier of the next sum, which every wave reaches after its
-// reads of this one.
-template <int W>
+constexpr int kMaxWaves = 16;
+constexpr int kSumsFloats = 4 * kMaxWaves;  // LDS of a row's sums
+
+// Sums over the waves of a row, in a fixed order.  Two buffers in turn: a wave
+// writes one again only after the barrier of the next sum, which every wave
+// reaches after its reads of this one.  What lies beyond the row's waves is 0.
 struct RowSums {
-  float* lds;  // [2][2][W] of this row
-  int turn = 0;
+  float* lds;  // [2][2][kMaxWaves] of this row
+  uint32_t waves, wave;
+  uint32_t turn = 0;
+  // Called by every thread, with one more barrier before the first sum.
+  __device__ __forceinline__ RowSums(float* all, uint32_t part, uint32_t n, uint32_t rows)
+      : lds(all + part * kSumsFloats), waves(n), wave(__builtin_amdgcn_readfirstlane(threadIdx.x / kWave) - part * n) {
+    if (waves > 1) {
+      for (uint32_t i = threadIdx.x; i < rows * kSumsFloats; i += blockDim.x) all[i] = 0.f;
+      __syncthreads();
+    }
+  }
   template <int N>
   __device__ __forceinline__ void total(float (&v)[N]) {
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] = wave_total(v[n]);
-    if constexpr (W > 1) {
-      float* const at = lds + turn * 2 * W;
-      const int wave = threadIdx.x / kWave % W;
+    if (waves > 1) {
+      float* const at = lds + turn * 2 * kMaxWaves;
       if (threadIdx.x % kWave == 0) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) at[n * W + wave] = v[n];
+        for (int n = 0; n < N; ++n) at[n * kMaxWaves + wave] = v[n];
       }
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        v[n] = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v[n] += at[n * W + w];
+        const floatx4* const q = reinterpret_cast<const floatx4*>(at + n * kMaxWaves);
+        floatx4 t = q[0];
+        if (waves > 4) t += q[1];
+        if (waves > 8) t += q[2] + q[3];
+        v[n] = (t[0] + t[1]) + (t[2] + t[3]);
       }
       turn ^= 1;
     }
@@ -136,11 +150,11 @@ struct RowSums {
 // the row's end those before it), so that no branch stands between them; `fix`
 // puts right what a piece beyond the end, or over it, has read, when it has come.
 // WHOLE: the columns are a multiple of V.
-template <int W, int P, int V, bool WHOLE>
+template <int P, int V, bool WHOLE>
 struct Places {
-  uint32_t cols, lane;
-  __device__ __forceinline__ Places(uint32_t columns, uint32_t thread) : cols(columns), lane(thread % (kWave * W)) {}
-  __device__ __forceinline__ uint32_t col(int p) const { return (p * W * kWave + lane) * V; }
+  uint32_t cols, width, lane;  // of the row; its lanes; this one
+  __device__ __forceinline__ Places(const JoinArgs& A, uint32_t which) : cols(A.cols), width(A.waves * kWave), lane(which) {}
+  __device__ __forceinline__ uint32_t col(int p) const { return (p * width + lane) * V; }
 
   // ONCE: it is read once.
   template <bool BF16, bool ONCE = true>
@@ -180,8 +194,8 @@ struct Places {
 };
 
 // Piece p of a vector of parameters, 0 beyond its end; without the vector, `none`.
-template <int W, int P, int V, bool WHOLE>
-__device__ __forceinline__ void load_param(const Places<W, P, V, WHOLE>& at, int p, const void* v, int bf16, float none,
+template <int P, int V, bool WHOLE>
+__device__ __forceinline__ void load_param(const Places<P, V, WHOLE>& at, int p, const void* v, int bf16, float none,
                                            float (&x)[V]) {
   if (v == nullptr) {
 #pragma unroll
@@ -191,34 +205,20 @@ __device__ __forceinline__ void load_param(const Places<W, P, V, WHOLE>& at, int
     at.fix(q, p);
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = elem(q, e);
-  } else if constexpr (V == 4) {
+  } else {
     Piece<false, V> q = at.template load<false, false>(v, p);
     at.fix(q, p);
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = elem(q, e);
-  } else if constexpr (WHOLE) {
-    const uint32_t col = min(at.col(p), at.cols - V);
-    Piece<false, 4> q[V / 4];
-#pragma unroll
-    for (int k = 0; k < V / 4; ++k) q[k].load_at(v, col + 4 * k);
-#pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = at.valid(p, e) ? elem(q[e / 4], e % 4) : 0.f;
-  } else {
-#pragma unroll
-    for (int k = 0; k < V / 4; ++k) {
-      const Piece<false, 4> q = load_row<false, 4>(v, at.cols, at.col(p) + 4 * k);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * k + e] = elem(q, e);
-    }
   }
 }
 
 // Parameters of a lane's pieces: kept in registers, or where those do not
 // suffice, read again for every use.
-template <int W, int P, int V, bool WHOLE, bool BIAS, bool KEPT>
+template <int P, int V, bool WHOLE, bool BIAS, bool KEPT>
 struct Parameters {
   static constexpr bool kKept = KEPT;
-  typedef Places<W, P, V, WHOLE> At;
+  typedef Places<P, V, WHOLE> At;
   float w[kKept ? P : 1][V], b[kKept ? P : 1][V];
   uint32_t run;
 
@@ -256,7 +256,7 @@ struct Parameters {
       }
     } else {
       __builtin_amdgcn_sched_barrier(0);  // one piece's parameters at a time
-      load(At(at.cols, anew(at.lane)), A, n, gated, p, wp, bp);
+      load(At(A, anew(at.lane)), A, n, gated, p, wp, bp);
       if constexpr (!BIAS) {
 #pragma unroll
         for (int e = 0; e < V; ++e) bp[e] = 0.f;
@@ -270,9 +270,9 @@ __device__ __forceinline__ float load_token(const JoinArgs& A, int64_t row) {
 }
 
 // Mean and s of a row held in pieces, zero beyond its end.
-template <int W, int P, int V, bool WHOLE>
-__device__ __forceinline__ void row_stats(const Places<W, P, V, WHOLE>& at, const float (&x)[P][V], bool centred,
-                                          float eps, RowSums<W>& sums, float& mean, float& s) {
+template <int P, int V, bool WHOLE>
+__device__ __forceinline__ void row_stats(const Places<P, V, WHOLE>& at, const float (&x)[P][V], bool centred,
+                                          float eps, RowSums& sums, float& mean, float& s) {
   const float over = 1.f / (float)at.cols;
   mean = 0.f;
   float ss = 0.f;
@@ -300,35 +300,22 @@ __device__ __forceinline__ void row_stats(const Places<W, P, V, WHOLE>& at, cons
   s = 1.f / sqrtf(sums.total1(ss) * over + eps);
 }
 
-// Rows that a workgroup of the forward kernel holds at once: 4 of a wave each, or one.
-template <int W>
-constexpr int kRowLanes = W == 1 ? 4 : 1;
-template <int W>
-constexpr int kRowThreads = kWave * W * kRowLanes<W>;
-
-// Of the backward kernel: 16 waves' worth, so that there are few partial sums,
-// or 4 where a lane needs more registers than 16 waves leave it (MANY: a join
-// with biases, 146).  Joins and norms of 2^25 bf16 elements, us with 16, 8 and
-// 4 waves: rows of 512 66, 67, - and 34, 35, -; of 2048 73, 72, 78 and 37, 38, 38;
-// 1000 rows of 2048 14, 16, - and 10, 12, -.
-template <int W, bool MANY>
-constexpr int kBackLanes = W <= (MANY ? 4 : 16) ? (MANY ? 4 : 16) / W : 1;
-template <int W, bool MANY>
-constexpr int kBackThreads = kWave * W * kBackLanes<W, MANY>;
-
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
 
-template <bool SB, bool BB, int W, int P, bool JOIN, bool WHOLE>
-__global__ void __launch_bounds__(kRowThreads<W>) join_forward_kernel(const JoinArgs A) {
-  constexpr int V = SB ? 8 : 4, L = kRowLanes<W>;
-  typedef Places<W, P, V, WHOLE> At;
-  __shared__ float red[4 * W];
-  RowSums<W> sums{red};
-  const int64_t step = (int64_t)gridDim.x * L;
-  int64_t row = (int64_t)blockIdx.x * L + __builtin_amdgcn_readfirstlane(threadIdx.x / (kWave * W));
-  if (row >= A.rows) return;  // a wave by itself (W = 1), or the whole workgroup
+// Several rows a workgroup only where each is a wave's, which needs no barrier.
+template <bool SB, bool BB, int P, bool JOIN, bool WHOLE>
+__global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const JoinArgs A) {
+  constexpr int V = SB ? 8 : 4;
+  typedef Places<P, V, WHOLE> At;
+  __shared__ __attribute__((aligned(16))) float red[kSumsFloats];
+  const uint32_t part = A.lanes > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : 0;
+  const uint32_t lane0 = threadIdx.x - part * kWave;
+  RowSums sums(red, 0, A.waves, 1);
+  const int64_t step = (int64_t)gridDim.x * A.lanes;
+  int64_t row = (int64_t)blockIdx.x * A.lanes + part;
+  if (row >= A.rows) return;  // a wave by itself, or the whole workgroup
   Piece<SB, V> r[P];
   Piece<BB, V> y[P];
   auto load = [&](const At& at, int64_t from) __attribute__((always_inline)) {
@@ -338,16 +325,16 @@ __global__ void __launch_bounds__(kRowThreads<W>) join_forward_kernel(const Join
       if constexpr (JOIN) y[p] = at.template load<BB>(row_at<BB>(A.y, from, A.ldy), p);
     }
   };
-  Parameters<W, P, V, WHOLE, true, (P * V <= 8)> n1, n2;
+  Parameters<P, V, WHOLE, true, (P * V <= 8)> n1, n2;
   {
-    const At at(A.cols, threadIdx.x);
+    const At at(A, lane0);
     load(at, row);
     if constexpr (JOIN)
       n1.keep(at, A, A.after, A.flags & kJoinRuns, __builtin_amdgcn_readfirstlane((uint32_t)row / A.gate_rows));
     n2.keep(at, A, A.before, false, 0);
   }
   while (true) {
-    const At at(A.cols, anew(threadIdx.x));
+    const At at(A, anew(lane0));
     const uint32_t flags = anew_uniform(A.flags);
     float x[P][V], rf[P][V];
 #pragma unroll
@@ -440,41 +427,35 @@ __global__ void __launch_bounds__(kRowThreads<W>) join_forward_kernel(const Join
 // ---------------------------------------------------------------------------
 
 // A lane's sums, added over the rows held side by side, to a row of partial sums.
-template <int W, int P, int V, int L>
-__device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, uint32_t pitch, uint32_t lane, int part,
-                                           float* lds) {
-  constexpr uint32_t kCols = kWave * W * V;  // of a piece
-  if constexpr (L == 1) {
+template <int P, int V>
+__device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, const JoinArgs& A, uint32_t lane,
+                                           uint32_t part, float* lds) {
+  const uint32_t cols = A.waves * kWave * V;  // of a piece
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const uint32_t col = p * kCols + lane * V;
-      if (col < pitch) {
+  for (int p = 0; p < P; ++p) {
+    floatx4 q[V / 4];
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q)
-          stg(reinterpret_cast<floatx4*>(to + col) + q,
-              floatx4{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]});
+    for (int i = 0; i < V / 4; ++i) q[i] = floatx4{acc[p][4 * i], acc[p][4 * i + 1], acc[p][4 * i + 2], acc[p][4 * i + 3]};
+    if (A.lanes == 1) {
+      const uint32_t col = p * cols + lane * V;
+      if (col < A.pitch) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) stg(reinterpret_cast<floatx4*>(to + col) + i, q[i]);
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      __syncthreads();  // the last piece, or the rows' sums, have been read
-#pragma unroll
-      for (int q = 0; q < V / 4; ++q)
-        reinterpret_cast<floatx4*>(lds + part * kCols + lane * V)[q] =
-            floatx4{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
+      for (int i = 0; i < V / 4; ++i) reinterpret_cast<floatx4*>(lds + part * cols + lane * V)[i] = q[i];
       __syncthreads();
-      for (uint32_t c = threadIdx.x; c < kCols; c += kWave * W * L) {
-        const uint32_t col = p * kCols + c;
-        if (col < pitch) {
+      for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
+        const uint32_t col = p * cols + c;
+        if (col < A.pitch) {
           float v = lds[c];
-#pragma unroll
-          for (int i = 1; i < L; ++i) v += lds[i * kCols + c];
+          for (uint32_t i = 1; i < A.lanes; ++i) v += lds[i * cols + c];
           stg(to + col, v);
         }
       }
+      __syncthreads();
     }
-    __syncthreads();  // before the rows' sums write here again
   }
 }
 
@@ -511,16 +492,20 @@ struct Kept {
   }
 };
 
-template <bool SB, bool BB, int W, int P, bool JOIN, bool KEEP, bool BIAS, bool WHOLE>
-__global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backward_kernel(const JoinArgs A) {
-  constexpr int V = SB ? 8 : 4, L = kBackLanes<W, JOIN && BIAS>;
-  typedef Places<W, P, V, WHOLE> At;
-  __shared__ __attribute__((aligned(16))) float lds[L == 1 ? 4 * W : L * kWave * W * V];
-  const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / (kWave * W));
+// FEW: 8 waves a workgroup at most, with twice the registers.
+template <bool SB, bool BB, int P, bool JOIN, bool KEEP, bool BIAS, bool FEW, bool WHOLE>
+__global__ void __launch_bounds__(kWave * (FEW ? kMaxWaves / 2 : kMaxWaves)) join_backward_kernel(const JoinArgs A) {
+  constexpr int V = SB ? 8 : 4;
+  typedef Places<P, V, WHOLE> At;
   // Parameters in registers and the next row's loads in flight, where there are registers for
   // them: 128 in a workgroup of 16 waves.  (4096 rows of 16384 without this rule: 690 us, in scratch memory.)
-  constexpr bool kAhead = P * V <= 8 && !(JOIN && BIAS && W == 16);
-  RowSums<W> sums{lds + part * 4 * W};
+  constexpr bool kAhead = P * V <= (FEW || !(JOIN && BIAS) ? 8 : 4);
+  __shared__ __attribute__((aligned(16))) float red[kMaxWaves * kSumsFloats];
+  __shared__ __attribute__((aligned(16))) float lds[kMaxWaves * kWave * V];  // the columns' sums of lanes x waves
+  const uint32_t L = A.lanes;
+  const uint32_t part = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / A.waves);
+  const uint32_t lane0 = threadIdx.x - part * A.waves * kWave;
+  RowSums sums(red, part, A.waves, L);
   const float over = 1.f / (float)A.cols;
 
   // One row's inputs, as they come from memory.
@@ -553,9 +538,9 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
 
   const uint32_t begin = blockIdx.x * A.per_block;
   const uint32_t end = min(begin + A.per_block, A.pieces);
-  Parameters<W, P, V, WHOLE, BIAS, kAhead> n1;
-  Parameters<W, P, V, WHOLE, false, kAhead> n2;
-  n2.keep(At(A.cols, threadIdx.x), A, A.before, false, 0);
+  Parameters<P, V, WHOLE, BIAS, kAhead> n1;
+  Parameters<P, V, WHOLE, false, kAhead> n2;
+  n2.keep(At(A, lane0), A, A.before, false, 0);
   float aw[P][V] = {}, ac[P][V] = {}, aa[P][V], ab[P][V];
   for (uint32_t piece = begin; piece < end; ++piece) {
     const uint32_t group = __builtin_amdgcn_readfirstlane(piece / A.per_group);
@@ -563,7 +548,7 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
     const int64_t row0 = (int64_t)group * A.gate_rows + (int64_t)(piece - group * A.per_group) * L;
     const int64_t row1 = (int64_t)(group + 1) * A.gate_rows, step = (int64_t)A.per_group * L;
     {
-      const At at(A.cols, anew(threadIdx.x));
+      const At at(A, anew(lane0));
       if (kAhead) load(at, A.flags, min(row0 + part, row1 - 1));
       if constexpr (JOIN) n1.keep(at, A, A.after, A.flags & kJoinRuns, group);
     }
@@ -575,8 +560,8 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
     }
     for (int64_t base = row0; base < row1; base += step) {
       const int64_t row = base + part;
-      const bool here = L == 1 || row < row1;  // else the waves of `part` only meet the others at the barriers
-      const At at(A.cols, anew(threadIdx.x));
+      const bool here = row < row1;  // else the waves of `part` only meet the others at the barriers
+      const At at(A, anew(lane0));
       const uint32_t flags = anew_uniform(A.flags);
       if (!kAhead) load(at, flags, min(row, row1 - 1));
       if (!here) {
@@ -736,19 +721,17 @@ __global__ void __launch_bounds__((kBackThreads<W, (JOIN && BIAS)>)) join_backwa
         }
       }
     }
-    const uint32_t lane = threadIdx.x % (kWave * W);
     if constexpr (JOIN) {
-      if (A.pa != nullptr) store_sums<W, P, V, L>(aa, A.pa + piece * (int64_t)A.pitch, A.pitch, lane, part, lds);
+      if (A.pa != nullptr) store_sums<P, V>(aa, A.pa + piece * (int64_t)A.pitch, A, lane0, part, lds);
       if constexpr (BIAS) {
-        if (A.pb != nullptr) store_sums<W, P, V, L>(ab, A.pb + piece * (int64_t)A.pitch, A.pitch, lane, part, lds);
+        if (A.pb != nullptr) store_sums<P, V>(ab, A.pb + piece * (int64_t)A.pitch, A, lane0, part, lds);
       }
     }
   }
   if (A.flags & kJoinNorm2) {
-    const uint32_t lane = threadIdx.x % (kWave * W);
-    if (A.pw != nullptr) store_sums<W, P, V, L>(aw, A.pw + blockIdx.x * (int64_t)A.pitch, A.pitch, lane, part, lds);
+    if (A.pw != nullptr) store_sums<P, V>(aw, A.pw + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
     if constexpr (BIAS) {
-      if (A.pc != nullptr) store_sums<W, P, V, L>(ac, A.pc + blockIdx.x * (int64_t)A.pitch, A.pitch, lane, part, lds);
+      if (A.pc != nullptr) store_sums<P, V>(ac, A.pc + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
     }
   }
 }

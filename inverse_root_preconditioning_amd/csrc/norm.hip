@@ -15,29 +15,31 @@ namespace {
 // one for every compute unit: enough that the parameters' loads do not count
 // and a row's loads overlap the row before, few enough that the workgroups end
 // together.  Joins of 2^25 bf16 elements with 8-bit copies, us by turns:
-// rows of 512:  1: 70, 2: 63, 4: 64;   of 4096 (8 waves):   1: 84, 2: 68, 4: 65, 6: 67;
-// of 8192 (16 waves):  1: 97, 4: 68, 8: 65, 12: 80.
-template <int W>
-constexpr int64_t kTurns = W > 4 ? W / 2 : 2;
+// rows of 512:  1: 70, 2: 63, 4: 64;   of 2050 (5 waves)  2: 110, 4: 99, 8: 100;
+// of 5120 (10):  5: 78, 8: 83, 9: 71, 10: 76;   of 8192 (16):  1: 97, 4: 68, 8: 65, 12: 80.
+int64_t turns(uint32_t waves) { return std::min<int64_t>(std::max<int64_t>(waves - 1, 3), 8); }
 
 template <bool SB, bool BB>
-int forward(const JoinArgs& a, hipStream_t stream) {
+int forward(JoinArgs a, hipStream_t stream) {
   constexpr int V = SB ? 8 : 4;
-  return with_row_shape<V>(a.cols, [&](auto w, auto p) {
-    constexpr int W = decltype(w)::value, P = decltype(p)::value;
-    const int64_t rows = (a.rows + kRowLanes<W> - 1) / kRowLanes<W>;
-    const int64_t blocks = std::min<int64_t>(
-        std::max<int64_t>((rows + kTurns<W> - 1) / kTurns<W>, std::min<int64_t>(rows, 256)), kMaxThreads / 1024);
-    const dim3 grid((uint32_t)blocks), block(kRowThreads<W>);
-    const bool whole = a.cols % V == 0;
+  const RowLayout layout = row_layout(a.cols, V);
+  a.waves = layout.waves;
+  a.lanes = a.waves == 1 ? 4 : 1;
+  const int64_t rows = (a.rows + a.lanes - 1) / a.lanes, each = turns(a.waves);
+  const int64_t blocks =
+      std::min<int64_t>(std::max<int64_t>((rows + each - 1) / each, std::min<int64_t>(rows, 256)), kMaxThreads / 1024);
+  const dim3 grid((uint32_t)blocks), block(kWave * a.waves * a.lanes);
+  const bool whole = a.cols % V == 0;
+  return with_pieces<V>(layout.pieces, [&](auto p) {
+    constexpr int P = decltype(p)::value;
     if (a.y != nullptr && whole) {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true, true>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, P, true, true>), grid, block, 0, stream, a);
     } else if (a.y != nullptr) {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, true, false>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, P, true, false>), grid, block, 0, stream, a);
     } else if (whole) {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false, true>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, P, false, true>), grid, block, 0, stream, a);
     } else {
-      hipLaunchKernelGGL((join_forward_kernel<SB, BB, W, P, false, false>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_forward_kernel<SB, BB, P, false, false>), grid, block, 0, stream, a);
     }
     return check_launch();
   });
@@ -129,25 +131,17 @@ int common(const shampoo_join* j, JoinArgs* a, bool* empty) {
 struct Split {
   int64_t groups, pieces, blocks;
   uint32_t per_group, per_block;
+  RowLayout layout;
+  uint32_t lanes;
 };
 Split split_rows(const shampoo_join& j) {
-  const bool bias = has_bias(j);
-  int64_t lanes = 1, resident = 256;
-  auto shape = [&](auto w, auto) {
-    constexpr int W = decltype(w)::value;
-    const bool many = bias && j.branch != nullptr;
-    lanes = many ? kBackLanes<W, true> : kBackLanes<W, false>;
-    resident = many && W <= 4 ? 768 : 256;
-    return 0;
-  };
-  if (j.stream_dtype == SHAMPOO_T_BF16) {
-    with_row_shape<8>((uint32_t)j.cols, shape);
-  } else {
-    with_row_shape<4>((uint32_t)j.cols, shape);
-  }
   Split s;
+  const bool bf16 = j.stream_dtype == SHAMPOO_T_BF16;
+  s.layout = row_layout(j.cols, bf16 ? 8 : 4);
+  const BackGrid grid = back_grid(s.layout, bf16 && has_bias(j) && j.branch != nullptr);
+  s.lanes = grid.lanes;
   const int64_t run = j.gate_kind == SHAMPOO_GATE_ROWS ? j.gate_rows : j.rows;
-  const int64_t want = (((j.rows + resident - 1) / resident) + lanes - 1) / lanes * lanes;
+  const int64_t want = (((j.rows + grid.resident - 1) / grid.resident) + s.lanes - 1) / s.lanes * s.lanes;
   s.groups = j.rows / run;
   s.per_group = (uint32_t)((run + want - 1) / want);
   s.pieces = s.groups * s.per_group;
@@ -244,6 +238,8 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   a.pieces = (uint32_t)s.pieces;
   a.per_group = s.per_group;
   a.per_block = s.per_block;
+  a.waves = s.layout.waves;
+  a.lanes = s.lanes;
   a.pitch = (uint32_t)pitch_of(cols);
   if (join->gate_kind == SHAMPOO_GATE_TOKEN) {
     a.dtoken = g->d_gate;
@@ -262,11 +258,11 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   const bool bias = has_bias(*join);
   const uint32_t blocks = (uint32_t)s.blocks;
   if (join->stream_dtype == SHAMPOO_T_BF16) {
-    rc = join_backward_bf16(a, has_y, keep, bias, blocks, stream);
+    rc = join_backward_bf16(a, s.layout.pieces, keep, bias, blocks, stream);
   } else if (join->branch_dtype == SHAMPOO_T_BF16) {
-    rc = join_backward_mixed(a, has_y, keep, bias, blocks, stream);
+    rc = join_backward_mixed(a, s.layout.pieces, keep, bias, blocks, stream);
   } else {
-    rc = join_backward_f32(a, has_y, keep, bias, blocks, stream);
+    rc = join_backward_f32(a, s.layout.pieces, keep, bias, blocks, stream);
   }
   if (rc != SHAMPOO_OK) return rc;
   SumArgs m = {};

@@ -3,8 +3,8 @@
 
 namespace shp {
 
-int join_backward_bf16(const JoinArgs& a, bool join, bool keep, bool bias, uint32_t blocks, hipStream_t stream) {
-  return launch_join_backward<true, true>(a, join, keep, bias, blocks, stream);
+int join_backward_bf16(const JoinArgs& a, int pieces, bool keep, bool bias, uint32_t blocks, hipStream_t stream) {
+  return launch_join_backward<true, true>(a, pieces, keep, bias, blocks, stream);
 }
 
 }  // namespace shp

@@ -178,17 +178,30 @@ __device__ __forceinline__ void store_row(void* row, uint32_t cols, uint32_t col
   typedef typename Piece<BF16, V>::Words Words;
   if (WHOLE || col + V <= cols) {
     stg_once<Words, BF16 ? 2 : 4>(static_cast<uint8_t*>(row) + col * (BF16 ? 2u : 4u), o.w);
-  } else {
+  } else if (col < cols) {
+    // the elements that are left in halves, quarters, ... of a piece, each stored from its front
+    const uint32_t left = cols - col;
+    uint8_t* at = static_cast<uint8_t*>(row) + col * (BF16 ? 2u : 4u);
+    static_for<3>([&](auto I) __attribute__((always_inline)) {
+      constexpr int n = V >> (decltype(I)::value + 1);  // elements, of kBytes
+      constexpr int kBytes = n * (BF16 ? 2 : 4);
+      if constexpr (n > 0) {
+        if (left & n) {
+          if constexpr (kBytes >= 4) {
+            typedef uint32_t Part __attribute__((ext_vector_type(kBytes / 4)));
+            Part q;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (col + e < cols) {
-        if constexpr (BF16) {
-          stg(static_cast<uint16_t*>(row) + col + e, (uint16_t)(o.w[e / 2] >> (16 * (e & 1))));
-        } else {
-          stg(static_cast<uint32_t*>(row) + col + e, (uint32_t)o.w[e]);
+            for (int i = 0; i < kBytes / 4; ++i) q[i] = o.w[i];
+            stg_any<Part, BF16 ? 2 : 4>(at, q);
+#pragma unroll
+            for (int i = 0; i + kBytes / 4 < o.kWords; ++i) o.w[i] = o.w[i + kBytes / 4];
+          } else {
+            stg(reinterpret_cast<uint16_t*>(at), (uint16_t)(uint32_t)o.w[0]);
+          }
+          at += kBytes;
         }
       }
-    }
+    });
   }
 }
 

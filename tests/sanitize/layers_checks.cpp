@@ -22,9 +22,9 @@ static int g_fail = 0;
 // The backward kernels' launches are in files of their own, which are not built here.
 namespace shp {
 struct JoinArgs;
-int join_backward_bf16(const JoinArgs&, bool, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
-int join_backward_f32(const JoinArgs&, bool, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
-int join_backward_mixed(const JoinArgs&, bool, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
+int join_backward_bf16(const JoinArgs&, int, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
+int join_backward_f32(const JoinArgs&, int, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
+int join_backward_mixed(const JoinArgs&, int, bool, bool, uint32_t, hipStream_t) { return SHAMPOO_EHIP; }
 }  // namespace shp
 
 int main() {
