@@ -156,13 +156,15 @@ struct Places {
   __device__ __forceinline__ Places(const JoinArgs& A, uint32_t which) : cols(A.cols), width(A.waves * kWave), lane(which) {}
   __device__ __forceinline__ uint32_t col(int p) const { return (p * width + lane) * V; }
 
-  // ONCE: it is read once.
+  // ONCE: it is read once, and where rows begin at a line's start or near it, its lines by one
+  // wave each: past the caches.  Elsewhere two waves share a line, which would come twice
+  // (2050 bf16 columns: norm 45 us that way, 34 through the caches).
   template <bool BF16, bool ONCE = true>
   __device__ __forceinline__ Piece<BF16, V> load(const void* row, int p) const {
     Piece<BF16, V> x;
     if (WHOLE || cols >= V) {
       const uint32_t from = min(col(p), cols - V);
-      if constexpr (ONCE) {
+      if constexpr (ONCE && WHOLE) {
         x.load_once(row, from);
       } else {
         x.load_at(row, from);

@@ -38,19 +38,20 @@ int with_pieces(int pieces, F&& f) {
 // Workgroups of the backward kernel: rows that one holds side by side, and how
 // many the compute units hold.  16 waves' worth of rows, so that there are few
 // partial sums, or 4 where a lane needs more registers than 16 waves leave it
-// (`many`: a join of 8 bf16 elements a lane with biases, 146, of which 12 waves fit a unit).  Joins and norms of
+// (`many`: a join of 8 bf16 elements a lane with biases, 146, of which 12 waves fit a unit; of 4 fp32 elements
+// a lane 20 do).  Joins and norms of
 // 2^25 bf16 elements, us with 16, 8 and 4 waves: rows of 512 66, 67, - and 34, 35, -;
 // of 2048 73, 72, 78 and 37, 38, 38; 1000 rows of 2048 14, 16, - and 10, 12, -.
 struct BackGrid {
   uint32_t lanes;
   int64_t resident;
 };
-inline BackGrid back_grid(const RowLayout& layout, bool many) {
+inline BackGrid back_grid(const RowLayout& layout, int V, bool many) {
   many = many && layout.pieces == 1 && layout.waves <= kMaxWaves / 2;
   const uint32_t all = many ? 4 : kMaxWaves;
   BackGrid g;
   g.lanes = layout.waves < all ? all / layout.waves : 1;
-  g.resident = 256 * std::max<uint32_t>(1, (many ? 12 : kMaxWaves) / (layout.waves * g.lanes));
+  g.resident = 256 * std::max<uint32_t>(1, (many ? 12 : V == 4 && layout.pieces == 1 ? 20 : kMaxWaves) / (layout.waves * g.lanes));
   return g;
 }
 
