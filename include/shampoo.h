@@ -585,7 +585,8 @@ enum {
 
 /* N(x) = (x - mean) s w + b over each row: RMS: mean = 0, s = 1 / sqrt(mean of
  * x^2 + eps); layer: s = 1 / sqrt(variance + eps).  Vectors of `cols` elements,
- * NULL: w = 1, b = 0. */
+ * NULL: w = 1, b = 0.  In fp32: a row whose squares overflow it (elements from
+ * about 2^60) has s = 0. */
 typedef struct shampoo_norm {
   int64_t kind;
   double eps;              /* > 0; as fp32 */
@@ -620,8 +621,8 @@ typedef struct shampoo_join {
   const void* gate;
   int64_t gate_dtype, gate_rows;
   /* Kept for the backward pass: MX8 copies of the inputs (all NULL: backward
-   * is given the inputs themselves), and fp32 [rows][2] mean and s of each norm
-   * (NULL in a forward pass without a backward one). */
+   * is given the inputs themselves), and fp32 [rows][2] mean and s of each norm,
+   * 8-byte aligned (NULL in a forward pass without a backward one). */
   uint8_t *residual_codes, *residual_scales, *branch_codes, *branch_scales;
   float *after_stats, *before_stats;
 } shampoo_join;

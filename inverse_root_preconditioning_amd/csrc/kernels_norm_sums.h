@@ -83,20 +83,20 @@ __global__ void __launch_bounds__(kSumCols * kSumLanes) join_sums_kernel(const S
   }
 }
 
-// The gate's rows where each has few pieces: an element a thread.
+// The gate's rows where each has few pieces: a column a thread, blockIdx.y the first of the rows that it takes.
 __global__ void __launch_bounds__(256) join_gate_kernel(const SumArgs S) {
-  const int64_t total = S.groups * S.cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t g = i / S.cols, col = i - g * S.cols;
-    const float w = S.after.w != nullptr ? param_at(S.after.w, S.after.w_bf16, col) : 1.f;
-    const float b = S.pb != nullptr && S.after.b != nullptr ? param_at(S.after.b, S.after.b_bf16, col) : 0.f;
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (col >= S.cols) return;
+  const float w = S.after.w != nullptr ? param_at(S.after.w, S.after.w_bf16, col) : 1.f;
+  const float b = S.pb != nullptr && S.after.b != nullptr ? param_at(S.after.b, S.after.b_bf16, col) : 0.f;
+  for (int64_t g = blockIdx.y; g < S.groups; g += gridDim.y) {
     float v = 0.f;
     for (uint32_t s = 0; s < S.per_group; ++s) {
       const int64_t at = (g * S.per_group + s) * S.pitch + col;
       v = __builtin_fmaf(w, ldg(S.pa + at), v);
       if (S.pb != nullptr) v = __builtin_fmaf(b, ldg(S.pb + at), v);
     }
-    store_param(S.dgate, S.dgate_bf16, i, v);
+    store_param(S.dgate, S.dgate_bf16, g * S.cols + col, v);
   }
 }
 

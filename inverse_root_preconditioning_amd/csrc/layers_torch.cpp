@@ -304,7 +304,8 @@ Kept join_forward(const JoinState& s, Inputs in, bool keep) {
   if (s.join) k.h = at::empty(s.shape, residual.options());
   if (n2) k.u = at::empty(s.shape, residual.options().dtype(s.branch_type));
   if (keep) {
-    if (n1 || n2) k.stats = at::empty({((int)n1 + (int)n2) * j.rows, 2}, residual.options().dtype(at::kFloat));
+    // as bytes: what rounds saved tensors of floating point leaves them alone
+    if (n1 || n2) k.stats = at::empty({((int)n1 + (int)n2) * j.rows * 8}, residual.options().dtype(at::kByte));
     if (s.low && (s.keep_r || s.keep_y))
       k.buf = at::empty({((int)s.keep_r + (int)s.keep_y) * mx8_bytes(j.rows, j.cols)}, residual.options().dtype(at::kByte));
   }

@@ -121,6 +121,8 @@ int common(const shampoo_join* j, JoinArgs* a, bool* empty) {
   a->flags = norm_flags(j->after.kind, kJoinNorm1, kJoinMean1) | norm_flags(j->before.kind, kJoinNorm2, kJoinMean2);
   if (j->gate_kind == SHAMPOO_GATE_ROWS) a->flags |= kJoinRuns;
   if (j->gate_kind == SHAMPOO_GATE_TOKEN) a->flags |= kJoinToken;
+  if ((reinterpret_cast<uintptr_t>(j->after_stats) & 7) != 0 || (reinterpret_cast<uintptr_t>(j->before_stats) & 7) != 0)
+    return SHAMPOO_EINVAL;
   a->stats1 = j->after_stats;
   a->stats2 = j->before_stats;
   return SHAMPOO_OK;
@@ -291,12 +293,12 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
     m.dgate = g->d_gate;
     m.dgate_bf16 = a.gate_bf16;
     m.groups = s.groups;
-    // Rows with some pieces each are summed like the jobs, beside them; else an element a thread.
+    // Rows with some pieces each are summed like the jobs, beside them; else by a thread an element.
     if (s.per_group > 4 && s.groups <= 1024) {
       rows_y += s.groups;
     } else {
-      const int64_t elems = s.groups * cols;
-      hipLaunchKernelGGL(join_gate_kernel, dim3((uint32_t)std::min<int64_t>((elems + 255) / 256, 8192)), dim3(256), 0,
+      hipLaunchKernelGGL(join_gate_kernel,
+                         dim3((uint32_t)((cols + 255) / 256), (uint32_t)std::min<int64_t>(s.groups, 4096)), dim3(256), 0,
                          stream, m);
       if ((rc = check_launch()) != SHAMPOO_OK) return rc;
     }

@@ -5,12 +5,10 @@ arithmetic runs in the HIP library (see capi and include/shampoo.h).
 
     q = quantize(x)                  # 1.03 bytes an element
     x = dequantize(q, x.dtype)       # within 2^-4 of each element, or 2^-18 of the largest of its 32
-    with saved_tensors():            # what any torch operation keeps inside is kept so
+    with saved_tensors():            # what torch's own operations keep of bfloat16 inside is kept so
         y = block(x)
 """
 from __future__ import annotations
-
-import math
 
 import torch
 
@@ -127,15 +125,22 @@ def dequantize(q, dtype=torch.float32, stream=None):
     return out
 
 
-def saved_tensors(min_elements=1 << 14):
-    """A context in which autograd keeps activations in MX8: every float32 or
-    bfloat16 CUDA tensor of at least `min_elements` that an operation inside
-    saves for its backward pass, but for leaves that require a gradient
+def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
+    """A context in which autograd keeps activations in MX8: every CUDA tensor of
+    `dtypes` (bfloat16, float32) and at least `min_elements` that an operation
+    inside saves for its backward pass, but for leaves that require a gradient
     (parameters) and views of them.  Backward then computes from the rounded values.
-    The operations of mx4 and layers save integers or are told by themselves
-    what to keep (keep=); their inputs are rounded like any others."""
+
+    float32 is not rounded unless asked for, since operations on bfloat16 keep
+    statistics in it (a norm's, the logarithms of an attention's sums) whose
+    rounding would spoil their gradients.  For the same reason a loss belongs outside: what it keeps
+    is a logarithm.  The operations of mx4 and layers keep integers, or with
+    keep="same" their inputs, which are rounded like any others."""
+    if not set(dtypes) <= set(_TYPES):
+        raise ValueError("dtypes are of float32 and bfloat16")
+
     def pack(t):
-        if t.dtype not in _TYPES or not t.is_cuda or t.numel() < max(min_elements, 1):
+        if t.dtype not in dtypes or not t.is_cuda or t.numel() < max(min_elements, 1):
             return t
         base = t if t._base is None else t._base
         if base.requires_grad and base.is_leaf or t.layout != torch.strided:

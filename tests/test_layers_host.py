@@ -137,7 +137,7 @@ def test_join_does_not_support(bad):
     dict(y=FAKE, gate=(f.GATE_TOKEN, 0, 0, 0)), dict(y=FAKE, scale=INF), dict(y=FAKE, scale=1e300), dict(residual=0),
     dict(ld=63, ldh=64, ldu=64), dict(y=FAKE, ldy=63), dict(y=FAKE, h=0), dict(u=0), dict(ldu=63), dict(y=FAKE, ldh=63),
     dict(kept=(FAKE, 0, 0, 0)), dict(kept=(0, FAKE, 0, 0)), dict(kept=(FAKE + 8, FAKE, 0, 0)), dict(kept=(0, 0, FAKE, FAKE)),
-    dict(y=FAKE, kept=(0, 0, FAKE, 0)),
+    dict(y=FAKE, kept=(0, 0, FAKE, 0)), dict(stats=(0, FAKE + 4)), dict(y=FAKE, after=RMS, stats=(FAKE + 4, FAKE)),
 ])
 def test_join_refuses(bad):
     assert _join(**bad) == f.EINVAL

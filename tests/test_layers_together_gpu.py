@@ -262,12 +262,20 @@ def test_gradients_of_gradients_and_tangents_are_refused():
                 f(dual)
 
 
-def test_inside_saved_tensors():
-    """Layers that keep their inputs take them rounded, as with keep="mx8"."""
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_inside_saved_tensors(dtype):
+    """Layers that keep their inputs take them rounded, as with keep="mx8"; row statistics are left alone."""
     gen = torch.Generator(device="cuda").manual_seed(8)
-    x = normal(gen, 100, 256).requires_grad_()
-    dy = normal(gen, 100, 256)
-    with M8.saved_tensors(min_elements=1000):
-        y = L.activation(x * 1.0, act="gelu")
-    got = torch.autograd.grad(y, x, dy)[0]
-    assert torch.equal(got, torch.autograd.grad(L.activation(x * 1.0, act="gelu", keep="mx8"), x, dy)[0])
+    x, r = normal(gen, 300, 256, dtype=dtype).requires_grad_(), normal(gen, 300, 256, dtype=dtype).requires_grad_()
+    dy = normal(gen, 300, 256, dtype=dtype)
+    n = L.Norm("layer", (1 + normal(gen, 256, std=0.1)).requires_grad_())
+
+    def step(keep):
+        y = L.activation(x * 1.0, act="gelu", keep=keep)
+        h, u = L.join(r * 1.0, y, n, None, 1.0, n, keep)
+        return L.norm(h, n, keep=keep) + u
+    want = torch.autograd.grad(step("mx8"), (x, r, n.weight), dy)
+    with M8.saved_tensors(min_elements=512, dtypes=(dtype,)):
+        out = step("same")
+    got = torch.autograd.grad(out, (x, r, n.weight), dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

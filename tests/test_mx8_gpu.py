@@ -139,7 +139,7 @@ def test_saved_tensors_are_kept_in_8_bits():
     x = torch.randn(96, 200, generator=gen, device="cuda")
     w = torch.randn(300, 200, generator=gen, device="cuda", requires_grad=True)
     xg = x.clone().requires_grad_()
-    with M8.saved_tensors(min_elements=64):
+    with M8.saved_tensors(min_elements=64, dtypes=(torch.float32,)):
         h = xg * 1.0
         before = torch.cuda.memory_allocated()
         y = torch.sin(h)
@@ -159,6 +159,12 @@ def test_saved_tensors_are_kept_in_8_bits():
             y = torch.sin(t * 1)
         assert torch.autograd.grad(y.sum(), t)[0].shape == t.shape
     small = torch.randn(10, generator=gen, device="cuda", requires_grad=True)
-    with M8.saved_tensors():
+    with M8.saved_tensors(dtypes=(torch.float32, torch.bfloat16)):
         y = torch.sin(small * 1)
     assert torch.equal(torch.autograd.grad(y.sum(), small)[0], torch.cos(small.detach()))
+    # float32 stays as it is unless asked for
+    with M8.saved_tensors(min_elements=64):
+        y = torch.sin(xg * 1.0)
+    assert torch.equal(torch.autograd.grad(y, xg, torch.ones_like(y))[0], torch.cos(x))
+    with pytest.raises(ValueError):
+        M8.saved_tensors(dtypes=(torch.float16,))
