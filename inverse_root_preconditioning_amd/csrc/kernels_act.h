@@ -33,7 +33,7 @@ template <int ACT, bool SLOPE, bool FINE>
 __device__ __forceinline__ void activation(float x, float& f, float& d) {
   if constexpr (ACT == SHAMPOO_ACT_RELU) {
     f = x < 0.f ? 0.f : x;
-    if (SLOPE) d = x > 0.f ? 1.f : 0.f;
+    if (SLOPE) d = x > 0.f ? 1.f : x <= 0.f ? 0.f : x;  // NaN stays: a kept group of NaN is no row of zeros
   } else if constexpr (ACT == SHAMPOO_ACT_RELU2) {
     const float r = x < 0.f ? 0.f : x;
     f = r * r;

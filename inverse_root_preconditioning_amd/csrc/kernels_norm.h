@@ -179,7 +179,7 @@ struct Places {
     if constexpr (WHOLE) {
       if (col(p) >= cols) x.w = 0u;
     } else if (cols >= V) {
-      const uint32_t over = col(p) + V;  // (cols - V itself is above 2^31 for no columns)
+      const uint32_t over = col(p) + V;
       if (over > cols) x.shift_down(min(over - cols, (uint32_t)V));
     }
   }
@@ -266,6 +266,7 @@ struct Parameters {
     }
   }
 };
+
 __device__ __forceinline__ float load_token(const JoinArgs& A, int64_t row) {
   if (A.gate_bf16) return __builtin_bit_cast(float, (uint32_t)ldg(static_cast<const uint16_t*>(A.gate) + row) << 16);
   return ldg(static_cast<const float*>(A.gate) + row);

@@ -16,6 +16,8 @@ from . import capi
 from .adamw import _TYPES, _current_device, _on_stream, _raw_stream
 from .mx4 import _matrix
 
+_MAX_COLS = 1 << 29                  # of a matrix of the library
+
 
 def _padded(cols):
     return (cols + 31) & -32         # capi.GROUP
@@ -93,6 +95,8 @@ def quantize(x, stream=None):
     if stream is not None:
         return _on_stream(stream, x.device, lambda: quantize(x), x)
     dtype, ld = _matrix(x, "x")
+    if x.is_neg():                   # a view that negates what is in memory
+        return quantize(x.resolve_neg())
     index = x.device.index
     if index != _current_device():
         with torch.cuda.device(index):
@@ -133,9 +137,10 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
 
     float32 is not rounded unless asked for, since operations on bfloat16 keep
     statistics in it (a norm's, the logarithms of an attention's sums) whose
-    rounding would spoil their gradients.  For the same reason a loss belongs outside: what it keeps
-    is a logarithm.  The operations of mx4 and layers keep integers, or with
-    keep="same" their inputs, which are rounded like any others."""
+    rounding would spoil their gradients.  For the same reason a loss belongs
+    outside: what it keeps is a logarithm.  The operations of mx4 and layers keep
+    integers, or with keep="same" their inputs, which are rounded like any others.
+    Columns are the last dimension, with those before it where it is short."""
     if not set(dtypes) <= set(_TYPES):
         raise ValueError("dtypes are of float32 and bfloat16")
 
@@ -145,10 +150,14 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
         base = t if t._base is None else t._base
         if base.requires_grad and base.is_leaf or t.layout != torch.strided:
             return t
-        t = t.detach()
-        # a row shorter than two groups would be mostly padding
-        flat = t.reshape(-1, t.shape[-1]) if t.dim() and t.shape[-1] >= 2 * capi.GROUP else t.reshape(1, -1)
-        return quantize(flat.contiguous()), t.dtype, t.shape
+        # rows of less than two groups would be mostly padding; a vector is one row
+        k, cols = t.dim(), 1
+        while k and (k == t.dim() or cols < 2 * capi.GROUP and cols % capi.GROUP):
+            k -= 1
+            cols *= t.shape[k]
+        if cols > _MAX_COLS:
+            return t
+        return quantize(t.detach().reshape(-1, cols).contiguous()), t.dtype, t.shape
 
     def unpack(kept):
         if isinstance(kept, torch.Tensor):

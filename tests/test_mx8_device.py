@@ -17,6 +17,9 @@ class Tensor(D.Tensor):
     def contiguous(self):
         return self
 
+    def is_neg(self):
+        return False
+
     def element_size(self):
         return 4
 

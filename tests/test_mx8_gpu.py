@@ -168,3 +168,36 @@ def test_saved_tensors_are_kept_in_8_bits():
     assert torch.equal(torch.autograd.grad(y, xg, torch.ones_like(y))[0], torch.cos(x))
     with pytest.raises(ValueError):
         M8.saved_tensors(dtypes=(torch.float16,))
+
+
+@pytest.mark.parametrize("shape", [(30, 8, 40), (1 << 13, 32), (7, 11, 3, 5), (2000, 1), (96, 200)])
+def test_saved_tensors_rows(shape):
+    """Short last dimensions are joined with those before them, as one matrix: x itself, of x^2's gradient 2 x dy."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16).requires_grad_()
+    h = x * 1
+    before = torch.cuda.memory_allocated()
+    with M8.saved_tensors(min_elements=64):
+        y = h * h
+    held = torch.cuda.memory_allocated() - before - 2 * y.numel()
+    cols = {(30, 8, 40): 320, (1 << 13, 32): 32, (7, 11, 3, 5): 165, (2000, 1): 2000, (96, 200): 200}[shape]
+    # both factors' copies, each allocation rounded up to 512 bytes, as is y's
+    assert held <= 2 * (x.numel() // cols * (cols + 31) // 32 * 33 + 512) + 512
+    want = 2 * M8.dequantize(M8.quantize(x.detach().reshape(-1, cols)), torch.bfloat16).view(shape)
+    assert torch.equal(torch.autograd.grad(y, x, torch.ones_like(y))[0], want)
+    n = torch.complex(h.detach().float(), h.detach().float()).requires_grad_()
+    m = (n * 1).conj().imag          # a view that negates what is in memory
+    assert m.is_neg()
+    with M8.saved_tensors(min_elements=64, dtypes=(torch.float32,)):
+        y = m * m
+    got = torch.autograd.grad(y, n, torch.ones_like(y))[0].imag
+    assert torch.equal(got, 2 * M8.dequantize(M8.quantize(h.detach().float().reshape(-1, cols))).view(shape))
+
+
+def test_saved_tensors_leave_what_a_matrix_cannot_hold():
+    """Vectors of more than 2^29 elements stay as they are."""
+    x = torch.ones((1 << 29) + 1, dtype=torch.bfloat16, device="cuda").requires_grad_()
+    h = x * 3
+    with M8.saved_tensors():
+        y = h * h
+    assert torch.equal(torch.autograd.grad(y.sum(), x)[0][-2:].float(), torch.full((2,), 18.0, device="cuda"))
