@@ -2,6 +2,7 @@
 gated activation, linear and join; graphs, streams, checkpoints and what is held
 until the backward pass."""
 import gc
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -183,6 +184,77 @@ def test_a_captured_training_step_replays():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+def test_a_captured_backward_pass_beside_an_eager_graph_is_refused():
+    """The leaf's gradient would go to a node on the eager graph's stream; freed, the capture works."""
+    x = torch.randn(40, 64, device="cuda", requires_grad=True)
+    n = L.Norm("rms", torch.ones(64, device="cuda", requires_grad=True))
+    for f in (lambda: L.activation(x, keep="mx8"), lambda: L.norm(x, n, keep="mx8")):
+        eager = f()
+        dy = torch.ones_like(eager)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            y = f()
+            with pytest.raises(RuntimeError, match="before the capture"):
+                torch.autograd.grad(y, x, dy)
+        want = torch.autograd.grad(eager, x, dy)[0]
+        del eager, y
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = torch.autograd.grad(f(), x, dy)[0]
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_two_captured_graphs_in_turn():
+    """Each has its own workspace: replays of one leave the other's results alone."""
+    net = Blocks(64, 96)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    xs = [normal(gen, rows, 64, dtype=BF16) for rows in (40, 33)]
+    dus = [normal(gen, rows, 64, dtype=BF16) for rows in (40, 33)]
+
+    def step(t, du):
+        t = t.detach().requires_grad_()
+        return torch.autograd.grad(net.forward(t, "mx8"), [t] + net.parameters(), du)
+    want = [step(x, du) for x, du in zip(xs, dus)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, du in zip(xs, dus):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(x, du))
+    for turn in range(3):
+        for g in graphs:
+            g.replay()
+        step(xs[turn % 2], dus[turn % 2])
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+def test_two_threads_at_once():
+    net = Blocks(64, 96)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    xs = [normal(gen, 40 + 7 * i, 64, dtype=BF16) for i in range(4)]
+
+    def step(t):
+        t = t.detach().requires_grad_()
+        u = net.forward(t, "mx8")
+        return torch.autograd.grad(u, [t] + net.parameters(), torch.ones_like(u))
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got = step(xs[i])
+            torch.cuda.current_stream().synchronize()
+        return all(torch.equal(a, b) for a, b in zip(got, want[i]))
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(run, range(4)))
 
 
 def test_on_a_side_stream():
