@@ -12,11 +12,14 @@ using namespace shp;
 namespace {
 
 // Rows that a workgroup of the forward kernel takes in turn, where that leaves
-// one for every compute unit: enough that the parameters' loads do not count
+// as many as are resident: enough that the parameters' loads do not count
 // and a row's loads overlap the row before, few enough that the workgroups end
 // together.  Joins of 2^25 bf16 elements with 8-bit copies, us by turns:
 // rows of 512:  1: 70, 2: 63, 4: 64;   of 2050 (5 waves)  2: 110, 4: 99, 8: 100;
 // of 5120 (10):  5: 78, 8: 83, 9: 71, 10: 76;   of 8192 (16):  1: 97, 4: 68, 8: 65, 12: 80.
+// Fewer rows, a join and a norm, us with workgroups for one a compute unit and for 16 waves a unit:
+// 1001 rows of 1537 fp32 11.7, 6.1 and 9.8, 5.3;  of 700 of 4096 bf16 8.1, 5.2 and 7.3, 4.6;  of 500 of
+// 8192 fp32 (16 waves a row, 512 workgroups instead of 256) 12.3, 7.3 and 16.8, 7.5.
 int64_t turns(uint32_t waves) { return std::min<int64_t>(std::max<int64_t>(waves - 1, 3), 8); }
 
 template <bool SB, bool BB>
@@ -26,8 +29,8 @@ int forward(JoinArgs a, hipStream_t stream) {
   a.waves = layout.waves;
   a.lanes = a.waves == 1 ? 4 : 1;
   const int64_t rows = (a.rows + a.lanes - 1) / a.lanes, each = turns(a.waves);
-  const int64_t blocks =
-      std::min<int64_t>(std::max<int64_t>((rows + each - 1) / each, std::min<int64_t>(rows, 256)), kMaxThreads / 1024);
+  const int64_t resident = 256 * (kMaxWaves / (a.waves * a.lanes));
+  const int64_t blocks = std::min(std::max((rows + each - 1) / each, std::min(rows, resident)), kMaxThreads / 1024);
   const dim3 grid((uint32_t)blocks), block(kWave * a.waves * a.lanes);
   const bool whole = a.cols % V == 0;
   return with_pieces<V>(layout.pieces, [&](auto p) {
