@@ -496,8 +496,9 @@ struct Kept {
 };
 
 // FEW: 8 waves a workgroup at most, with twice the registers.
+constexpr int kFewWaves = 8;
 template <bool SB, bool BB, int P, bool JOIN, bool KEEP, bool BIAS, bool FEW, bool WHOLE>
-__global__ void __launch_bounds__(kWave * (FEW ? kMaxWaves / 2 : kMaxWaves)) join_backward_kernel(const JoinArgs A) {
+__global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_backward_kernel(const JoinArgs A) {
   constexpr int V = SB ? 8 : 4;
   typedef Places<P, V, WHOLE> At;
   // Parameters in registers and the next row's loads in flight, where there are registers for
