@@ -109,6 +109,11 @@ struct Mx8Args {
   RowShape shape;
 };
 
+// Bound by HBM: each element is read once, each code written once.  Lanes hold
+// consecutive pieces of 16 bytes, so that a group is 4 (bf16) or 8 (fp32) lanes, whose
+// largest magnitude is found by DPP without LDS; 4 rows a thread keep 4 loads in
+// flight.  16384 x 8192 bf16: 70 us to codes and 65 back, 5.8 and 6.2 TB/s; with
+// stores through the caches 155 us for both.
 constexpr int kMx8Passes = 4;  // rows a thread takes
 
 template <bool BF16>

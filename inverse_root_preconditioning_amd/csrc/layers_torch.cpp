@@ -2,8 +2,9 @@
 // nodes and the calls of the C ABI (include/shampoo.h).  In C++ because a small
 // layer's time is the host's: autograd runs a backward pass on a thread of its
 // own, where Python costs twice what it does on the caller's.  Forward and
-// backward of 1001 x 1537 fp32 elements, host-bound, with nodes in Python -> here:
-// activation 87 -> 47 us, LayerNorm 137 -> 62, join 200 -> 78.
+// backward of small fp32 matrices, bound by the host, with nodes in Python -> here:
+// 1001 x 1537 activation 87 -> 43 us (torch's own silu takes 41), 333 x 1001 LayerNorm
+// 137 -> 51 to 65, 1001 x 1537 join 200 -> 106, of which its kernels take 37.
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
