@@ -434,21 +434,61 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const J
 // workgroup, then go to memory for join_sums_kernel: no atomics, a fixed order.
 // Bound by HBM: 16384 rows of 2048 bf16 from 8-bit copies 70 us as a join (4.8
 // TB/s) and 35 as a norm (4.9); with biases (layer norms) 78, by registers: the four sums of a column,
-// its parameters and the row leave 12 waves a compute unit.  Rows of more than 8192 columns
-// hold 16 elements a lane, which 128 registers do not: 2048 rows of 16384 as a join take 207 us, in scratch memory.
+// its parameters and the row leave 12 waves a compute unit.  Rows of more than
+// 8192 columns are 16 elements a lane, which 128 registers hold only without the sums: 2048 rows of 16384 bf16 as a
+// join 98 us with two of those in LDS, 216 without; with biases (two more) 274, in scratch memory.
 // ---------------------------------------------------------------------------
 
+// A lane's sums over its columns: in registers, or its own places in LDS.
+template <int P, int V, bool IN_LDS>
+struct ColumnSums {
+  static constexpr int kFloats = IN_LDS ? P * V * kWave * kMaxWaves : 0;  // of a workgroup
+  float v[IN_LDS ? 1 : P][V];
+  floatx4* at;
+  __device__ __forceinline__ explicit ColumnSums(float* lds) : at(reinterpret_cast<floatx4*>(lds) + threadIdx.x) {}
+  __device__ __forceinline__ void clear() {
+    const float zero[V] = {};
+#pragma unroll
+    for (int p = 0; p < P; ++p) put(p, zero);
+  }
+  __device__ __forceinline__ void get(int p, float (&x)[V]) const {
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const floatx4 q = at[(p * (V / 4) + i) * kWave * kMaxWaves];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * i + e] = q[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = v[p][e];
+    }
+  }
+  __device__ __forceinline__ void put(int p, const float (&x)[V]) {
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        at[(p * (V / 4) + i) * kWave * kMaxWaves] = floatx4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[p][e] = x[e];
+    }
+  }
+};
+
 // A lane's sums, added over the rows held side by side, to a row of partial sums.
-template <int P, int V>
-__device__ __forceinline__ void store_sums(const float (&acc)[P][V], float* to, const JoinArgs& A, uint32_t lane,
-                                           uint32_t part, float* lds) {
+template <int P, int V, bool IN_LDS>
+__device__ __forceinline__ void store_sums(const ColumnSums<P, V, IN_LDS>& sums, float* to, const JoinArgs& A,
+                                           uint32_t lane, uint32_t part, float* lds) {
   const uint32_t cols = A.waves * kWave * V;  // of a piece
 #pragma unroll
   for (int p = 0; p < P; ++p) {
+    float acc[V];
+    sums.get(p, acc);
     floatx4 q[V / 4];
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) q[i] = floatx4{acc[p][4 * i], acc[p][4 * i + 1], acc[p][4 * i + 2], acc[p][4 * i + 3]};
-    if (A.lanes == 1) {
+    for (int i = 0; i < V / 4; ++i) q[i] = floatx4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+    if (IN_LDS || A.lanes == 1) {
       const uint32_t col = p * cols + lane * V;
       if (col < A.pitch) {
 #pragma unroll
@@ -514,7 +554,12 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
   // them: 128 in a workgroup of 16 waves.  (4096 rows of 16384 without this rule: 690 us, in scratch memory.)
   constexpr bool kAhead = P * V <= (FEW || !(JOIN && BIAS) ? 8 : 4);
   __shared__ __attribute__((aligned(16))) float red[kMaxWaves * kSumsFloats];
-  __shared__ __attribute__((aligned(16))) float lds[kMaxWaves * kWave * V];  // the columns' sums of lanes x waves
+  // 16 elements a lane: the sums for w2 and w1 (or the gate) in LDS, 128 KB of its 160.  It is read and written
+  // once a row, by every lane at its own place: no barrier, and 1 us of the 12 that such a row takes a compute unit.
+  constexpr bool kInLds = JOIN && P * V == 16;
+  typedef ColumnSums<P, V, kInLds> LdsSums;
+  // the columns' sums of lanes x waves, where a workgroup has several rows; else those of every lane
+  __shared__ __attribute__((aligned(16))) float lds[kInLds ? 2 * LdsSums::kFloats : kMaxWaves * kWave * V];
   const uint32_t L = A.lanes;
   const uint32_t part = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / A.waves);
   const uint32_t lane0 = threadIdx.x - part * A.waves * kWave;
@@ -554,7 +599,10 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
   Parameters<P, V, WHOLE, BIAS, kAhead> n1;
   Parameters<P, V, WHOLE, false, kAhead> n2;
   n2.keep(At(A, lane0), A, A.before, false, 0);
-  float aw[P][V] = {}, ac[P][V] = {}, aa[P][V], ab[P][V];
+  LdsSums aw(lds), aa(lds + LdsSums::kFloats);
+  ColumnSums<P, V, false> ac(nullptr), ab(nullptr);
+  aw.clear();
+  ac.clear();
   for (uint32_t piece = begin; piece < end; ++piece) {
     const uint32_t group = __builtin_amdgcn_readfirstlane(piece / A.per_group);
     // every per_group-th set of L rows of the run: workgroups side by side read side by side
@@ -566,10 +614,8 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
       if constexpr (JOIN) n1.keep(at, A, A.after, A.flags & kJoinRuns, group);
     }
     if constexpr (JOIN) {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int e = 0; e < V; ++e) aa[p][e] = ab[p][e] = 0.f;
+      aa.clear();
+      ab.clear();
     }
     for (int64_t base = row0; base < row1; base += step) {
       const int64_t row = base + part;
@@ -635,15 +681,18 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
             }
           }
           n2.get(at, A, A.before, false, p, w, b);
+          float sw[V];
+          aw.get(p, sw);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             hn[p][e] = __builtin_fmaf(hn[p][e], s2, c2);
             const float d = elem(du[p], e);
             gu[p][e] = d * w[e];
-            aw[p][e] = __builtin_fmaf(d, hn[p][e], aw[p][e]);
-            if constexpr (BIAS) ac[p][e] += d;
+            sw[e] = __builtin_fmaf(d, hn[p][e], sw[e]);
+            if constexpr (BIAS) ac.v[p][e] += d;
             t[0] = __builtin_fmaf(gu[p][e], hn[p][e], t[0]);
           }
+          aw.put(p, sw);
           if (flags & kJoinMean2) {
 #pragma unroll
             for (int e = 0; e < V; ++e) t[1] += gu[p][e];
@@ -693,13 +742,16 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
               dt[p][e] *= token;
             }
           }
+          float sa[V];
+          aa.get(p, sa);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            aa[p][e] = __builtin_fmaf(dt[p][e], yn[p][e], aa[p][e]);
-            if constexpr (BIAS) ab[p][e] += dt[p][e];
+            sa[e] = __builtin_fmaf(dt[p][e], yn[p][e], sa[e]);
+            if constexpr (BIAS) ab.v[p][e] += dt[p][e];
             dt[p][e] *= w[e];  // dz w
             t[0] = __builtin_fmaf(dt[p][e], yn[p][e], t[0]);
           }
+          aa.put(p, sa);
           if (flags & kJoinMean1) {
 #pragma unroll
             for (int e = 0; e < V; ++e) t[1] += dt[p][e];
@@ -735,16 +787,16 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
       }
     }
     if constexpr (JOIN) {
-      if (A.pa != nullptr) store_sums<P, V>(aa, A.pa + piece * (int64_t)A.pitch, A, lane0, part, lds);
+      if (A.pa != nullptr) store_sums(aa, A.pa + piece * (int64_t)A.pitch, A, lane0, part, lds);
       if constexpr (BIAS) {
-        if (A.pb != nullptr) store_sums<P, V>(ab, A.pb + piece * (int64_t)A.pitch, A, lane0, part, lds);
+        if (A.pb != nullptr) store_sums(ab, A.pb + piece * (int64_t)A.pitch, A, lane0, part, lds);
       }
     }
   }
   if (A.flags & kJoinNorm2) {
-    if (A.pw != nullptr) store_sums<P, V>(aw, A.pw + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
+    if (A.pw != nullptr) store_sums(aw, A.pw + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
     if constexpr (BIAS) {
-      if (A.pc != nullptr) store_sums<P, V>(ac, A.pc + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
+      if (A.pc != nullptr) store_sums(ac, A.pc + blockIdx.x * (int64_t)A.pitch, A, lane0, part, lds);
     }
   }
 }

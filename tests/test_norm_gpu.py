@@ -155,6 +155,18 @@ def test_sums_over_many_rows(gate, seqs, length, keep):
     _check_join(case, keep, 0.5, normal(gen, seqs, length, 48), normal(gen, seqs, length, 48))
 
 
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "mixed", "bf16"])
+@pytest.mark.parametrize("gate,seqs,length,cols", [("channel", 1, 700, 9000), ("sequence", 2, 280, 8203),
+                                                   ("row", 30, 20, 9001), (None, 3, 180, 16384)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_sums_of_wide_rows(types, gate, seqs, length, cols, bias):
+    """Workgroups that take some rows each of more than 8192 columns."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    case = _join_case(gen, seqs, length, cols, "rms", "layer", gate, bias, types, F32)
+    _check_join(case, "mx8" if seqs % 2 else "same", 1.0, normal(gen, seqs, length, cols, dtype=types[0]),
+                normal(gen, seqs, length, cols, dtype=types[1]))
+
+
 @pytest.mark.parametrize("given", ["h", "u"])
 @pytest.mark.parametrize("keep", ["same", "mx8"])
 def test_a_gradient_of_one_output_only(given, keep):
