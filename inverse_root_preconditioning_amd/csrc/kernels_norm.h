@@ -433,10 +433,11 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const J
 // taken of the gated dt.  Columns' sums stay in registers over all rows of a
 // workgroup, then go to memory for join_sums_kernel: no atomics, a fixed order.
 // Bound by HBM: 16384 rows of 2048 bf16 from 8-bit copies 70 us as a join (4.8
-// TB/s) and 35 as a norm (4.9); with biases (layer norms) 78, by registers: the four sums of a column,
-// its parameters and the row leave 12 waves a compute unit.  Rows of more than
-// 8192 columns are 16 elements a lane, which 128 registers hold only without the sums: 2048 rows of 16384 bf16 as a
-// join 98 us with two of those in LDS, 216 without; with biases (two more) 274, in scratch memory.
+// TB/s) and 35 as a norm (4.9).  128 registers a lane do not hold the row, the next
+// one's loads, the parameters and four sums a column (with biases), nor 16 elements a lane with two: then
+// the sums are in LDS.  Joins of 2^25 bf16 elements, us with the sums in registers (fewer waves, no
+// next row, or scratch memory) and in LDS: with biases rows of 2048 78, 80; 2050 159, 113; 5120 139, 97; 8192
+// 113, 81; without, of 16384 216, 98.  With biases those take 238: two of the four sums do not fit.
 // ---------------------------------------------------------------------------
 
 // A lane's sums over its columns: in registers, or its own places in LDS.
@@ -444,8 +445,14 @@ template <int P, int V, bool IN_LDS>
 struct ColumnSums {
   static constexpr int kFloats = IN_LDS ? P * V * kWave * kMaxWaves : 0;  // of a workgroup
   float v[IN_LDS ? 1 : P][V];
+  float* all;
   floatx4* at;
-  __device__ __forceinline__ explicit ColumnSums(float* lds) : at(reinterpret_cast<floatx4*>(lds) + threadIdx.x) {}
+  __device__ __forceinline__ explicit ColumnSums(float* lds)
+      : all(lds), at(reinterpret_cast<floatx4*>(lds) + threadIdx.x) {}
+  // Column c of the first piece, from the lanes of a row whose first is thread `from`.
+  __device__ __forceinline__ float column(uint32_t from, uint32_t c) const {
+    return all[(c % V / 4 * kWave * kMaxWaves + from + c / V) * 4 + c % 4];
+  }
   __device__ __forceinline__ void clear() {
     const float zero[V] = {};
 #pragma unroll
@@ -485,25 +492,23 @@ __device__ __forceinline__ void store_sums(const ColumnSums<P, V, IN_LDS>& sums,
   for (int p = 0; p < P; ++p) {
     float acc[V];
     sums.get(p, acc);
-    floatx4 q[V / 4];
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) q[i] = floatx4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
-    if (IN_LDS || A.lanes == 1) {
+    if (P > 1 || A.lanes == 1) {
       const uint32_t col = p * cols + lane * V;
       if (col < A.pitch) {
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) stg(reinterpret_cast<floatx4*>(to + col) + i, q[i]);
+        for (int i = 0; i < V / 4; ++i)
+          stg(reinterpret_cast<floatx4*>(to + col) + i, floatx4{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]});
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) reinterpret_cast<floatx4*>(lds + part * cols + lane * V)[i] = q[i];
+      // sums in LDS are added where they are
+      ColumnSums<1, V, true> there(IN_LDS ? sums.all : lds);
+      if constexpr (!IN_LDS) there.put(0, acc);
       __syncthreads();
       for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
-        const uint32_t col = p * cols + c;
-        if (col < A.pitch) {
-          float v = lds[c];
-          for (uint32_t i = 1; i < A.lanes; ++i) v += lds[i * cols + c];
-          stg(to + col, v);
+        if (c < A.pitch) {
+          float v = 0.f;
+          for (uint32_t i = 0; i < A.lanes; ++i) v += there.column(i * A.waves * kWave, c);
+          stg(to + c, v);
         }
       }
       __syncthreads();
@@ -544,22 +549,22 @@ struct Kept {
   }
 };
 
-// FEW: 8 waves a workgroup at most, with twice the registers.
-constexpr int kFewWaves = 8;
-template <bool SB, bool BB, int P, bool JOIN, bool KEEP, bool BIAS, bool FEW, bool WHOLE>
-__global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_backward_kernel(const JoinArgs A) {
+template <bool SB, bool BB, int P, bool JOIN, bool KEEP, bool BIAS, bool WHOLE>
+__global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const JoinArgs A) {
   constexpr int V = SB ? 8 : 4;
   typedef Places<P, V, WHOLE> At;
   // Parameters in registers and the next row's loads in flight, where there are registers for
   // them: 128 in a workgroup of 16 waves.  (4096 rows of 16384 without this rule: 690 us, in scratch memory.)
-  constexpr bool kAhead = P * V <= (FEW || !(JOIN && BIAS) ? 8 : 4);
+  constexpr bool kAhead = P * V <= 8;
   __shared__ __attribute__((aligned(16))) float red[kMaxWaves * kSumsFloats];
-  // 16 elements a lane: the sums for w2 and w1 (or the gate) in LDS, 128 KB of its 160.  It is read and written
-  // once a row, by every lane at its own place: no barrier, and 1 us of the 12 that such a row takes a compute unit.
-  constexpr bool kInLds = JOIN && P * V == 16;
-  typedef ColumnSums<P, V, kInLds> LdsSums;
-  // the columns' sums of lanes x waves, where a workgroup has several rows; else those of every lane
-  __shared__ __attribute__((aligned(16))) float lds[kInLds ? 2 * LdsSums::kFloats : kMaxWaves * kWave * V];
+  // Columns' sums in LDS where 128 registers do not hold them, 128 KB of its 160: those for w2 and w1 (or the
+  // gate) of 16 elements a lane, all four of 8 with biases.  Read and written once a row, by every
+  // lane at its own place: no barrier, and some 1 us of the 12 that such a row takes a compute unit.
+  constexpr bool kInLds = JOIN && (P * V == 16 || (BIAS && P * V == 8)), kAllInLds = kInLds && P * V == 8;
+  typedef ColumnSums<P, V, kInLds> SumsW;
+  typedef ColumnSums<P, V, kAllInLds> SumsB;
+  // those, or for registers one such array in which rows side by side meet
+  __shared__ __attribute__((aligned(16))) float lds[kInLds ? 2 * SumsW::kFloats + 2 * SumsB::kFloats : kMaxWaves * kWave * V];
   const uint32_t L = A.lanes;
   const uint32_t part = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / A.waves);
   const uint32_t lane0 = threadIdx.x - part * A.waves * kWave;
@@ -599,10 +604,10 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
   Parameters<P, V, WHOLE, BIAS, kAhead> n1;
   Parameters<P, V, WHOLE, false, kAhead> n2;
   n2.keep(At(A, lane0), A, A.before, false, 0);
-  LdsSums aw(lds), aa(lds + LdsSums::kFloats);
-  ColumnSums<P, V, false> ac(nullptr), ab(nullptr);
+  SumsW aw(lds), aa(lds + SumsW::kFloats);
+  SumsB ac(lds + 2 * SumsW::kFloats), ab(lds + 2 * SumsW::kFloats + SumsB::kFloats);
   aw.clear();
-  ac.clear();
+  if constexpr (BIAS) ac.clear();
   for (uint32_t piece = begin; piece < end; ++piece) {
     const uint32_t group = __builtin_amdgcn_readfirstlane(piece / A.per_group);
     // every per_group-th set of L rows of the run: workgroups side by side read side by side
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
     }
     if constexpr (JOIN) {
       aa.clear();
-      ab.clear();
+      if constexpr (BIAS) ab.clear();
     }
     for (int64_t base = row0; base < row1; base += step) {
       const int64_t row = base + part;
@@ -681,18 +686,20 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
             }
           }
           n2.get(at, A, A.before, false, p, w, b);
-          float sw[V];
+          float sw[V], sc[V];
           aw.get(p, sw);
+          if constexpr (BIAS) ac.get(p, sc);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             hn[p][e] = __builtin_fmaf(hn[p][e], s2, c2);
             const float d = elem(du[p], e);
             gu[p][e] = d * w[e];
             sw[e] = __builtin_fmaf(d, hn[p][e], sw[e]);
-            if constexpr (BIAS) ac.v[p][e] += d;
+            if constexpr (BIAS) sc[e] += d;
             t[0] = __builtin_fmaf(gu[p][e], hn[p][e], t[0]);
           }
           aw.put(p, sw);
+          if constexpr (BIAS) ac.put(p, sc);
           if (flags & kJoinMean2) {
 #pragma unroll
             for (int e = 0; e < V; ++e) t[1] += gu[p][e];
@@ -742,16 +749,18 @@ __global__ void __launch_bounds__(kWave * (FEW ? kFewWaves : kMaxWaves)) join_ba
               dt[p][e] *= token;
             }
           }
-          float sa[V];
+          float sa[V], sb[V];
           aa.get(p, sa);
+          if constexpr (BIAS) ab.get(p, sb);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             sa[e] = __builtin_fmaf(dt[p][e], yn[p][e], sa[e]);
-            if constexpr (BIAS) ab.v[p][e] += dt[p][e];
+            if constexpr (BIAS) sb[e] += dt[p][e];
             dt[p][e] *= w[e];  // dz w
             t[0] = __builtin_fmaf(dt[p][e], yn[p][e], t[0]);
           }
           aa.put(p, sa);
+          if constexpr (BIAS) ab.put(p, sb);
           if (flags & kJoinMean1) {
 #pragma unroll
             for (int e = 0; e < V; ++e) t[1] += dt[p][e];

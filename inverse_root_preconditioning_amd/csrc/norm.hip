@@ -143,7 +143,7 @@ Split split_rows(const shampoo_join& j) {
   Split s;
   const bool bf16 = j.stream_dtype == SHAMPOO_T_BF16;
   s.layout = row_layout(j.cols, bf16 ? 8 : 4);
-  const BackGrid grid = back_grid(s.layout, bf16 ? 8 : 4, bf16 && has_bias(j) && j.branch != nullptr);
+  const BackGrid grid = back_grid(s.layout, bf16 ? 8 : 4);
   s.lanes = grid.lanes;
   const int64_t run = j.gate_kind == SHAMPOO_GATE_ROWS ? j.gate_rows : j.rows;
   const int64_t want = (((j.rows + grid.resident - 1) / grid.resident) + s.lanes - 1) / s.lanes * s.lanes;

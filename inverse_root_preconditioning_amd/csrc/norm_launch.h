@@ -37,24 +37,17 @@ int with_pieces(int pieces, F&& f) {
 
 // Workgroups of the backward kernel: rows that one holds side by side, and how
 // many the compute units hold.  16 waves' worth of rows, so that there are few
-// partial sums, or a row (4 waves' worth) where a lane needs more registers than 16 waves leave it
-// (`many`: a join of 8 bf16 elements a lane with biases, 148, of which 3 waves fit each of a unit's four
-// SIMDs; of 4 fp32 elements a lane 5 do).  A row of 5 waves takes two of one of them, and with 148 no
-// other workgroup fits beside it: 16 waves' worth again.
-// Joins and norms of 2^25 bf16 elements, us with 16, 8 and 4 waves: rows of 512 66, 67, - and 34, 35, -;
-// of 2048 73, 72, 78 and 37, 38, 38; 1000 rows of 2048 14, 16, - and 10, 12, -.
-// Joins of them with biases, 16 waves' worth without and a row with more registers: 2560 (5 waves) 116,
-// 134, 2944 (6) 132, 130, 3584 (7) 117, 102, 4096 (8) 110, 92; 2050 (5) 161, 210, 3842 (8) 135, 99.
+// partial sums: joins and norms of 2^25 bf16 elements, us with 16, 8 and 4 waves: rows of 512 66, 67, - and
+// 34, 35, -; of 2048 73, 72, 78 and 37, 38, 38; 1000 rows of 2048 14, 16, - and 10, 12, -.
+// (Of 4 fp32 elements a lane 20 waves fit a unit.)
 struct BackGrid {
   uint32_t lanes;
   int64_t resident;
 };
-inline BackGrid back_grid(const RowLayout& layout, int V, bool many) {
-  many = many && layout.pieces == 1 && layout.waves <= kFewWaves && layout.waves != 5;
-  const uint32_t all = many ? 4 : kMaxWaves;
+inline BackGrid back_grid(const RowLayout& layout, int V) {
   BackGrid g;
-  g.lanes = layout.waves < all ? all / layout.waves : 1;
-  g.resident = 256 * std::max<uint32_t>(1, (many ? 12 : V == 4 && layout.pieces == 1 ? 20 : kMaxWaves) / (layout.waves * g.lanes));
+  g.lanes = kMaxWaves / layout.waves;
+  g.resident = 256 * std::max<uint32_t>(1, (V == 4 && layout.pieces == 1 ? 20 : kMaxWaves) / (layout.waves * g.lanes));
   return g;
 }
 
@@ -65,20 +58,10 @@ int launch_join_backward(const JoinArgs& a, int pieces, uint32_t blocks, hipStre
   return with_pieces<V>(pieces, [&](auto p) {
     constexpr int P = decltype(p)::value;
     const bool whole = a.cols % V == 0;
-    if constexpr (JOIN && BIAS && P == 1 && V == 8) {
-      if (block.x <= kWave * kFewWaves) {
-        if (whole) {
-          hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, true, true>), grid, block, 0, stream, a);
-        } else {
-          hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, true, false>), grid, block, 0, stream, a);
-        }
-        return check_launch();
-      }
-    }
     if (whole) {
-      hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, false, true>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, true>), grid, block, 0, stream, a);
     } else {
-      hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, false, false>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((join_backward_kernel<SB, BB, P, JOIN, KEEP, BIAS, false>), grid, block, 0, stream, a);
     }
     return check_launch();
   });
