@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
   constexpr int V = SB ? 8 : 4;
   typedef Places<P, V, WHOLE> At;
   // Parameters in registers and the next row's loads in flight, where there are registers for
-  // them: 128 in a workgroup of 16 waves.  (4096 rows of 16384 without this rule: 690 us, in scratch memory.)
+  // them: 128 in a workgroup of 16 waves.
   constexpr bool kAhead = P * V <= 8;
   __shared__ __attribute__((aligned(16))) float red[kMaxWaves * kSumsFloats];
   // Columns' sums in LDS where 128 registers do not hold them, 128 KB of its 160: those for w2 and w1 (or the
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
   typedef ColumnSums<P, V, kInLds> SumsW;
   typedef ColumnSums<P, V, kAllInLds> SumsB;
   // those, or for registers one such array in which rows side by side meet
-  __shared__ __attribute__((aligned(16))) float lds[kInLds ? 2 * SumsW::kFloats + 2 * SumsB::kFloats : kMaxWaves * kWave * V];
+  constexpr int kLds = kInLds ? 2 * SumsW::kFloats + 2 * SumsB::kFloats : kMaxWaves * kWave * V;
+  __shared__ __attribute__((aligned(16))) float lds[kLds];
   const uint32_t L = A.lanes;
   const uint32_t part = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / A.waves);
   const uint32_t lane0 = threadIdx.x - part * A.waves * kWave;
