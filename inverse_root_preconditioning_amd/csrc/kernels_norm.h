@@ -785,16 +785,19 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
             }
           }
         }
+        // Without a norm yn is the branch, and infinities times m0 = 0 are no part of dz.
+        if (!(flags & kJoinNorm1)) {
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int e = 0; e < V; ++e) yn[p][e] = 0.f;
+        }
         if (here && A.dy != nullptr) {
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             float o[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = dt[p][e];
-            if (flags & kJoinNorm1) {  // without it yn is the branch, whose infinities times m0 = 0 are no part of dz
-#pragma unroll
-              for (int e = 0; e < V; ++e) o[e] = __builtin_fmaf(o[e], s1, __builtin_fmaf(yn[p][e], m0, m1));
-            }
+            for (int e = 0; e < V; ++e) o[e] = __builtin_fmaf(dt[p][e], s1, __builtin_fmaf(yn[p][e], m0, m1));
             at.template store<BB>(row_at<BB>(A.dy, row, A.lddy), p, o);
           }
         }
