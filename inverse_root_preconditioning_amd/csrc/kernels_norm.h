@@ -272,7 +272,9 @@ __device__ __forceinline__ float load_token(const JoinArgs& A, int64_t row) {
   return ldg(static_cast<const float*>(A.gate) + row);
 }
 
-// Mean and s of a row held in pieces, zero beyond its end.
+// Mean and s of a row held in pieces, zero beyond its end; the row is centred: what is normed is formed as
+// (x - mean) s, whose difference is exact near the mean.  As x s - mean s it would keep the product's rounding:
+// 0.03 where x = mean = 1000 and the variance is 0.
 template <int P, int V, bool WHOLE>
 __device__ __forceinline__ void row_stats(const Places<P, V, WHOLE>& at, const float (&x)[P][V], bool centred,
                                           float eps, RowSums& sums, float& mean, float& s) {
@@ -285,7 +287,9 @@ __device__ __forceinline__ void row_stats(const Places<P, V, WHOLE>& at, const f
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int e = 0; e < V; ++e) t += x[p][e];
-    mean = sums.total1(t) * over;
+    t = sums.total1(t);
+    mean = t * over;
+    mean = __builtin_fmaf(__builtin_fmaf(-mean, (float)anew_uniform(at.cols), t), over, mean);  // as rounded once: exact where t / cols is
 #pragma unroll
     for (int p = 0; p < P; ++p) {
 #pragma unroll
@@ -378,8 +382,6 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const J
         const uint32_t now = __builtin_amdgcn_readfirstlane((uint32_t)row / A.gate_rows);
         if (now != n1.run) n1.keep(at, A, A.after, true, now);
       }
-      // (x - mean) s as one operation: the product mean s is rounded by no more than the mean itself
-      const float c = -mean * s;
       const float token = flags & kJoinToken ? load_token(A, row) : 1.f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -388,13 +390,13 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const J
         if (flags & kJoinToken) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float z = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], b[e]);
+            const float z = __builtin_fmaf((x[p][e] - mean) * s, w[e], b[e]);
             x[p][e] = __builtin_fmaf(token, z, A.scale * rf[p][e]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            x[p][e] = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], __builtin_fmaf(A.scale, rf[p][e], b[e]));
+            x[p][e] = __builtin_fmaf((x[p][e] - mean) * s, w[e], __builtin_fmaf(A.scale, rf[p][e], b[e]));
         }
       }
 #pragma unroll
@@ -409,13 +411,12 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_forward_kernel(const J
       float mean, s;
       row_stats(at, x, (flags & kJoinMean2) != 0, A.before.eps, sums, mean, s);
       if (A.stats2 != nullptr && at.lane == 0) stg(reinterpret_cast<f32x2_t*>(A.stats2) + row, f32x2_t{mean, s});
-      const float c = -mean * s;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         float u[V], w[V], b[V];
         n2.get(at, A, A.before, false, p, w, b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = __builtin_fmaf(__builtin_fmaf(x[p][e], s, c), w[e], b[e]);
+        for (int e = 0; e < V; ++e) u[e] = __builtin_fmaf((x[p][e] - mean) * s, w[e], b[e]);
         at.template store<BB>(row_at<BB>(A.u, row, A.ldu), p, u);
       }
     }
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
       }
       float yn[P][V], hn[P][V], dt[P][V], gu[P][V];
       float t[2] = {0.f, 0.f};
-      const float s1 = st1[1], c1 = -st1[0] * st1[1], s2 = st2[1], c2 = -st2[0] * st2[1];
+      const float mean1 = st1[0], s1 = st1[1], mean2 = st2[0], s2 = st2[1];
       float token = 1.f;
       if constexpr (JOIN) {
         if (here && (flags & kJoinToken)) token = load_token(A, row);
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
           for (int p = 0; p < P; ++p) {
             y[p].get(at, A.ky, p, yn[p]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) yn[p][e] = __builtin_fmaf(yn[p][e], s1, c1);
+            for (int e = 0; e < V; ++e) yn[p][e] = (yn[p][e] - mean1) * s1;
           }
         }
       }
@@ -677,11 +678,11 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
             if (flags & kJoinToken) {
 #pragma unroll
               for (int e = 0; e < V; ++e)
-                hn[p][e] = __builtin_fmaf(token, __builtin_fmaf(yn[p][e], w[e], b[e]), A.scale * hn[p][e]);
+                hn[p][e] = __builtin_fmaf(token, __builtin_fmaf(yn[p][e], w[e], b[e]), __builtin_fmaf(A.scale, hn[p][e], -mean2));
             } else {
 #pragma unroll
               for (int e = 0; e < V; ++e) {
-                hn[p][e] = BIAS ? __builtin_fmaf(A.scale, hn[p][e], b[e]) : A.scale * hn[p][e];
+                hn[p][e] = __builtin_fmaf(A.scale, hn[p][e], BIAS ? b[e] - mean2 : -mean2);
                 hn[p][e] = __builtin_fmaf(yn[p][e], w[e], hn[p][e]);
               }
             }
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
           if constexpr (BIAS) ac.get(p, sc);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            hn[p][e] = __builtin_fmaf(hn[p][e], s2, c2);
+            hn[p][e] = JOIN ? hn[p][e] * s2 : (hn[p][e] - mean2) * s2;
             const float d = elem(du[p], e);
             gu[p][e] = d * w[e];
             sw[e] = __builtin_fmaf(d, hn[p][e], sw[e]);
