@@ -129,11 +129,31 @@ def dequantize(q, dtype=torch.float32, stream=None):
     return out
 
 
+# Of autograd's nodes those that hand their input on: copies of another type or layout, and views.
+_COPIES = {"ToCopyBackward0", "CloneBackward0", "TBackward0", "TransposeBackward0", "PermuteBackward0", "ViewBackward0",
+           "UnsafeViewBackward0", "ReshapeAliasBackward0", "AliasBackward0", "SliceBackward0", "SelectBackward0",
+           "UnsqueezeBackward0", "ExpandBackward0"}
+
+
+def _of_leaf(t):
+    """Whether t is a leaf of autograd's graph, a view of one, or a copy of either."""
+    node = t.grad_fn if t._base is None else t._base.grad_fn
+    while node is not None and node.name() in _COPIES:
+        node = node.next_functions[0][0]
+    return node is None or hasattr(node, "variable")     # the node that gathers a leaf's gradient
+
+
 def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
     """A context in which autograd keeps activations in MX8: every CUDA tensor of
     `dtypes` (bfloat16, float32) and at least `min_elements` that an operation
-    inside saves for its backward pass, but for leaves that require a gradient
-    (parameters) and views of them.  Backward then computes from the rounded values.
+    inside saves for its backward pass and that autograd formed.  Backward then
+    computes from the rounded values.
+
+    Leaves stay as they are: parameters, trained or frozen, inputs, and what was formed
+    without a gradient (masks, statistics); so do views of leaves and copies of
+    them in another type, as mixed precision makes of its weights.  A weight that is
+    computed otherwise (scaled, composed) is rounded like an activation: form
+    it, and use it, outside.
 
     float32 is not rounded unless asked for, since operations on bfloat16 keep
     statistics in it (a norm's, the logarithms of an attention's sums) whose
@@ -147,8 +167,7 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
     def pack(t):
         if t.dtype not in dtypes or not t.is_cuda or t.numel() < max(min_elements, 1):
             return t
-        base = t if t._base is None else t._base
-        if base.requires_grad and base.is_leaf or t.layout != torch.strided:
+        if t.layout != torch.strided or _of_leaf(t):
             return t
         # rows of less than two groups would be mostly padding; a vector is one row
         k, cols = t.dim(), 1
