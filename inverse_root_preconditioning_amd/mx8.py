@@ -10,7 +10,10 @@ arithmetic runs in the HIP library (see capi and include/shampoo.h).
 """
 from __future__ import annotations
 
+import weakref
+
 import torch
+from torch.utils.weak import WeakTensorKeyDictionary
 
 from . import capi
 from .adamw import _TYPES, _current_device, _on_stream, _raw_stream
@@ -143,6 +146,15 @@ def _of_leaf(t):
     return node is None or hasattr(node, "variable")     # the node that gathers a leaf's gradient
 
 
+class _Kept:
+    """A copy, alive while a graph that saved the tensor holds it."""
+
+    __slots__ = ("q", "__weakref__")
+
+    def __init__(self, q):
+        self.q = q
+
+
 def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
     """A context in which autograd keeps activations in MX8: every CUDA tensor of
     `dtypes` (bfloat16, float32) and at least `min_elements` that an operation
@@ -160,9 +172,31 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
     rounding would spoil their gradients.  For the same reason a loss belongs
     outside: what it keeps is a logarithm.  The operations of mx4 and layers keep
     integers, or with keep="same" their inputs, which are rounded like any others.
-    Columns are the last dimension, with those before it where it is short."""
+    Columns are the last dimension, with those before it where it is short.
+
+    A tensor that several operations save has one copy, as it is one tensor to
+    autograd: while a graph holds that copy and the tensor lives unchanged (autograd counts
+    changes in place), on the same stream, and not while a graph is captured."""
+    dtypes = tuple(dtypes)
     if not set(dtypes) <= set(_TYPES):
         raise ValueError("dtypes are of float32 and bfloat16")
+    copies = WeakTensorKeyDictionary()   # tensor -> {version, part, layout and stream: its copy}, both weakly
+
+    def copy_of(t, cols):
+        def make():
+            return _Kept(quantize(t.detach().reshape(-1, cols).contiguous()))
+        if torch.cuda.is_current_stream_capturing():
+            return make()
+        layout = (t.numel(), cols) if t.is_contiguous() else (t.shape, t.stride())
+        key = (t._version, t.dtype, t.is_neg(), t.storage_offset(), layout, _raw_stream(t.device.index))
+        known = copies.setdefault(t if t._base is None else t._base, {})
+        kept = known[key]() if key in known else None
+        if kept is None:
+            for gone in [k for k, ref in known.items() if ref() is None]:
+                del known[gone]
+            kept = make()
+            known[key] = weakref.ref(kept)
+        return kept
 
     def pack(t):
         if t.dtype not in dtypes or not t.is_cuda or t.numel() < max(min_elements, 1):
@@ -176,11 +210,11 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
             cols *= t.shape[k]
         if cols > _MAX_COLS:
             return t
-        return quantize(t.detach().reshape(-1, cols).contiguous()), t.dtype, t.shape
+        return copy_of(t, cols), t.dtype, t.shape
 
     def unpack(kept):
         if isinstance(kept, torch.Tensor):
             return kept
-        q, dtype, shape = kept
-        return dequantize(q, dtype).view(shape)
+        copy, dtype, shape = kept
+        return dequantize(copy.q, dtype).view(shape)
     return torch.autograd.graph.saved_tensors_hooks(pack, unpack)
