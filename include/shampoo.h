@@ -655,12 +655,17 @@ typedef struct shampoo_join_grads {
  * are of fixed order: the same call gives the same bits.  The residual's codes
  * are read only where there is d_u, the branch's only with a norm after
  * it, a gate or d_u.  Copies are as shampoo_mx8_quantize writes them (NaN codes beside s = 255).
- *   ws         shampoo_join_workspace_bytes(join) bytes
+ *   ws         shampoo_join_backward_workspace_bytes(join, grads) bytes: rows of fp32 sums for some hundred
+ *              workgroups, and where gradients of a gate of rows or of the norm after the branch
+ *              are wanted, one (with a bias of that norm up to two) for each run of gate_rows
+ *              rows: with gate_rows = 1 as much as an fp32 matrix.
+ *              shampoo_join_workspace_bytes(join): enough for any grads
  */
 int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* grads, void* ws, size_t ws_bytes,
                           hipStream_t stream);
 /* 0 for a join that is refused, and for one without rows or columns. */
 size_t shampoo_join_workspace_bytes(const shampoo_join* join);
+size_t shampoo_join_backward_workspace_bytes(const shampoo_join* join, const shampoo_join_grads* grads);
 
 /* Workspace size in bytes for an operation (op = SHAMPOO_OP_*).  `count` is
  * nfactors for SCALE/NEWTON/CHEBY and nblocks for ACCUMULATE/PRECONDITION;

@@ -183,6 +183,7 @@ _SIGNATURES = {
     "shampoo_join_forward": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
     "shampoo_join_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "shampoo_join_workspace_bytes": (c_size_t, [c_void_p]),
+    "shampoo_join_backward_workspace_bytes": (c_size_t, [c_void_p, c_void_p]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -377,3 +378,7 @@ def shampoo_join_backward(join, grads, ws, ws_bytes, stream):
 
 def shampoo_join_workspace_bytes(join):
     return load().shampoo_join_workspace_bytes(join)
+
+
+def shampoo_join_backward_workspace_bytes(join, grads):
+    return load().shampoo_join_backward_workspace_bytes(join, grads)

@@ -428,7 +428,7 @@ struct Join : torch::autograd::Function<Join> {
       g.d_gate = at(kGate);
       g.d_before_weight = at(kW2);
       g.d_before_bias = at(kB2);
-      const int64_t size = (int64_t)shampoo_join_workspace_bytes(&j);
+      const int64_t size = (int64_t)shampoo_join_backward_workspace_bytes(&j, &g);
       const Tensor ws = at::empty({size}, given.options().dtype(at::kByte));
       check_backward(shampoo_join_backward(&j, &g, ws.data_ptr(), (size_t)size, stream_of(given)),
                      "shampoo_join_backward");

@@ -157,6 +157,18 @@ Split split_rows(const shampoo_join& j) {
 
 int64_t pitch_of(int64_t cols) { return (cols + 7) / 8 * 8; }
 
+// Bytes of the partial sums: rows for each workgroup, and for each piece where gradients of what
+// multiplies or follows the normed branch are wanted (no g: those of every parameter that there is).
+size_t sums_bytes(const shampoo_join& j, const Split& s, const shampoo_join_grads* g) {
+  const bool norm = j.after.kind != SHAMPOO_NORM_NONE, weight = norm && j.after.weight != nullptr;
+  const bool bias = norm && j.after.bias != nullptr;
+  const bool gate = j.gate_kind == SHAMPOO_GATE_ROWS && (g == nullptr || g->d_gate != nullptr);
+  const bool scaled = gate || (weight && (g == nullptr || g->d_after_weight != nullptr));
+  const bool added = bias && (gate || g == nullptr || g->d_after_bias != nullptr);
+  const int64_t rows = s.blocks * (has_bias(j) ? 2 : 1) + s.pieces * ((int)scaled + (int)added);
+  return (size_t)rows * (size_t)pitch_of(j.cols) * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -182,12 +194,15 @@ int shampoo_join_forward(const shampoo_join* join, void* h, int64_t ld_h, void* 
   return join->branch_dtype == SHAMPOO_T_BF16 ? forward<false, true>(a, stream) : forward<false, false>(a, stream);
 }
 
-size_t shampoo_join_workspace_bytes(const shampoo_join* join) {
+size_t shampoo_join_backward_workspace_bytes(const shampoo_join* join, const shampoo_join_grads* g) {
   JoinArgs a;
   bool empty;
   if (common(join, &a, &empty) != SHAMPOO_OK || empty) return 0;
-  const Split s = split_rows(*join);
-  return (size_t)((s.pieces + s.blocks) * (has_bias(*join) ? 2 : 1)) * (size_t)pitch_of(join->cols) * sizeof(float);
+  return sums_bytes(*join, split_rows(*join), g);
+}
+
+size_t shampoo_join_workspace_bytes(const shampoo_join* join) {
+  return shampoo_join_backward_workspace_bytes(join, nullptr);
 }
 
 int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g, void* ws, size_t ws_bytes,
@@ -224,10 +239,9 @@ int shampoo_join_backward(const shampoo_join* join, const shampoo_join_grads* g,
   }
   if ((has1 && a.stats1 == nullptr) || (has2 && a.stats2 == nullptr)) return SHAMPOO_EINVAL;
   const int64_t gate_rows = join->gate_kind == SHAMPOO_GATE_ROWS ? join->gate_rows : 0;
-  const size_t need = shampoo_join_workspace_bytes(join);
-  if (ws == nullptr || ws_bytes < need) return SHAMPOO_EWORKSPACE;
-  if (!aligned16(ws)) return SHAMPOO_EINVAL;
   const Split s = split_rows(*join);
+  if (ws == nullptr || ws_bytes < sums_bytes(*join, s, g)) return SHAMPOO_EWORKSPACE;
+  if (!aligned16(ws)) return SHAMPOO_EINVAL;
   if (s.blocks > kMaxThreads / 1024) return SHAMPOO_EUNSUPPORTED;
   a.dh = g->d_h;
   a.lddh = g->ld_d_h;

@@ -118,7 +118,10 @@ def join(residual, branch, after=None, gate=None, scale=1.0, before=None, keep="
     after, before the Norm of the branch (None: the branch as it is) and the
                   next block's Norm (None: u is None)
     gate          [C]; [..., 1], a number for each row; or a row of C for each run of
-                  the rows, such as [B, 1, C] for [B, S, C]
+                  the rows, such as [B, 1, C] for [B, S, C].  The backward pass sums
+                  gradients of the gate, and of after's parameters, run by run, in
+                  workspace of 4 bytes an element of the gate (8 where after has a bias):
+                  with a row of the gate for each row that is as much as an fp32 h
     scale         a number"""
     if branch is None:
         raise ValueError("branch must be a tensor")
