@@ -6,15 +6,20 @@
 
 namespace shp {
 
-// exp(-v) for 0 <= v <= 150.  FINE: to about an ulp, v (given in two floats)
+// exp(-v) = e unit for 0 <= v <= 120.  FINE: to about an ulp, v (given in two floats)
 // times log2(e) in two floats, so that the error of a large exponent does not
 // reach the result.  Else within 2^-15: v's own rounding and that of the
 // product, up to 300 ulps where v is large, which a bf16 result (half a step: 2^-9) does not show.
-template <bool FINE>
-__device__ __forceinline__ float exp_minus(float v, float v_low = 0.f) {
+// The instruction has no subnormal results: e is 0 below 2^-126, but for FAR, where unit is 2^-64 for large v and e
+// a normal number, so that what it is multiplied by is not lost.
+template <bool FINE, bool FAR>
+__device__ __forceinline__ float exp_minus(float v, float v_low, float& unit) {
+#pragma clang fp contract(off)
   constexpr float kHi = 1.44269504088896341f, kLo = 1.9259629911e-8f;  // log2(e) and what fp32 leaves of it
-  const float t = -v * kHi;
-  const float e = __builtin_amdgcn_exp2f(t);
+  const float t = -v * kHi;  // rounded by itself, so that `low` is what it lacks
+  const bool far = FAR && v > 80.f;  // t below -115, so that t + 64 is exact
+  unit = far ? 0x1p-64f : 1.f;
+  const float e = __builtin_amdgcn_exp2f(far ? t + 64.f : t);
   if constexpr (!FINE) return e;
   const float low = __builtin_fmaf(-v_low, kHi, __builtin_fmaf(-v, kLo, __builtin_fmaf(-v, kHi, -t)));
   return __builtin_fmaf(e, low * 0.693147180559945309f, e);
@@ -26,10 +31,16 @@ __device__ __forceinline__ float clamp_abs(float x, float limit) {
   return x < -limit ? -limit : x;
 }
 
-// f(x) and, with SLOPE, f'(x); FINE for fp32 results (see exp_minus).  Beyond the
-// clamps f is 0 or x and f' 0 or 1 to the last bit, and no intermediate result overflows into a
-// NaN.  (The exponential is 0 below 2^-126, so that far tails end there.)
-template <int ACT, bool SLOPE, bool FINE>
+// Magnitudes up to which every factor of f and f' is a normal number.  v is at most 80 there, so that such values'
+// results are the same bits in either form, whatever stands beside them.
+template <int ACT>
+constexpr float kNear = ACT == SHAMPOO_ACT_SILU ? 80.f : ACT == SHAMPOO_ACT_GELU ? 12.5f : 9.5f;
+
+// f(x) and, with SLOPE, f'(x); FINE for fp32 results (see exp_minus), FAR where x may lie beyond kNear and its result
+// is to keep its relative precision down to 2^-126; without it the tails end with the exponential, at
+// results of some 2^-119.  Beyond the clamps f is 0 or x and f' 0 or 1 to the last bit, and no intermediate
+// result overflows into a NaN for any finite x.  (-infinity: f = -infinity 0, a NaN, but for the relus; f' = 0.)
+template <int ACT, bool SLOPE, bool FINE, bool FAR>
 __device__ __forceinline__ void activation(float x, float& f, float& d) {
   if constexpr (ACT == SHAMPOO_ACT_RELU) {
     f = x < 0.f ? 0.f : x;
@@ -57,16 +68,27 @@ __device__ __forceinline__ void activation(float x, float& f, float& d) {
     q = __builtin_fmaf(q, t, 0.08976174890995026f);
     q = __builtin_fmaf(q, t, 0.08976201713085175f);
     const float h = 0.5f * z, s = h * z;
-    const float e = exp_minus<FINE>(s, __builtin_fmaf(h, z, -s));
-    const float tail = e * (q * t);
+    float unit;
+    const float e = exp_minus<FINE, FAR>(s, __builtin_fmaf(h, z, -s), unit);
+    float a = e, last = 1.f;
+    if constexpr (FAR) {  // a negative x takes e as it is and the unit last
+      a = x < 0.f ? (x < -15.f ? 0.f : e) : e * unit;
+      last = x < 0.f ? unit : 1.f;
+    }
+    const float tail = a * (q * t);
     const float p = x < 0.f ? tail : 1.f - tail;
     f = x * p;
-    if (SLOPE) d = __builtin_fmaf(c * e, 0.398942280401432678f, p);
+    if (SLOPE) d = __builtin_fmaf(c * a, 0.398942280401432678f, p);
+    if constexpr (FAR) {
+      f *= last;
+      if (SLOPE) d *= last;
+    }
   } else {
     // x p with p = 1 / (1 + exp(-v)): v = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)
     constexpr bool kTanh = ACT == SHAMPOO_ACT_GELU_TANH;
     constexpr float kA = 1.59576912160573071f, kALow = -4.534068054e-8f, kB = 0.044715f, kBLow = 1.546144435e-9f;
-    const float c = clamp_abs(x, kTanh ? 11.f : 105.f);  // v at most 112 and 105: e is 0 in fp32 from 104 on
+    constexpr float kLimit = kTanh ? 11.f : 111.f;  // v at most 113 and 111: x exp(-v) is 0 in fp32 from 109 on
+    const float c = clamp_abs(x, kLimit);
     float v, v_low = 0.f;
     if constexpr (kTanh && FINE) {
 #pragma clang fp contract(off)
@@ -82,16 +104,42 @@ __device__ __forceinline__ void activation(float x, float& f, float& d) {
     } else {
       v = kTanh ? kA * __builtin_fmaf(kB * c, c * c, c) : c;
     }
-    const float e = exp_minus<FINE>(fabsf(v), v_low);
-    const float r = __builtin_amdgcn_rcpf(1.f + e);
-    const float er = e * r;
+    float unit;
+    const float e = exp_minus<FINE, FAR>(fabsf(v), v_low, unit);
+    const float r = __builtin_amdgcn_rcpf(1.f + (FAR ? e * unit : e));
+    float a = e, last = 1.f;
+    if constexpr (FAR) {  // a negative x takes e as it is and the unit last
+      a = x < 0.f ? (x < -kLimit ? 0.f : e) : e * unit;
+      last = x < 0.f ? unit : 1.f;
+    }
+    const float er = a * r;
     const float p = x < 0.f ? er : r;
     f = x * p;
     if (SLOPE) {
       const float slope = kTanh ? kA * __builtin_fmaf(3.f * kB, c * c, 1.f) : 1.f;
       d = __builtin_fmaf(c * slope, er * r, p);
     }
+    if constexpr (FAR) {
+      f *= last;
+      if (SLOPE) d *= last;
+    }
   }
+}
+
+// each(far): a lane's V values x, in the form for far values where results are fp32 and the wave has one.  Taken
+// always it cost 4 to 6% (silu of 4096 x 8192 39 -> 41 us).
+template <int ACT, bool FINE, int V, class X, class F>
+__device__ __forceinline__ void near_or_far(X&& x, F&& each) {
+  if constexpr (FINE && ACT != SHAMPOO_ACT_RELU && ACT != SHAMPOO_ACT_RELU2) {
+    bool far = false;
+#pragma unroll
+    for (int e = 0; e < V; ++e) far |= fabsf(x(e)) > kNear<ACT>;
+    if (__builtin_expect(__any(far), 0)) {
+      each(std::true_type{});
+      return;
+    }
+  }
+  each(std::false_type{});
 }
 
 struct ActArgs {
@@ -137,12 +185,14 @@ __global__ void __launch_bounds__(256) act_forward_kernel(const ActArgs P) {
       }
     }
     if (r < P.rows) {
-      float y[V], unused;
+      float y[V], unused = 0.f;
+      near_or_far<ACT, !BF16, V>([&](int e) { return elem(a[i], e); }, [&](auto far) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        activation<ACT, false, !BF16>(elem(a[i], e), y[e], unused);
-        if constexpr (GATED) y[e] *= elem(b[i], e);
-      }
+        for (int e = 0; e < V; ++e) {
+          activation<ACT, false, !BF16, decltype(far)::value>(elem(a[i], e), y[e], unused);
+          if constexpr (GATED) y[e] *= elem(b[i], e);
+        }
+      });
       store_row<BF16, V>(row_at<BF16>(P.y, r, P.ldy), P.cols, col, y);
     }
   }
@@ -179,21 +229,23 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const ActArgs P) {
       qa[i].decode(av);
       if constexpr (GATED) qb[i].decode(bv);
     }
+    near_or_far<ACT, !BF16, V>([&](int e) { return KEEP ? av[e] : elem(a[i], e); }, [&](auto far) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if constexpr (!KEEP) {
-        av[e] = elem(a[i], e);
-        if constexpr (GATED) bv[e] = elem(b[i], e);
+      for (int e = 0; e < V; ++e) {
+        if constexpr (!KEEP) {
+          av[e] = elem(a[i], e);
+          if constexpr (GATED) bv[e] = elem(b[i], e);
+        }
+        float f, d;
+        activation<ACT, true, !BF16, decltype(far)::value>(av[e], f, d);
+        const float g = elem(dy[i], e);
+        da[e] = g * d;
+        if constexpr (GATED) {
+          da[e] *= bv[e];
+          db[e] = g * f;
+        }
       }
-      float f, d;
-      activation<ACT, true, !BF16>(av[e], f, d);
-      const float g = elem(dy[i], e);
-      da[e] = g * d;
-      if constexpr (GATED) {
-        da[e] *= bv[e];
-        db[e] = g * f;
-      }
-    }
+    });
     if (P.da != nullptr) store_row<BF16, V>(row_at<BF16>(P.da, r, P.ldda), P.cols, col, da);
     if constexpr (GATED) {
       if (P.db != nullptr) store_row<BF16, V>(row_at<BF16>(P.db, r, P.lddb), P.cols, col, db);
