@@ -71,6 +71,13 @@ def gated(x, b=None, act="silu", keep="same"):
 # Norms and joins
 # ---------------------------------------------------------------------------
 
+def _number(value, name):
+    """A float.  A tensor that requires a gradient would get none, and is refused."""
+    if isinstance(value, torch.Tensor) and value.requires_grad:
+        raise ValueError(f"{name} is a number: no gradient of it is formed")
+    return float(value)
+
+
 class Norm:
     """A norm over the last dimension: "rms", x / sqrt(mean(x^2) + eps), or
     "layer", (x - mean) / sqrt(variance + eps); times weight, plus bias
@@ -82,9 +89,10 @@ class Norm:
         self._code = _KINDS.get(kind)
         if self._code is None:
             raise ValueError(f"kind must be one of {sorted(_KINDS)}")
+        eps = _number(eps, "eps")
         if not 0.0 < eps < math.inf:
             raise ValueError("eps must be positive")
-        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, float(eps)
+        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, eps
 
 
 _NO_NORM = (capi.NORM_NONE, 0.0, None, None)
@@ -128,4 +136,4 @@ def join(residual, branch, after=None, gate=None, scale=1.0, before=None, keep="
     n1, n2 = _parts(after, "after"), _parts(before, "before")
     if forward_ad._current_level >= 0:
         _refuse_tangents(residual, branch, gate, *n1[2:], *n2[2:])
-    return capi.load_layers().join(residual, branch, *n1, gate, scale, *n2, False, _low(keep))
+    return capi.load_layers().join(residual, branch, *n1, gate, _number(scale, "scale"), *n2, False, _low(keep))
