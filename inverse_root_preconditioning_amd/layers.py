@@ -83,16 +83,32 @@ class Norm:
     "layer", (x - mean) / sqrt(variance + eps); times weight, plus bias
     (vectors, float32 or bfloat16; None: 1 and 0)."""
 
-    __slots__ = ("kind", "weight", "bias", "eps", "_code")
+    __slots__ = ("weight", "bias", "_kind", "_code", "_eps")
 
     def __init__(self, kind="rms", weight=None, bias=None, eps=1e-6):
-        self._code = _KINDS.get(kind)
-        if self._code is None:
+        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, eps
+
+    @property
+    def kind(self):
+        return self._kind
+
+    @kind.setter
+    def kind(self, kind):
+        code = _KINDS.get(kind)
+        if code is None:
             raise ValueError(f"kind must be one of {sorted(_KINDS)}")
+        self._kind, self._code = kind, code
+
+    @property
+    def eps(self):
+        return self._eps
+
+    @eps.setter
+    def eps(self, eps):
         eps = _number(eps, "eps")
         if not 0.0 < eps < math.inf:
             raise ValueError("eps must be positive")
-        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, eps
+        self._eps = eps
 
 
 _NO_NORM = (capi.NORM_NONE, 0.0, None, None)
@@ -103,7 +119,7 @@ def _parts(n, name):
         return _NO_NORM
     if not isinstance(n, Norm):
         raise ValueError(f"{name} must be a Norm")
-    return n._code, n.eps, n.weight, n.bias
+    return n._code, n._eps, n.weight, n.bias
 
 
 def norm(x, n, dtype=None, keep="same"):
