@@ -8,8 +8,10 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <cmath>
@@ -41,6 +43,17 @@ void check(int rc, const char* where) {
 }
 void check_backward(int rc, const char* where) {
   TORCH_CHECK(rc == SHAMPOO_OK, where, ": ", shampoo_strerror(rc), " (code ", rc, ")");
+}
+
+// A trace would hold the allocation of the outputs and not the call that fills them.
+void refuse_trace() {
+  using c10::impl::TorchDispatchModeKey;
+  if (!torch::jit::tracer::isTracing() &&
+      !c10::impl::TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY).has_value())
+    return;
+  py::gil_scoped_acquire gil;
+  PyErr_SetString(PyExc_NotImplementedError, "the layers cannot be recorded in a trace");
+  throw py::error_already_set();
 }
 
 int type_of(const Tensor& t) {
@@ -240,6 +253,7 @@ struct Activation : torch::autograd::Function<Activation> {
 };
 
 Tensor activate(const Tensor& a, const OptTensor& b, bool packed, int64_t act, bool low) {
+  refuse_trace();
   auto s = c10::make_intrusive<ActState>();
   s->type = checked_type(a, "x");
   s->act = (int)act;
@@ -475,6 +489,7 @@ std::pair<Tensor, Tensor> join(const Tensor& residual, const OptTensor& branch, 
                                const OptTensor& w1, const OptTensor& b1, const OptTensor& gate, double scale,
                                int64_t kind2, double eps2, const OptTensor& w2, const OptTensor& b2, bool to_bf16,
                                bool low) {
+  refuse_trace();
   auto s = c10::make_intrusive<JoinState>();
   shampoo_join& j = s->j;
   j.stream_dtype = checked_type(residual, branch ? "residual" : "x");

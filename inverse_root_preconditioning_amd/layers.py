@@ -12,8 +12,8 @@ keep says what waits for the backward pass: "same", the inputs as they are, or
 backward computes; outputs and row statistics are those of the inputs
 themselves.  Arithmetic is fp32, rounded once into each output.  Calls run on
 the current stream; tensors are float32 or bfloat16 on one device, of any
-strides (rows that are not evenly spaced are copied first).  Gradients of gradients and
-forward-mode tangents are refused.
+strides (rows that are not evenly spaced are copied first).  Gradients of gradients,
+forward-mode tangents and traces (torch.jit.trace, make_fx) are refused; torch.compile runs the calls between its graphs.
 """
 from __future__ import annotations
 

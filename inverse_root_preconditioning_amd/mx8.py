@@ -93,14 +93,30 @@ class MX8Matrix:
             t.record_stream(stream)
 
 
+_tracing, _modes = torch._C._is_tracing, torch._C._len_torch_dispatch_stack   # cheap; the kind of a mode is not
+_PROXY = torch._C._TorchDispatchModeKey.PROXY
+
+
+def _in_trace():
+    return _tracing() or torch._C._get_dispatch_mode(_PROXY) is not None
+
+
+def _refuse_trace():
+    """A trace would hold the allocation of the result and not the call that fills it."""
+    if _in_trace():
+        raise NotImplementedError("MX8 conversions cannot be recorded in a trace")
+
+
 def quantize(x, stream=None):
     """x [rows, cols] as MX8, 32 consecutive columns sharing a scale; nearest even."""
+    if _tracing() or _modes():
+        _refuse_trace()
     if stream is not None:
         return _on_stream(stream, x.device, lambda: quantize(x), x)
     dtype, ld = _matrix(x, "x")
     if x.is_neg():                   # a view that negates what is in memory
         return quantize(x.resolve_neg())
-    index = x.device.index
+    index = x.get_device()
     if index != _current_device():
         with torch.cuda.device(index):
             return quantize(x)
@@ -115,6 +131,8 @@ def quantize(x, stream=None):
 
 def dequantize(q, dtype=torch.float32, stream=None):
     """The values of q."""
+    if _tracing() or _modes():
+        _refuse_trace()
     if stream is not None:
         return _on_stream(stream, q.device, lambda: dequantize(q, dtype), q)
     code = _TYPES.get(dtype)
@@ -201,7 +219,7 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
     def pack(t):
         if t.dtype not in dtypes or not t.is_cuda or t.numel() < max(min_elements, 1):
             return t
-        if t.layout != torch.strided or _of_leaf(t):
+        if t.layout != torch.strided or _of_leaf(t) or _in_trace():
             return t
         # rows of less than two groups would be mostly padding; a vector is one row
         k, cols = t.dim(), 1
