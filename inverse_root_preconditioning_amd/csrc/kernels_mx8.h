@@ -16,7 +16,7 @@ typedef short i16x2 __attribute__((ext_vector_type(2)));
 
 // Scale byte of a group from the bits of its largest magnitude (as fp32): that
 // one comes to lie in [2^7, 2^8), below E4M3's largest, 448, so that nothing
-// saturates; the 15 binades below it are held to a relative 2^-4.
+// saturates; the 13 binades below it are held to a relative 2^-4, what lies lower to 2^-17 of the largest.
 __device__ __forceinline__ uint32_t mx8_row_scale(uint32_t top_bits) {
   const int e = (int)(top_bits >> 23);
   return e == 255 ? 255u : (uint32_t)max(e - 7, 1);

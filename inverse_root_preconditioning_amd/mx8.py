@@ -4,7 +4,7 @@ pass (see layers, whose calls keep and read them by themselves).  All the
 arithmetic runs in the HIP library (see capi and include/shampoo.h).
 
     q = quantize(x)                  # 1.03 bytes an element
-    x = dequantize(q, x.dtype)       # within 2^-4 of each element, or 2^-18 of the largest of its 32
+    x = dequantize(q, x.dtype)       # within 2^-4 of each element, or 2^-17 of the largest of its 32
     with saved_tensors():            # what torch's own operations keep of bfloat16 inside is kept so
         y = block(x)
 """
