@@ -86,11 +86,19 @@ Copy copy_at(const Tensor& buf, int64_t index, int64_t rows, int64_t cols) {
   return c;
 }
 
+// A tensor's memory.  One that only stands for others (a wrapper subclass) has none, and an address of 0 would
+// say that the argument is not there.
+void* memory_of(const Tensor& t) {
+  void* const p = t.data_ptr();
+  if (p == nullptr && t.numel() > 0) refuse("a tensor without memory of its own (a wrapper of others)");
+  return p;
+}
+
 // A tensor as a matrix of evenly spaced rows of its last dimension: itself or a copy.
 struct Rows {
   Tensor t;
   int64_t ld = 0;
-  void* ptr() const { return t.data_ptr(); }
+  void* ptr() const { return memory_of(t); }
 };
 Rows rows_of(const Tensor& t) {
   if (t.is_neg()) return rows_of(t.resolve_neg());  // a view that negates what is in memory
@@ -295,7 +303,7 @@ void place_parameters(shampoo_join& j, Inputs& in) {
   auto place = [&](int i, const void*& ptr, int64_t& type) {
     if (!in.t[i].defined()) return;
     if (!in.t[i].is_contiguous() || in.t[i].is_neg()) in.t[i] = in.t[i].resolve_neg().contiguous();
-    ptr = in.t[i].data_ptr();
+    ptr = memory_of(in.t[i]);
     type = type_of(in.t[i]);
   };
   place(kW1, j.after.weight, j.after.weight_dtype);
