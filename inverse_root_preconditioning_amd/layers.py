@@ -13,7 +13,8 @@ backward computes; outputs and row statistics are those of the inputs
 themselves.  Arithmetic is fp32, rounded once into each output.  Calls run on
 the current stream; tensors are float32 or bfloat16 on one device, of any
 strides (rows that are not evenly spaced are copied first).  Gradients of gradients,
-forward-mode tangents and traces (torch.jit.trace, make_fx) are refused; torch.compile runs the calls between its graphs.
+forward-mode tangents, torch.func's transforms and traces (torch.jit.trace,
+make_fx) are refused; torch.compile runs the calls between its graphs.
 """
 from __future__ import annotations
 
@@ -72,10 +73,10 @@ def gated(x, b=None, act="silu", keep="same"):
 # ---------------------------------------------------------------------------
 
 def _number(value, name):
-    """A float.  A tensor that requires a gradient would get none, and is refused."""
+    """value; a tensor that requires a gradient would get none, and is refused."""
     if isinstance(value, torch.Tensor) and value.requires_grad:
         raise ValueError(f"{name} is a number: no gradient of it is formed")
-    return float(value)
+    return value
 
 
 class Norm:
@@ -105,10 +106,9 @@ class Norm:
 
     @eps.setter
     def eps(self, eps):
-        eps = _number(eps, "eps")
-        if not 0.0 < eps < math.inf:
+        if not 0.0 < _number(eps, "eps") < math.inf:
             raise ValueError("eps must be positive")
-        self._eps = eps
+        self._eps = float(eps)
 
 
 _NO_NORM = (capi.NORM_NONE, 0.0, None, None)

@@ -16,6 +16,13 @@ def test_numbers_that_require_a_gradient_are_refused():
         L.Norm("rms", eps=t)
 
 
+def test_texts_are_no_numbers():
+    with pytest.raises(TypeError):
+        L.join(X, X, scale="0.5")
+    with pytest.raises(TypeError):
+        L.Norm("rms", eps="1e-6")
+
+
 def test_other_numbers_are_taken():
     for one in (torch.tensor(0.5), torch.tensor(0.5).numpy(), 1):
         assert L.Norm("rms", eps=one).eps == float(one)
