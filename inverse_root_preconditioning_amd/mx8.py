@@ -152,8 +152,9 @@ def dequantize(q, dtype=torch.float32, stream=None):
 
 # Of autograd's nodes those that hand their input on: copies of another type or layout, and views.
 _COPIES = {"ToCopyBackward0", "CloneBackward0", "TBackward0", "TransposeBackward0", "PermuteBackward0", "ViewBackward0",
-           "UnsafeViewBackward0", "ReshapeAliasBackward0", "AliasBackward0", "SliceBackward0", "SelectBackward0",
-           "UnsqueezeBackward0", "ExpandBackward0"}
+           "UnsafeViewBackward0", "ReshapeAliasBackward0", "AliasBackward0", "AsStridedBackward0", "SliceBackward0",
+           "SelectBackward0", "SplitBackward0", "SplitWithSizesBackward0", "UnbindBackward0", "UnsqueezeBackward0",
+           "SqueezeBackward0", "SqueezeBackward1", "ExpandBackward0"}
 
 
 def _of_leaf(t):
@@ -161,7 +162,7 @@ def _of_leaf(t):
     node = t.grad_fn if t._base is None else t._base.grad_fn
     while node is not None and node.name() in _COPIES:
         node = node.next_functions[0][0]
-    return node is None or hasattr(node, "variable")     # the node that gathers a leaf's gradient
+    return node is None or node.name() == "torch::autograd::AccumulateGrad"
 
 
 class _Kept:
