@@ -116,7 +116,7 @@ class shampoo_join_grads(ctypes.Structure):
                 ("d_before_weight", c_void_p), ("d_before_bias", c_void_p)]
 
 
-# The same layouts for one call of pack (a tenth of the time of filling a Structure).
+# The same layouts for one call of pack: what shampoo_join_forward and _backward below take as bytes.
 JOIN = struct.Struct("=4qQqQqdqdQqQqqdQqQqqQqq6Q")
 JOIN_GRADS = struct.Struct("=QqQqQqQq5Q")
 

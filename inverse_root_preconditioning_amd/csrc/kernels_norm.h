@@ -272,9 +272,9 @@ __device__ __forceinline__ float load_token(const JoinArgs& A, int64_t row) {
   return ldg(static_cast<const float*>(A.gate) + row);
 }
 
-// Mean and s of a row held in pieces, zero beyond its end; the row is centred: what is normed is formed as
-// (x - mean) s, whose difference is exact near the mean.  As x s - mean s it would keep the product's rounding:
-// 0.03 where x = mean = 1000 and the variance is 0.
+// Mean and s of a row held in pieces, zero beyond its end.  What is normed is formed as (x - mean) s, whose
+// difference is exact near the mean.  As x s - mean s it would keep the product's rounding: 0.03 where
+// x = mean = 1000 and the variance is 0.
 template <int P, int V, bool WHOLE>
 __device__ __forceinline__ void row_stats(const Places<P, V, WHOLE>& at, const float (&x)[P][V], bool centred,
                                           float eps, RowSums& sums, float& mean, float& s) {
@@ -289,7 +289,8 @@ __device__ __forceinline__ void row_stats(const Places<P, V, WHOLE>& at, const f
       for (int e = 0; e < V; ++e) t += x[p][e];
     t = sums.total1(t);
     mean = t * over;
-    mean = __builtin_fmaf(__builtin_fmaf(-mean, (float)anew_uniform(at.cols), t), over, mean);  // as rounded once: exact where t / cols is
+    // as rounded once: exact where t / cols is
+    mean = __builtin_fmaf(__builtin_fmaf(-mean, (float)anew_uniform(at.cols), t), over, mean);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
 #pragma unroll
@@ -678,7 +679,8 @@ __global__ void __launch_bounds__(kWave * kMaxWaves) join_backward_kernel(const 
             if (flags & kJoinToken) {
 #pragma unroll
               for (int e = 0; e < V; ++e)
-                hn[p][e] = __builtin_fmaf(token, __builtin_fmaf(yn[p][e], w[e], b[e]), __builtin_fmaf(A.scale, hn[p][e], -mean2));
+                hn[p][e] = __builtin_fmaf(token, __builtin_fmaf(yn[p][e], w[e], b[e]),
+                                          __builtin_fmaf(A.scale, hn[p][e], -mean2));
             } else {
 #pragma unroll
               for (int e = 0; e < V; ++e) {

@@ -17,6 +17,8 @@ namespace {
 // together.  Joins of 2^25 bf16 elements with 8-bit copies, us by turns:
 // rows of 512:  1: 70, 2: 63, 4: 64;   of 2050 (5 waves)  2: 110, 4: 99, 8: 100;
 // of 5120 (10):  5: 78, 8: 83, 9: 71, 10: 76;   of 8192 (16):  1: 97, 4: 68, 8: 65, 12: 80.
+// The rule suits up to 8 waves and 16; at 10 its 8 is the slowest of those measured (820 workgroups, whose last ones
+// run by themselves).
 // Fewer rows, a join and a norm, us with workgroups for one a compute unit and for 16 waves a unit:
 // 1001 rows of 1537 fp32 11.7, 6.1 and 9.8, 5.3;  of 700 of 4096 bf16 8.1, 5.2 and 7.3, 4.6;  of 500 of
 // 8192 fp32 (16 waves a row, 512 workgroups instead of 256) 12.3, 7.3 and 16.8, 7.5.
