@@ -4,7 +4,8 @@
 // own, where Python costs twice what it does on the caller's.  Forward and
 // backward of small fp32 matrices, bound by the host, with nodes in Python -> here:
 // 1001 x 1537 activation 87 -> 43 us (torch's own silu takes 41), 333 x 1001 LayerNorm
-// 137 -> 51 to 65, 1001 x 1537 join 200 -> 106 to 110, of which its kernels take 37.
+// 137 -> 51 to 78, 1001 x 1537 join 200 -> 99 to 120, of which its kernels take 37; the
+// host's part varies from box to box.
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
