@@ -209,10 +209,12 @@ def saved_tensors(min_elements=1 << 14, dtypes=(torch.bfloat16,)):
         layout = (t.numel(), cols) if t.is_contiguous() else (t.shape, t.stride())
         key = (t._version, t.dtype, t.is_neg(), t.storage_offset(), layout, _raw_stream(t.device.index))
         known = copies.setdefault(t if t._base is None else t._base, {})
-        kept = known[key]() if key in known else None
+        found = known.get(key)
+        kept = found and found()
         if kept is None:
-            for gone in [k for k, ref in known.items() if ref() is None]:
-                del known[gone]
+            for other, ref in list(known.items()):           # another thread may be here too
+                if ref() is None:
+                    known.pop(other, None)
             kept = make()
             known[key] = weakref.ref(kept)
         return kept

@@ -29,6 +29,7 @@ def test_three_projections_keep_one_copy():
     x = normal(gen, 4, 64, 256, dtype=BF16).requires_grad_()
     ws = [normal(gen, 8, 256, dtype=BF16).requires_grad_() for _ in range(3)]
     t = x * 1
+    torch.autograd.grad(F.linear(x, ws[0]).sum(), (x, ws[0]))   # the library's own workspaces, autograd's thread's too
     gc.collect()
     before = torch.cuda.memory_allocated()
     with M8.saved_tensors():
@@ -128,3 +129,23 @@ def test_a_captured_pass_makes_its_own():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_one_context_in_several_threads():
+    """Threads that save the same tensors at once, each time in other versions."""
+    from concurrent.futures import ThreadPoolExecutor
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    leaves = [normal(gen, 64, 64, dtype=BF16).requires_grad_() for _ in range(3)]
+    ts = [x * 1 for x in leaves]
+    context = M8.saved_tensors(min_elements=64)
+    want = [torch.cos(_values(t.detach())) for t in ts]
+    torch.cuda.synchronize()
+
+    def run(i):
+        with context:
+            for _ in range(20):
+                ys = [torch.sin(t) for t in ts] + [torch.sin(t[8 * i:8 * i + 8]) for t in ts]
+        got = [torch.autograd.grad(y, t, torch.ones_like(y), retain_graph=True)[0] for y, t in zip(ys, ts)]
+        return all(torch.equal(a, b) for a, b in zip(got, want))
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(run, range(4)))
